@@ -17,3 +17,7 @@ from .binding import (  # noqa: F401
     taco_decompress_shards_int8_ptrs, taco_reduce_recompress_batched_ptrs, FORMAT_E4M3, FORMAT_INT8,
     workspace_bytes,
 )
+from .fp8 import (  # noqa: F401
+    Fp8Tensor, RmsNormOutput, fp8_empty, taco_fp8_quantize, taco_matmul_fp8,
+    taco_rms_norm_fp8, taco_rms_norm_fp8_backward, taco_swiglu_fp8, taco_swiglu_fp8_backward,
+)

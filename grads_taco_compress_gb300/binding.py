@@ -48,6 +48,9 @@ EXPORTED_SYMBOLS = (
     "taco_reduce_recompress", "taco_reduce_recompress_ptrs",
     "taco_decompress_shards", "taco_decompress_shards_ptrs",
     "taco_e4m3_encode_f32", "taco_e4m3_decode_f32",
+    "taco_fp8_quantize", "taco_fp8_requantize",
+    "taco_rms_norm_fp8", "taco_rms_norm_workspace_bytes", "taco_rms_norm_fp8_backward",
+    "taco_swiglu_fp8", "taco_swiglu_fp8_backward", "taco_matmul_fp8",
     "taco_get_fault", "taco_selftest_wait_timeout",
     "taco_status_string", "taco_abi_version",
 )
@@ -100,6 +103,15 @@ def _lib() -> ctypes.CDLL:
                                                   vp, vp, vp, vp, sz, vp]),
             "taco_e4m3_encode_f32": (i32, [vp, vp, i64, vp]),
             "taco_e4m3_decode_f32": (i32, [vp, vp, i64, vp]),
+            "taco_fp8_quantize": (i32, [vp, i32, i64, i64, i64, vp, vp, vp]),
+            "taco_fp8_requantize": (i32, [vp, vp, vp, vp]),
+            "taco_rms_norm_fp8": (i32, [vp, i64, vp, i64, vp, i32, i32, i64, i64, f32, vp, i64, vp, vp, vp, vp]),
+            "taco_rms_norm_workspace_bytes": (sz, [i64, i64]),
+            "taco_rms_norm_fp8_backward": (i32, [vp, i64, vp, vp, i64, vp, i32, vp, vp, i64, i32, i64, i64,
+                                                 vp, i64, vp, vp, sz, vp]),
+            "taco_swiglu_fp8": (i32, [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, vp]),
+            "taco_swiglu_fp8_backward": (i32, [vp, i64, vp, vp, i32, i64, i64, vp, i64, vp, i64, vp]),
+            "taco_matmul_fp8": (i32, [vp, vp, vp, i64, vp, i64, i32, vp]),
             "taco_get_fault": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
             "taco_selftest_wait_timeout": (i32, [ctypes.c_uint64, vp, vp]),
             "taco_status_string": (ctypes.c_char_p, [i32]),

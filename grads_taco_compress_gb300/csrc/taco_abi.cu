@@ -696,14 +696,15 @@ taco_status taco_e4m3_decode_f32(const uint8_t* in, float* out, int64_t n, void*
 
 taco_status taco_get_fault(uint32_t* bits, int clear) {
   if (!bits) return TACO_ERR_NULL;
-  unsigned int c = 0, d = 0, t = 0, m = 0, dm = 0, dp = 0;
+  unsigned int c = 0, d = 0, t = 0, m = 0, dm = 0, dp = 0, fm = 0;
   if (compress_fault(&c, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
   if (decompress_pw_fault(&dp, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
   if (compress_mma_fault(&m, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
   if (decompress_mma_fault(&dm, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
   if (decompress_fault(&d, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
   if (selftest_fault(&t, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
-  *bits = c | d | t | m | dm | dp;
+  if (matmul_fault(&fm, clear != 0) != cudaSuccess) return TACO_ERR_CUDA;
+  *bits = c | d | t | m | dm | dp | fm;
   return TACO_OK;
 }
 

@@ -37,6 +37,7 @@ constexpr unsigned kFaultDecompressWait = 2u;
 constexpr unsigned kFaultSelftestWait = 4u;
 constexpr unsigned kFaultCompressMmaWait = 8u;
 constexpr unsigned kFaultDecompressMmaWait = 16u;
+constexpr unsigned kFaultFp8MatmulWait = 32u;
 
 // ------------------------------------------------------- alpha range ----
 // alpha = sqrt(E*/E) is stored as an fp32 number and kept inside

@@ -147,4 +147,109 @@ cudaError_t launch_e4m3_decode(const uint8_t* in, float* out, int64_t n, cudaStr
 cudaError_t launch_selftest_wait(unsigned long long limit_ns, uint32_t* status, cudaStream_t st);
 cudaError_t selftest_fault(unsigned int* bits, bool clear);
 
+// ---- FP8 block tensors (fp8_*.cu) ----
+// Pointers to elements are void* of the TACO_DTYPE_* given beside the struct;
+// ld* are elements between rows, of codes and scales bytes. `vec`: every such
+// pointer is 16-byte aligned and every row of it starts on 16 bytes.
+struct NormArgs {
+  const void* x;
+  const void* residual;     // may be null (then h is not written)
+  void* h;
+  int64_t ldx, ldr, ldh;
+  const void* weight;
+  int weight_dtype;
+  float eps;
+  int64_t M, H;
+  float* rstd;              // may be null
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldc, lds;
+  uint8_t* ck_codes;        // checkpoint of h; may be null
+  uint8_t* ck_scales;
+  int64_t ck_ld, ck_lds;
+};
+struct NormBackwardArgs {
+  const void* dy;
+  const void* h;            // null: the checkpoint is read
+  const void* dh;           // may be null
+  void* dx;
+  int64_t lddy, ldh, lddh, lddx;
+  const uint8_t* ck_codes;
+  const uint8_t* ck_scales;
+  int64_t ck_ld, ck_lds;
+  const void* weight;
+  int weight_dtype;
+  const float* rstd;
+  int64_t M, H;
+  float* partial;           // [CTAs][H]
+  float* dw;
+};
+struct SwigluArgs {
+  const void* gate;
+  const void* up;
+  int64_t ldg, ldu, M, F;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ldc, lds;
+  uint8_t* g_codes;         // checkpoints; all null or none
+  uint8_t* g_scales;
+  uint8_t* u_codes;
+  uint8_t* u_scales;
+  int64_t g_ld, g_lds, u_ld, u_lds;
+};
+struct SwigluBackwardArgs {
+  const void* dy;
+  int64_t lddy, M, F;
+  const uint8_t* g_codes;
+  const uint8_t* g_scales;
+  const uint8_t* u_codes;
+  const uint8_t* u_scales;
+  int64_t g_ld, g_lds, u_ld, u_lds;
+  void* dgate;
+  void* dup;
+  int64_t lddg, lddu;
+};
+struct QuantizeArgs {
+  const void* x;
+  int64_t ldx;
+  const uint8_t* x_scales;  // not null: x holds codes
+  int64_t x_lds;
+  int x_tile;
+  int64_t M, K;
+  int tile;                 // rows per scale of the outputs, 1 or 128
+  uint8_t* codes;           // rows out; may be null
+  uint8_t* scales;
+  int64_t ldc, lds;
+  uint8_t* t_codes;         // transpose out; may be null
+  uint8_t* t_scales;
+  int64_t t_ldc, t_lds;
+};
+struct MatmulArgs {
+  const uint8_t* a;
+  const uint8_t* b;
+  int64_t lda, ldb;
+  const uint8_t* sa;
+  const uint8_t* sb;
+  int64_t lda_s, ldb_s;
+  int tile_a, tile_b;
+  int64_t M, N, K;
+  const void* add;          // may be null
+  int64_t ldadd;
+  void* out;
+  int64_t ldo;
+};
+
+cudaError_t launch_norm(const NormArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
+// Most CTAs, and so rows of partial sums, of the norm's backward pass.
+constexpr int64_t kNormMaxPartials = 512;
+int norm_backward_ctas(int64_t M, int sms);
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, bool vec, int grid, cudaStream_t st);
+cudaError_t launch_swiglu(const SwigluArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
+cudaError_t prepare_quantize();
+cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
+cudaError_t prepare_matmul();
+cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, cudaStream_t st);
+cudaError_t matmul_fault(unsigned int* bits, bool clear);
+
 }  // namespace taco

@@ -1,0 +1,282 @@
+"""FP8 block tensors and the layer operators that make and read them.
+
+Argument marshalling of the taco_*_fp8 and taco_fp8_* entry points of
+include/taco.h, which states formats, formulas and errors. A block tensor is
+E4M3 codes plus one E8M0 scale byte per row and 128 columns, or per 128 x 128
+tile for weights. As in ``binding``, torch supplies device memory and streams
+only, every output can be preallocated, and the work goes to ``stream`` or to
+the current one.
+
+A linear layer y = x W^T in training::
+
+    xq, _ = taco_fp8_quantize(x)                          # or an operator's 8-bit output
+    wq, wt = taco_fp8_quantize(w, cols=True, tile=128)    # W and its transpose
+    y = taco_matmul_fp8(xq, wq)
+    dyq, dyt = taco_fp8_quantize(dy, cols=True)
+    dx = taco_matmul_fp8(dyq, wt)
+    _, xt = taco_fp8_quantize(xq, rows=False, cols=True)  # the checkpoint, along the tokens
+    taco_matmul_fp8(dyt, xt, out=dw, add=dw)              # f32 running gradient
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from .binding import _check, _lib, _ptr, _stream_ptr
+
+BLOCK = 128
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class Fp8Tensor(NamedTuple):
+    """Codes u8 [rows, cols] and scales u8 [rows, ceil(cols / 128)], or
+    [ceil(rows / 128), ceil(cols / 128)] for one scale per 128 x 128 tile.
+    Rows of codes start at multiples of 16 bytes, rows of scales at multiples
+    of 4 (``fp8_empty`` allocates them so). The checkpoint of a gated
+    activation has a leading dimension of 2: gate, up."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def dequantize(self) -> torch.Tensor:
+        """The values as fp32 (plain torch operations, for inspection)."""
+        s = self.scales.contiguous().view(torch.float8_e8m0fnu).float()
+        if s.shape[-2] != self.codes.shape[-2]:
+            s = s.repeat_interleave(BLOCK, dim=-2)[..., : self.codes.shape[-2], :]
+        s = s.repeat_interleave(BLOCK, dim=-1)[..., : self.codes.shape[-1]]
+        return self.codes.contiguous().view(torch.float8_e4m3fn).float() * s
+
+
+class RmsNormOutput(NamedTuple):
+    y: Fp8Tensor
+    h: torch.Tensor
+    rstd: torch.Tensor
+    checkpoint: Fp8Tensor | None
+
+
+class _Fp8Struct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
+                ("ld_scales", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("tile_rows", ctypes.c_int32)]
+
+
+def _up(n: int, m: int) -> int:
+    return -(-n // m) * m
+
+
+def fp8_empty(*shape: int, tile: int = 1, device="cuda") -> Fp8Tensor:
+    """An uninitialised FP8 block tensor [..., rows, cols]."""
+    *lead, rows, cols = shape
+    kb = -(-cols // BLOCK)
+    codes = torch.empty((*lead, rows, _up(cols, 16)), dtype=torch.uint8, device=device)
+    scales = torch.empty((*lead, -(-rows // tile), _up(kb, 4)), dtype=torch.uint8, device=device)
+    return Fp8Tensor(codes[..., :cols], scales[..., :kb])
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements between rows of a 2-D tensor (its width where it has one row)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _describe(t: Fp8Tensor, what: str) -> _Fp8Struct:
+    codes, scales = t
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2 or scales.dim() != 2:
+        raise ValueError(f"{what} must be 2-D uint8 codes and scales")
+    if not (codes.is_cuda and scales.is_cuda):
+        raise ValueError(f"{what} must be CUDA tensors")
+    rows, cols = codes.shape
+    tile = 1 if scales.shape[0] == rows else BLOCK
+    if scales.shape != (-(-rows // tile), -(-cols // BLOCK)):
+        raise ValueError(f"{what}: scales {tuple(scales.shape)} do not fit codes {tuple(codes.shape)}")
+    if (cols > 1 and codes.stride(1) != 1) or (scales.shape[1] > 1 and scales.stride(1) != 1):
+        raise ValueError(f"{what} must have contiguous columns")
+    ld = codes.stride(0) if rows > 1 else _up(cols, 16)
+    lds = scales.stride(0) if scales.shape[0] > 1 else _up(scales.shape[1], 4)
+    return _Fp8Struct(codes.data_ptr(), scales.data_ptr(), ld, lds, rows, cols, tile)
+
+
+def _matrix(t: torch.Tensor, what: str, shape=None, dtype=None) -> int:
+    """Checks a plain matrix; its row stride."""
+    if not t.is_cuda or t.dtype not in DTYPES or t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D bf16, f16 or f32 CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous columns")
+    return _row_stride(t)
+
+
+def _vector(t: torch.Tensor, what: str, n: int, dtype=None) -> None:
+    if not t.is_cuda or t.dtype not in DTYPES or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor [{n}]")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def taco_fp8_quantize(x, rows: bool = True, cols: bool = False, tile: int = 1, out: Fp8Tensor | None = None,
+                      out_t: Fp8Tensor | None = None, stream=None):
+    """x [M, K] (bf16, f16, f32 or an Fp8Tensor) -> (its rows as an Fp8Tensor
+    [M, K] or None, its transpose as one [K, M] or None), from one read."""
+    if tile not in (1, BLOCK):
+        raise ValueError(f"tile must be 1 or {BLOCK}")
+    source = None
+    if isinstance(x, Fp8Tensor):
+        source = _describe(x, "x")
+        M, K, dev = source.rows, source.cols, x.codes.device
+    else:
+        ld = _matrix(x, "x")
+        (M, K), dev = x.shape, x.device
+    if rows and out is None:
+        out = fp8_empty(M, K, tile=tile, device=dev)
+    if cols and out_t is None:
+        out_t = fp8_empty(K, M, tile=tile, device=dev)
+    out, out_t = out if rows else None, out_t if cols else None
+    a = None if out is None else _describe(out, "out")
+    b = None if out_t is None else _describe(out_t, "out_t")
+    for d in (a, b):
+        if d is not None and d.rows == 1:   # the shapes of both tilings are the same
+            d.tile_rows = tile
+    if source is not None:
+        st = _lib().taco_fp8_requantize(ctypes.byref(source), _ref(a), _ref(b), _stream_ptr(stream))
+    else:
+        st = _lib().taco_fp8_quantize(_ptr(x), DTYPES[x.dtype], M, K, ld, _ref(a), _ref(b), _stream_ptr(stream))
+    _check(st, "taco_fp8_quantize")
+    return out, out_t
+
+
+def taco_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                      eps: float = 1e-6, checkpoint: bool | Fp8Tensor = False, out: Fp8Tensor | None = None,
+                      h: torch.Tensor | None = None, rstd: torch.Tensor | None = None,
+                      stream=None) -> RmsNormOutput:
+    """Root-mean-square norm of h = x + residual, [M, H], with the 8-bit output
+    y = h * rstd * weight and, with ``checkpoint`` (True or a preallocated
+    Fp8Tensor), h in 8 bits for the backward pass. Returns (y, h, rstd,
+    checkpoint); h is x itself where there is no residual. ``h`` may be x or
+    residual (in place)."""
+    ldx = _matrix(x, "x")
+    M, H = x.shape
+    if not weight.is_cuda or weight.dtype not in DTYPES or weight.shape != (H,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous CUDA tensor [{H}]")
+    ldr = ldh = 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", x.shape, x.dtype)
+        if h is None:
+            h = torch.empty((M, H), dtype=x.dtype, device=x.device)
+        ldh = _matrix(h, "h", x.shape, x.dtype)
+    elif h is not None:
+        raise ValueError("h is an output of the residual's addition: pass residual too")
+    if out is None:
+        out = fp8_empty(M, H, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    _vector(rstd, "rstd", M, torch.float32)
+    ck = fp8_empty(M, H, device=x.device) if checkpoint is True else (checkpoint or None)
+    y, c = _describe(out, "out"), None if ck is None else _describe(ck, "checkpoint")
+    st = _lib().taco_rms_norm_fp8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), DTYPES[weight.dtype],
+                                  DTYPES[x.dtype], M, H, float(eps), _ptr(h), ldh, _ptr(rstd), ctypes.byref(y),
+                                  _ref(c), _stream_ptr(stream))
+    _check(st, "taco_rms_norm_fp8")
+    return RmsNormOutput(out, x if residual is None else h, rstd, ck)
+
+
+def taco_rms_norm_fp8_backward(dy: torch.Tensor, saved, weight: torch.Tensor, rstd: torch.Tensor,
+                               dh: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                               dw: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (dx [M, H], dw f32 [H]) of taco_rms_norm_fp8 from ``saved``, its
+    8-bit checkpoint (an Fp8Tensor) or its h. ``dh`` is the gradient that h
+    received elsewhere; ``dx``, the gradient of x and of residual alike, may be
+    dy or dh (in place)."""
+    lddy = _matrix(dy, "dy")
+    M, H = dy.shape
+    _vector(weight, "weight", H)
+    _vector(rstd, "rstd", M, torch.float32)
+    c, held, ldh = None, None, 0
+    if isinstance(saved, Fp8Tensor):
+        c = _describe(saved, "checkpoint")
+    else:
+        held, ldh = saved, _matrix(saved, "h", dy.shape, dy.dtype)
+    lddh = 0 if dh is None else _matrix(dh, "dh", dy.shape, dy.dtype)
+    if dx is None:
+        dx = torch.empty((M, H), dtype=dy.dtype, device=dy.device)
+    lddx = _matrix(dx, "dx", dy.shape, dy.dtype)
+    if dw is None:
+        dw = torch.empty(H, dtype=torch.float32, device=dy.device)
+    _vector(dw, "dw", H, torch.float32)
+    if workspace is None:
+        workspace = torch.empty(_lib().taco_rms_norm_workspace_bytes(M, H), dtype=torch.uint8, device=dy.device)
+    st = _lib().taco_rms_norm_fp8_backward(
+        _ptr(dy), lddy, _ref(c), _ptr(held), ldh, _ptr(weight), DTYPES[weight.dtype], _ptr(rstd), _ptr(dh), lddh,
+        DTYPES[dy.dtype], M, H, _ptr(dx), lddx, _ptr(dw), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    _check(st, "taco_rms_norm_fp8_backward")
+    return dx, dw
+
+
+def taco_swiglu_fp8(gate_up: torch.Tensor, checkpoint: bool | Fp8Tensor = False, out: Fp8Tensor | None = None,
+                    stream=None):
+    """y = silu(gate) * up in 8 bits, from gate_up [M, 2 F] (gate in the first F
+    columns). With ``checkpoint`` (True or a preallocated Fp8Tensor [2, M, F])
+    gate and up are kept in 8 bits. Returns (y, checkpoint or None)."""
+    ld = _matrix(gate_up, "gate_up")
+    M, F2 = gate_up.shape
+    if F2 < 2 or F2 % 2:
+        raise ValueError("gate_up must have an even number of columns")
+    F = F2 // 2
+    if out is None:
+        out = fp8_empty(M, F, device=gate_up.device)
+    ck = fp8_empty(2, M, F, device=gate_up.device) if checkpoint is True else (checkpoint or None)
+    y, g, u = _describe(out, "out"), None, None
+    if ck is not None:
+        g, u = _planes(ck)
+    p = _ptr(gate_up)
+    st = _lib().taco_swiglu_fp8(p, ld, p + F * gate_up.element_size(), ld, DTYPES[gate_up.dtype], M, F,
+                                ctypes.byref(y), _ref(g), _ref(u), _stream_ptr(stream))
+    _check(st, "taco_swiglu_fp8")
+    return out, ck
+
+
+def _planes(ck: Fp8Tensor):
+    if ck.codes.dim() != 3 or ck.scales.dim() != 3 or ck.codes.shape[0] != 2 or ck.scales.shape[0] != 2:
+        raise ValueError("the checkpoint of a gated activation is [2, M, F]: gate, up")
+    return tuple(_describe(Fp8Tensor(ck.codes[i], ck.scales[i]), "checkpoint") for i in (0, 1))
+
+
+def taco_swiglu_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor, out: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Gradient [M, 2 F] of gate_up from taco_swiglu_fp8's checkpoint."""
+    lddy = _matrix(dy, "dy")
+    M, F = dy.shape
+    g, u = _planes(checkpoint)
+    if out is None:
+        out = torch.empty((M, 2 * F), dtype=dy.dtype, device=dy.device)
+    ldo = _matrix(out, "out", (M, 2 * F), dy.dtype)
+    p = _ptr(out)
+    st = _lib().taco_swiglu_fp8_backward(_ptr(dy), lddy, ctypes.byref(g), ctypes.byref(u), DTYPES[dy.dtype], M, F,
+                                         p, ldo, p + F * dy.element_size(), ldo, _stream_ptr(stream))
+    _check(st, "taco_swiglu_fp8_backward")
+    return out
+
+
+def taco_matmul_fp8(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
+                    out_dtype: torch.dtype = torch.bfloat16, add: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """a [M, K] times the transpose of b [N, K] (+ add) -> [M, N], summed in
+    fp32 on the block-scaled tensor cores. ``add`` may be ``out`` (in place)."""
+    x, w = _describe(a, "a"), _describe(b, "b")
+    M, N = x.rows, w.rows
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
+    ldo = _matrix(out, "out", (M, N))
+    ldadd = 0 if add is None else _matrix(add, "add", (M, N), out.dtype)
+    st = _lib().taco_matmul_fp8(ctypes.byref(x), ctypes.byref(w), _ptr(add), ldadd, _ptr(out), ldo,
+                                DTYPES[out.dtype], _stream_ptr(stream))
+    _check(st, "taco_matmul_fp8")
+    return out

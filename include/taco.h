@@ -344,6 +344,120 @@ taco_status taco_reduce_recompress_ptrs(const void* const* shards, int P, int64_
 taco_status taco_e4m3_encode_f32(const float* in, uint8_t* out, int64_t n, void* stream);
 taco_status taco_e4m3_decode_f32(const uint8_t* in, float* out, int64_t n, void* stream);
 
+/* ---- FP8 block tensors ------------------------------------------------------
+ * What a tensor-parallel layer computes between its compressed all-reduces,
+ * in 8 bits: the TACO pages compress the tensors that such layers exchange
+ * (pt summary, section 1) and leave the layers themselves to the training
+ * framework; these entry points are this library's own.
+ *
+ * A matrix [rows, cols] is held as E4M3 codes and E8M0 scale bytes (byte b
+ * stands for 2^(b - 127), 255 for NaN), one scale per row and 128 columns
+ * (tile_rows 1) or per 128 x 128 tile (tile_rows 128, for weights):
+ *   value[r][c] = E4M3(codes[r][c]) * 2^(scales[r / tile_rows][c / 128] - 127).
+ * Quantising a block with largest magnitude m takes the smallest power of two
+ * s >= m / 448, s >= 2^-126 (1 for an all-zero block), and rounds value / s to
+ * nearest even. A block that holds an infinity or a NaN gets the scale byte
+ * 255, so that all its values, and every sum they enter, are NaN; its codes
+ * are unspecified. Values below half a code step of a block with s = 2^-126
+ * round to zero like any others.
+ *
+ * Conventions: rows of codes start at multiples of 16 bytes (codes 16-byte
+ * aligned, ld_codes % 16 == 0), rows of scales at multiples of 4 (scales
+ * 4-byte aligned, ld_scales % 4 == 0). ld_codes >= cols, and ld_scales >=
+ * ceil(cols / 128). Bytes between the end of a row and the next row are
+ * never written; a product may read them, in the scales' rows only, and
+ * makes no use of them. rows == 0 is valid everywhere; cols >= 1.
+ *
+ * Plain matrices are bf16, f16 or f32 (dtype) with contiguous columns and ld
+ * elements between rows (ld >= cols), aligned to their element; rows that all
+ * start on 16 bytes are read and written faster. No output may overlap an
+ * input or another output except where an entry says so. Statuses:
+ * TACO_ERR_NULL, TACO_ERR_SHAPE (sizes, strides or two descriptors that
+ * disagree), TACO_ERR_BLOCK (tile_rows), TACO_ERR_ALIGN, TACO_ERR_ARG (dtype,
+ * eps), TACO_ERR_WORKSPACE, TACO_ERR_CUDA. */
+enum { TACO_DTYPE_BF16 = 0, TACO_DTYPE_F16 = 1, TACO_DTYPE_F32 = 2 };
+
+typedef struct taco_fp8_tensor {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t ld_codes;  /* bytes between rows of codes  */
+  int64_t ld_scales; /* bytes between rows of scales */
+  int64_t rows;
+  int64_t cols;
+  int32_t tile_rows; /* 1 or 128 */
+} taco_fp8_tensor;
+
+/* x [M, K] -> its FP8 blocks in `rows_out` [M, K], its transpose's in
+ * `cols_out` [K, M] (blocks of 128 of x's rows: the operand of a product that
+ * sums over them), or both from one read of x (either may be NULL, not both).
+ * The outputs' tile_rows are equal where both are given; with 128 the two
+ * hold the same codes and scales, transposed. */
+taco_status taco_fp8_quantize(const void* x, int dtype, int64_t M, int64_t K, int64_t ld,
+                              const taco_fp8_tensor* rows_out, const taco_fp8_tensor* cols_out,
+                              void* stream);
+/* The same from an FP8 block tensor: a checkpoint quantised along its columns
+ * becomes the operand of the weight gradient, which sums over its rows. */
+taco_status taco_fp8_requantize(const taco_fp8_tensor* x, const taco_fp8_tensor* rows_out,
+                                const taco_fp8_tensor* cols_out, void* stream);
+
+/* Root-mean-square norm of h = x + residual, rows of H (1 <= H <= 32768):
+ *   h    = x + residual rounded to dtype   (h = x where residual is NULL)
+ *   rstd = (mean over the row of h^2 + eps)^(-1/2)          (fp32 sums)
+ *   y    = h * rstd * weight               quantised to `y` [M, H], tile_rows 1
+ * residual, h_out: both NULL or neither; h_out may be x or residual itself
+ * (same pointer and stride). weight [H] has the type weight_dtype. rstd [M]
+ * (f32) and `checkpoint` [M, H] (h in FP8 blocks, tile_rows 1, for the
+ * backward pass) may be NULL. eps >= 0. */
+taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                              const void* weight, int weight_dtype, int dtype, int64_t M, int64_t H,
+                              float eps, void* h_out, int64_t ldh, float* rstd,
+                              const taco_fp8_tensor* y, const taco_fp8_tensor* checkpoint,
+                              void* stream);
+
+/* Its gradient, the quantisation of y taken as the identity. With xh = h *
+ * rstd, g = dy * weight, c = mean over the row of g * xh:
+ *   dx = rstd * (g - xh * c) + dh     the gradient of x and of the residual
+ *   dw = sum over the rows of dy * xh (f32 [H])
+ * h is read from `checkpoint`, or from h itself where that is not NULL
+ * (exactly one of the two). dh is the gradient that reached h_out by other
+ * ways (NULL: none). dy, h, dh and dx have the type dtype; dx may be dy, h or
+ * dh itself. The row sums of dw are formed in a fixed order. `workspace`
+ * (f32 partial sums, 16-byte aligned) need not be zeroed. M == 0 zeroes dw. */
+size_t taco_rms_norm_workspace_bytes(int64_t M, int64_t H);
+taco_status taco_rms_norm_fp8_backward(const void* dy, int64_t lddy,
+                                       const taco_fp8_tensor* checkpoint, const void* h, int64_t ldh,
+                                       const void* weight, int weight_dtype, const float* rstd,
+                                       const void* dh, int64_t lddh, int dtype, int64_t M, int64_t H,
+                                       void* dx, int64_t lddx, float* dw, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* Gated activation y = silu(gate) * up, silu(g) = g / (1 + exp(-g)), of
+ * matrices [M, F], quantised to `y` (tile_rows 1); gate and up are also
+ * quantised as they are to checkpoint_gate and checkpoint_up (tile_rows 1,
+ * both or neither NULL). */
+taco_status taco_swiglu_fp8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int dtype,
+                            int64_t M, int64_t F, const taco_fp8_tensor* y,
+                            const taco_fp8_tensor* checkpoint_gate,
+                            const taco_fp8_tensor* checkpoint_up, void* stream);
+/* Its gradient at the checkpointed gate and up, s = 1 / (1 + exp(-gate)):
+ *   dgate = dy * up * s * (1 + gate * (1 - s)),  dup = dy * gate * s.
+ * dup or dgate may be dy itself. */
+taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy,
+                                     const taco_fp8_tensor* checkpoint_gate,
+                                     const taco_fp8_tensor* checkpoint_up, int dtype, int64_t M,
+                                     int64_t F, void* dgate, int64_t lddg, void* dup, int64_t lddu,
+                                     void* stream);
+
+/* out [M, N] = a [M, K] * b [N, K]^T (+ add), on the block-scaled tensor
+ * cores: products of codes times both scales, summed in fp32, `add` (NULL:
+ * none; out's type) added in fp32, rounded once to dtype. a and b may have
+ * either tile_rows. add may be out itself (the running sum of a weight
+ * gradient). A linear layer y = x W^T takes a = x, b = W; its input gradient
+ * a = dy, b = W^T quantised; its weight gradient a = dy^T, b = x^T, both
+ * quantised along the tokens. M, N and K at most 2^31 - 256. */
+taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, const void* add,
+                            int64_t ldadd, void* out, int64_t ldo, int dtype, void* stream);
+
 /* ---- Device faults ---------------------------------------------------------
  * The kernels wait on shared-memory barriers for their bulk copies; each wait
  * gives up after one second of wall-clock time, sets a bit in a device-side
@@ -353,7 +467,8 @@ taco_status taco_e4m3_decode_f32(const uint8_t* in, float* out, int64_t n, void*
  *   TACO_FAULT_COMPRESS_MMA_WAIT (taco_compress_shards_mma: a wait on a copy,
  *   an MMA or the epilogue gave up; the CTA drains its MMAs and copies and
  *   frees its tensor memory before it returns), TACO_FAULT_DECOMPRESS_MMA_WAIT
- *   (the same for taco_decompress_reduce_mma).
+ *   (the same for taco_decompress_reduce_mma), TACO_FAULT_FP8_MATMUL_WAIT (the
+ *   same for taco_matmul_fp8).
  * taco_get_fault reads (and with clear != 0 resets) the word of the current
  * device; it synchronises with the device. */
 #define TACO_FAULT_COMPRESS_WAIT 1u
@@ -361,6 +476,7 @@ taco_status taco_e4m3_decode_f32(const uint8_t* in, float* out, int64_t n, void*
 #define TACO_FAULT_SELFTEST_WAIT 4u
 #define TACO_FAULT_COMPRESS_MMA_WAIT 8u
 #define TACO_FAULT_DECOMPRESS_MMA_WAIT 16u
+#define TACO_FAULT_FP8_MATMUL_WAIT 32u
 taco_status taco_get_fault(uint32_t* bits, int clear);
 
 /* Self-test of that time-out path: one warp waits on a barrier that nothing
