@@ -376,9 +376,9 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   TACO_TRY(check_fp8(a, a->rows, a->cols, true, &in[0], &in[1]));
   TACO_TRY(check_fp8(b, b->rows, b->cols, true, &in[2], &in[3]));
   const int64_t M = a->rows, N = b->rows;
-  bool vec = true;
-  if (add) TACO_TRY(check_matrix(add, M, N, ldadd, dtype, &in[4], &vec));
-  if (N > 0) TACO_TRY(check_matrix(out, M, N, ldo, dtype, &o, &vec));
+  bool vec_add = true, vec_out = true;
+  if (add) TACO_TRY(check_matrix(add, M, N, ldadd, dtype, &in[4], &vec_add));
+  if (N > 0) TACO_TRY(check_matrix(out, M, N, ldo, dtype, &o, &vec_out));
   TACO_TRY(check_apart(in, 5, &o, 1, &o));
   if (M == 0 || N == 0) return TACO_OK;
   if (((M + 127) / 128) * ((N + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
@@ -400,6 +400,9 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   m.ldadd = ldadd;
   m.out = out;
   m.ldo = ldo;
+  m.vec_add = vec_add;
+  // a tensor map wants a row stride of 16 bytes even where there is one row
+  m.tma_out = vec_out && (ldo * elem(dtype)) % 16 == 0;
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
   return done(launch_matmul(m, dtype, sms, static_cast<cudaStream_t>(stream)));

@@ -60,6 +60,7 @@ constexpr uint32_t mx_desc(uint32_t m, uint32_t n) {
   return ((n >> 3) << 17) | (1u << 23) | ((m >> 7) << 27);
 }
 constexpr uint32_t kDesc = mx_desc(kTileM, kTileN);
+constexpr uint32_t kDescPair256 = mx_desc(256, 256), kDescPair128 = mx_desc(256, 128);
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -80,6 +81,52 @@ __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatil
 struct MatmulMaps {
   CUtensorMap a, b;
 };
+
+// 16 bytes of outputs from fp32.
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* v) {
+  if constexpr (std::is_same<T, float>::value) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  } else if constexpr (std::is_same<T, __half>::value) {
+    __half2 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    return *reinterpret_cast<const uint4*>(h);
+  } else {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  }
+}
+template <typename T>
+__device__ __forceinline__ T load_staged(uint32_t addr) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(lds_u32(addr));
+  } else {
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(addr));
+    T v;
+    memcpy(&v, &r, 2);
+    return v;
+  }
+}
+// v += the `left` (or COLS) elements of a row of `add`; vec: 16-byte aligned.
+template <typename T, int COLS>
+__device__ __forceinline__ void add_row(float* v, const T* p, int64_t left, bool vec) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+  if (vec && left >= COLS) {
+#pragma unroll
+    for (int i = 0; i < COLS; i += kPer) {
+      alignas(16) T q[kPer];
+      *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(p + i);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[i + e] += to_f32(q[e]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < COLS; ++i)
+      if (i < left) v[i] += to_f32(p[i]);
+  }
+}
 
 // The scale word of one row for chunk q (bytes beyond the last block are
 // whatever the row's padding holds and are never used).
@@ -225,6 +272,405 @@ matmul_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a) {
   }
 }
 
+// ------------------------------------------------------------ CTA pairs ----
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `addr` in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// wait_or_abort for barriers that the other CTA of the pair arrives on.
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1u;
+      atomicOr(&g_fp8_matmul_fault, kFaultFp8MatmulWait);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n}"
+      :: "r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+}
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = umma_desc(saddr, 0, 128);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs once every tcgen05
+// operation this thread has issued so far has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+      :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+// 32 consecutive fp32 columns of this thread's lane, without the wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  tmem_ld16(taddr, v);
+  tmem_ld16(taddr + 16, v + 16);
+}
+__device__ __forceinline__ void tmem_ready32(float (&v)[32]) {
+  tmem_wait_ld();
+  reg_fence16(v);
+  reg_fence16(v + 16);
+}
+
+// Output tile t of the persistent grid: bands of 8 row tiles, all column
+// tiles of a band before the next, so that the tiles in flight at one time
+// share rows of A and of B in L2.
+constexpr int64_t kBand = 8;
+struct TileMap {
+  int64_t tiles_m, tiles_n;
+  __device__ __forceinline__ void at(int64_t t, int64_t& mt, int64_t& nt) const {
+    const int64_t per = kBand * tiles_n, band = t / per, in = t - band * per;
+    const int64_t left = tiles_m - band * kBand, size = left < kBand ? left : kBand;
+    nt = in / size;
+    mt = band * kBand + (in - nt * size);
+  }
+};
+
+template <int TN>
+struct Pair {
+  static constexpr int kStages = TN == 256 ? 6 : 8;
+  static constexpr uint32_t kA = 128 * kFp8Block, kB = TN / 2 * kFp8Block, kStage = kA + kB;
+  static constexpr uint32_t kScale = (128 + TN) * 4;       // scale words of one chunk
+  static constexpr uint32_t stages = 0;
+  static constexpr uint32_t staging = kStages * kStage;    // 4 epilogue warps x 4 KB
+  static constexpr uint32_t scales = staging + 4 * 4096;
+  static constexpr uint32_t full = scales + 2 * kScale;
+  static constexpr uint32_t empty = full + 8 * kStages;
+  static constexpr uint32_t sfull = empty + 8 * kStages;
+  static constexpr uint32_t sempty = sfull + 16;
+  static constexpr uint32_t tfull = sempty + 16;
+  static constexpr uint32_t tempty = tfull + 16;
+  static constexpr uint32_t done = tempty + 16;
+  static constexpr uint32_t slot = done + 8;
+  static constexpr uint32_t abort_flag = slot + 4;
+  static constexpr uint32_t bytes = abort_flag + 4 + 1024;
+  static_assert(bytes <= 232448, "shared memory per CTA");
+  // Tensor memory: two accumulators of TN columns and two sets of scale words
+  // (4 columns of A's, TN / 32 of B's). At TN = 256 the accumulators share 32
+  // columns (224 - 255), which the epilogue reads first.
+  static constexpr uint32_t kAcc1 = TN == 256 ? 224 : TN;
+  static constexpr uint32_t kColScales = TN == 256 ? 480 : 2 * TN;
+  static constexpr uint32_t kScaleCols = 4 + TN / 32;
+  static_assert(kColScales + 2 * kScaleCols <= 512, "tensor memory");
+};
+
+// Two CTAs, one 256 x TN output tile: CTA r holds rows 128 r .. of A, the r-th
+// half of B's TN rows and accumulator rows 128 r .. ; the even CTA issues the
+// MMAs of both. Persistent: pair p takes tiles p, p + pairs, ...; a tile's
+// epilogue overlaps the next one's MMAs. SEG: the sum over K is formed in
+// segments of kSegment stages, each started from zero in tensor memory, that
+// the epilogue adds in registers: the tensor cores cut, not round, what falls
+// below an accumulator's last bit, and a long sum drifts.
+constexpr int kSegment = 8;
+
+template <typename T, int TN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constant__ CUtensorMap out_map,
+                   MatmulArgs a) {
+  using S = Pair<TN>;
+  constexpr bool kSeg = std::is_same<T, float>::value;
+  static_assert(!kSeg || TN == 128, "the segments' sum is held in registers");
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  volatile uint32_t* abort_flag =
+      reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + S::abort_flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const TileMap tm{(a.M + 255) / 256, (a.N + TN - 1) / TN};
+  const int64_t tiles = tm.tiles_m * tm.tiles_n;
+  const int kb = static_cast<int>((a.K + kFp8Block - 1) / kFp8Block);
+  const int chunks = (kb + kChunk - 1) / kChunk;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(base + S::full + 8 * s, 1);
+      mbar_init(base + S::empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(base + S::sfull + 8 * s, 2);    // the scale warps of both CTAs
+      mbar_init(base + S::sempty + 8 * s, 1);
+      mbar_init(base + S::tfull + 8 * s, 1);
+      mbar_init(base + S::tempty + 8 * s, 8);   // 4 epilogue warps of both CTAs
+    }
+    mbar_init(base + S::done, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(base + S::slot) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the other CTA's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = lds_u32(base + S::slot);
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ---------------------------------------------------- TMA producer ----
+    if (lane == 0) {
+      prefetch_map(&maps.a);
+      prefetch_map(&maps.b);
+      uint32_t i = 0;
+      bool ok = true;
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        int64_t mt, nt;
+        tm.at(t, mt, nt);
+        const int row_a = static_cast<int>(mt * 256 + rank * 128);
+        const int row_b = static_cast<int>(nt * TN + rank * (TN / 2));
+        for (int k = 0; k < kb; ++k, ++i) {
+          const uint32_t s = i % S::kStages, ph = (i / S::kStages) & 1u;
+          if (!wait_pair(base + S::empty + 8 * s, ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          // both CTAs' copies count on the even CTA's barrier
+          const uint32_t bar = in_cta(base + S::full + 8 * s, 0);
+          if (rank == 0) mbar_arrive_expect_tx(base + S::full + 8 * s, 2 * S::kStage);
+          const uint32_t st = base + S::stages + s * S::kStage;
+          tma_load_pair(st, &maps.a, k * kFp8Block, row_a, bar);
+          tma_load_pair(st + S::kA, &maps.b, k * kFp8Block, row_b, bar);
+        }
+      }
+      if (!ok && rank == 0) {   // copies still in flight land before the CTAs exit
+        const uint32_t first = i > static_cast<uint32_t>(S::kStages) ? i - S::kStages : 0u;
+        for (uint32_t j = first; j < i; ++j) mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer ----
+    if (lane == 0 && rank == 0) {
+      uint32_t i = 0, q = 0, u = 0;   // stages, scale chunks and accumulators used so far
+      bool ok = true;
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        for (int k = 0; k < kb && ok; ++k, ++i) {
+          const int j = k % kChunk;
+          const uint32_t s = i % S::kStages, sb = q & 1u;
+          const bool first = kSeg ? k % kSegment == 0 : k == 0;
+          const bool last = k + 1 == kb || (kSeg && (k + 1) % kSegment == 0);
+          if (first) {
+            // the accumulator is free, and so are the columns it shares
+            const uint32_t before = TN == 256 ? 1u : 2u;
+            if (u >= before)
+              ok = wait_pair(base + S::tempty + 8 * ((u - before) & 1u), ((u - before) >> 1) & 1u, abort_flag);
+          }
+          if (ok && j == 0) ok = wait_pair(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
+          if (ok) ok = wait_pair(base + S::full + 8 * s, (i / S::kStages) & 1u, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sfa = tmem + S::kColScales + sb * S::kScaleCols, sfb = sfa + 4;
+          if (j == 0) {
+            const uint32_t sc = base + S::scales + sb * S::kScale;
+            tmem_copy_scales_pair(sfa, sc);
+#pragma unroll
+            for (int g = 0; g < TN / 128; ++g) tmem_copy_scales_pair(sfb + 4 * g, sc + 512 * (g + 1));
+          }
+          const uint32_t st = base + S::stages + s * S::kStage;
+          const uint32_t d = tmem + (u & 1u) * S::kAcc1;
+          const uint32_t idesc =
+              (TN == 256 ? kDescPair256 : kDescPair128) | (static_cast<uint32_t>(j) << 29) | (static_cast<uint32_t>(j) << 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_mx_pair(d, umma_desc(st + 32 * kk, kSwizzle128, 1024), umma_desc(st + S::kA + 32 * kk, kSwizzle128, 1024),
+                        idesc, sfa, sfb, !first || kk > 0);
+          commit_pair(base + S::empty + 8 * s);
+          if (j == kChunk - 1 || k + 1 == kb) {
+            commit_pair(base + S::sempty + 8 * sb);   // the scale words, in shared and in tensor memory
+            ++q;
+          }
+          if (last) {
+            commit_pair(base + S::tfull + 8 * (u & 1u));
+            ++u;
+          }
+        }
+      }
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                   :: "r"(base + S::done) : "memory");
+      mbar_wait(base + S::done, 0);   // nothing in flight when the tensor memory is freed
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- scales ----
+    // Words of the next chunk are read before the buffer they go to is free.
+    uint32_t wa[4], wb[TN / 32];
+    auto fetch = [&](int64_t t, int q) {
+      int64_t mt, nt;
+      tm.at(t, mt, nt);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        wa[r] = scale_word(a.sa, a.lda_s, mt * 256 + rank * 128 + r * 32 + lane, a.M, a.tile_a, q);
+#pragma unroll
+      for (int r = 0; r < TN / 32; ++r)
+        wb[r] = scale_word(a.sb, a.ldb_s, nt * TN + r * 32 + lane, a.N, a.tile_b, q);
+    };
+    uint32_t q = 0;
+    int64_t t = pair;
+    int k = 0;
+    if (t < tiles) fetch(t, 0);
+    while (t < tiles) {
+      const uint32_t sb = q & 1u;
+      const bool ok = wait_pair(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
+      if (!__all_sync(kFullMask, ok)) break;
+      const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(sc), "r"(wa[0]), "r"(wa[1]), "r"(wa[2]), "r"(wa[3])
+                   : "memory");
+#pragma unroll
+      for (int g = 0; g < TN / 128; ++g)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(sc + 512 * (g + 1)), "r"(wb[4 * g]),
+                     "r"(wb[4 * g + 1]), "r"(wb[4 * g + 2]), "r"(wb[4 * g + 3]) : "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(in_cta(base + S::sfull + 8 * sb, 0));
+      ++q;
+      if (++k == chunks) {
+        k = 0;
+        t += pairs;
+      }
+      if (t < tiles) fetch(t, k);
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------- epilogue ----
+    const int quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t staging = base + S::staging + quad * 4096;
+    const uint32_t tempty[2] = {in_cta(base + S::tempty, 0), in_cta(base + S::tempty + 8, 0)};
+    constexpr int kCols = 128 / static_cast<int>(sizeof(T));   // columns of one 128-byte staging row
+    if (lane == 0 && a.tma_out) prefetch_map(&out_map);
+    uint32_t u = 0;
+    bool ok = true;
+    for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      int64_t mt, nt;
+      tm.at(t, mt, nt);
+      const int64_t m0 = mt * 256 + rank * 128 + quad * 32, n0 = nt * TN;
+      float sum[kSeg ? TN : 1];
+      if constexpr (kSeg) {
+        const int segments = (kb + kSegment - 1) / kSegment;
+#pragma unroll
+        for (int c = 0; c < TN; ++c) sum[c] = 0.0f;
+        for (int g = 0; g < segments && ok; ++g, ++u) {
+          ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < TN; c += 32) {
+            float v[32];
+            tmem_ld32(tmem + lanes + (u & 1u) * S::kAcc1 + c, v);
+            tmem_ready32(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[c + i] += v[i];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(tempty[u & 1u]);
+        }
+      } else {
+        ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+        ok = __all_sync(kFullMask, ok);
+      }
+      if (!ok) break;
+      if constexpr (!kSeg) tc_fence_after();
+      const uint32_t acc = tmem + lanes + (u & 1u) * S::kAcc1;
+#pragma unroll
+      for (int c = 0; c < TN / kCols; ++c) {
+        // the shared columns first: the last ones of accumulator 0, the first of accumulator 1
+        const int chunk = (TN == 256 && (u & 1u) == 0) ? (c + TN / kCols - 1) % (TN / kCols) : c;
+        float v[kCols];
+        if constexpr (kSeg) {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) v[i] = sum[c * kCols + i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kCols; i += 16) tmem_ld16(acc + chunk * kCols + i, v + i);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < kCols; i += 16) reg_fence16(v + i);
+          if (c == (TN == 256 ? 0 : TN / kCols - 1)) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(tempty[u & 1u]);
+          }
+        }
+        const int64_t m = m0 + lane, n = n0 + static_cast<int64_t>(chunk) * kCols;
+        if (a.add && m < a.M) add_row<T, kCols>(v, static_cast<const T*>(a.add) + m * a.ldadd + n, a.N - n, a.vec_add);
+        // staging: 32 rows of 128 bytes, 16-byte pieces permuted by row & 7
+        if (lane == 0) bulk_wait_read<0>();   // the last store has read it
+        __syncwarp();
+#pragma unroll
+        for (int p = 0; p < 8; ++p) sts128(staging + lane * 128 + 16 * (p ^ (lane & 7)), pack16<T>(v + p * (kCols / 8)));
+        if (a.tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m0 < a.M && n < a.N) {
+            tma_store_2d(&out_map, staging, static_cast<int>(n), static_cast<int>(m0));
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          for (int r = 0; r < 32; ++r) {
+            if (m0 + r >= a.M) break;
+            T* p = static_cast<T*>(a.out) + (m0 + r) * a.ldo + n;
+#pragma unroll
+            for (int e = lane; e < kCols; e += 32)
+              if (n + e < a.N)
+                p[e] = load_staged<T>(staging + r * 128 + 16 * (((e * static_cast<int>(sizeof(T))) >> 4) ^ (r & 7)) +
+                                      ((e * sizeof(T)) & 15));
+          }
+          __syncwarp();
+        }
+      }
+      if constexpr (!kSeg) ++u;
+    }
+    if (lane == 0) bulk_wait_read<0>();   // every store has read the staging
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the other CTA is done with this one's barriers and shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+  }
+}
+
 bool encode_codes(EncodeTiled encode, CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t cols,
                   int64_t ld, int box_rows) {
   const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -236,22 +682,61 @@ bool encode_codes(EncodeTiled encode, CUtensorMap* map, const uint8_t* p, int64_
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [32 rows x 128 bytes] boxes of the output.
+template <typename T>
+bool encode_out(EncodeTiled encode, CUtensorMap* map, const MatmulArgs& a) {
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.M)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(a.ldo) * sizeof(T)};
+  const cuuint32_t box[2] = {128 / sizeof(T), 32};
+  const cuuint32_t unit[2] = {1, 1};
+  const CUtensorMapDataType type = std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return encode(map, type, 2, a.out, dim, stride, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 cudaError_t prepare_matmul() {
   cudaError_t e = cudaSuccess;
-  for (const void* k : {reinterpret_cast<const void*>(matmul_kernel<__nv_bfloat16>),
-                        reinterpret_cast<const void*>(matmul_kernel<__half>),
-                        reinterpret_cast<const void*>(matmul_kernel<float>)})
+  const auto set = [&](const void* k, uint32_t bytes) {
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  };
+  set(reinterpret_cast<const void*>(matmul_kernel<__nv_bfloat16>), kSmemBytes);
+  set(reinterpret_cast<const void*>(matmul_kernel<__half>), kSmemBytes);
+  set(reinterpret_cast<const void*>(matmul_kernel<float>), kSmemBytes);
+  set(reinterpret_cast<const void*>(matmul_pair_kernel<__nv_bfloat16, 256>), Pair<256>::bytes);
+  set(reinterpret_cast<const void*>(matmul_pair_kernel<__half, 256>), Pair<256>::bytes);
+  set(reinterpret_cast<const void*>(matmul_pair_kernel<float, 128>), Pair<128>::bytes);
   return e;
 }
 
+// One 256 x TN tile per CTA pair, at most one pair per two SMs.
+template <typename T, int TN>
+cudaError_t launch_pair(EncodeTiled encode, MatmulArgs a, int sms, cudaStream_t st) {
+  MatmulMaps maps;
+  if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, 128) ||
+      !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, TN / 2))
+    return cudaErrorInvalidValue;
+  CUtensorMap out = maps.a;
+  if (a.tma_out && !encode_out<T>(encode, &out, a)) return cudaErrorInvalidValue;
+  const int64_t tiles = ((a.M + 255) / 256) * ((a.N + TN - 1) / TN);
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  return launch_dependent(matmul_pair_kernel<T, TN>, dim3(static_cast<unsigned>(2 * pairs)), kThreads,
+                          Pair<TN>::bytes, st, maps, out, a);
+}
+
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, cudaStream_t st) {
-  (void)sms;
   EncodeTiled encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
+  if (a.M > 64) {
+    if (dtype == TACO_DTYPE_F32) return launch_pair<float, 128>(encode, a, sms, st);
+    return dtype == TACO_DTYPE_BF16 ? launch_pair<__nv_bfloat16, 256>(encode, a, sms, st)
+                                    : launch_pair<__half, 256>(encode, a, sms, st);
+  }
   MatmulMaps maps;
   if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, kTileM) ||
       !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, kTileN))

@@ -237,6 +237,8 @@ struct MatmulArgs {
   int64_t ldadd;
   void* out;
   int64_t ldo;
+  bool vec_add;             // add's rows all start on 16 bytes
+  bool tma_out;             // out's rows all start on 16 bytes, as tensor copies need
 };
 
 cudaError_t launch_norm(const NormArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
