@@ -42,14 +42,18 @@ bool overlap(const Region& a, const Region& b) {
   return true;
 }
 
-// Checks a plain matrix; 16-byte rows or not in *vec.
-taco_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int dtype, Region* r, bool* vec) {
+// Checks a plain matrix; lowers *vec to what the alignment of its rows allows.
+taco_status check_matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int dtype, Region* r, int* vec) {
   const int64_t es = elem(dtype);
   if (ld < cols || (rows > 0 && ld > kMaxElements / rows)) return TACO_ERR_SHAPE;
   if (rows > 0 && !p) return TACO_ERR_NULL;
   if (addr(p) % es) return TACO_ERR_ALIGN;
   *r = Region{addr(p), rows, cols * es, ld * es};
-  if (vec) *vec = *vec && addr(p) % 16 == 0 && (rows <= 1 || (ld * es) % 16 == 0);
+  if (vec) {
+    const uintptr_t low = addr(p) | (rows > 1 ? static_cast<uintptr_t>(ld * es) : 0);
+    const int level = low % 32 == 0 ? kVec32 : low % 16 == 0 ? kVec16 : kVecNone;
+    if (level < *vec) *vec = level;
+  }
   return TACO_OK;
 }
 
@@ -93,7 +97,6 @@ cudaError_t device_sms(int* sms) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(g_once[dev], [dev]() {
     cudaError_t err = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
-    if (err == cudaSuccess) err = prepare_quantize();
     if (err == cudaSuccess) err = prepare_matmul();
     g_err[dev] = err;
   });
@@ -109,7 +112,7 @@ inline taco_status done(cudaError_t e) { return e == cudaSuccess ? TACO_OK : TAC
     if (st_ != TACO_OK) return st_;           \
   } while (0)
 
-taco_status quantize_common(QuantizeArgs& a, int dtype, bool vec, const Region* in, int nin,
+taco_status quantize_common(QuantizeArgs& a, int dtype, int vec, const Region* in, int nin,
                             const taco_fp8_tensor* rows_out, const taco_fp8_tensor* cols_out, void* stream) {
   if (!rows_out && !cols_out) return TACO_ERR_NULL;
   Region out[4];
@@ -136,7 +139,7 @@ taco_status quantize_common(QuantizeArgs& a, int dtype, bool vec, const Region* 
   if (a.M == 0) return TACO_OK;
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_quantize(a, dtype, vec, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_quantize(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -153,7 +156,7 @@ taco_status taco_fp8_quantize(const void* x, int dtype, int64_t M, int64_t K, in
   if (M < 0 || K < 1 || M > kMaxSide || K > kMaxSide) return TACO_ERR_SHAPE;
   QuantizeArgs a{};
   Region in;
-  bool vec = true;
+  int vec = kVec32;
   TACO_TRY(check_matrix(x, M, K, ld, dtype, &in, &vec));
   a.x = x;
   a.ldx = ld;
@@ -175,7 +178,7 @@ taco_status taco_fp8_requantize(const taco_fp8_tensor* x, const taco_fp8_tensor*
   a.x_tile = x->tile_rows;
   a.M = x->rows;
   a.K = x->cols;
-  return quantize_common(a, TACO_DTYPE_BF16, true, in, 2, rows_out, cols_out, stream);
+  return quantize_common(a, TACO_DTYPE_BF16, kVec32, in, 2, rows_out, cols_out, stream);
 }
 
 taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
@@ -187,7 +190,7 @@ taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
   if (M < 0 || M > kMaxSide || H < 1 || H > kMaxNormColumns) return TACO_ERR_SHAPE;
   if (!y || !weight || (residual != nullptr) != (h_out != nullptr)) return TACO_ERR_NULL;
   Region in[3], out[6];
-  bool vec = true;
+  int vec = kVec32;
   TACO_TRY(check_matrix(x, M, H, ldx, dtype, &in[0], &vec));
   TACO_TRY(check_matrix(weight, 1, H, H, weight_dtype, &in[1], &vec));
   if (residual) {
@@ -243,7 +246,7 @@ taco_status taco_rms_norm_fp8_backward(const void* dy, int64_t lddy, const taco_
   if ((checkpoint != nullptr) == (h != nullptr)) return TACO_ERR_NULL;
   if (!weight || !dw || (M > 0 && !rstd)) return TACO_ERR_NULL;
   Region in[7], out[3];
-  bool vec = true;
+  int vec = kVec32;
   TACO_TRY(check_matrix(dy, M, H, lddy, dtype, &in[0], &vec));
   if (checkpoint) TACO_TRY(check_fp8(checkpoint, M, H, false, &in[1], &in[2]));
   if (h) TACO_TRY(check_matrix(h, M, H, ldh, dtype, &in[3], &vec));
@@ -291,7 +294,7 @@ taco_status taco_swiglu_fp8(const void* gate, int64_t ldg, const void* up, int64
   if (M < 0 || F < 1 || M > kMaxSide || F > kMaxSide) return TACO_ERR_SHAPE;
   if (!y || (checkpoint_gate != nullptr) != (checkpoint_up != nullptr)) return TACO_ERR_NULL;
   Region in[2], out[6];
-  bool vec = true;
+  int vec = kVec32;
   TACO_TRY(check_matrix(gate, M, F, ldg, dtype, &in[0], &vec));
   TACO_TRY(check_matrix(up, M, F, ldu, dtype, &in[1], &vec));
   TACO_TRY(check_fp8(y, M, F, false, &out[0], &out[1]));
@@ -322,9 +325,7 @@ taco_status taco_swiglu_fp8(const void* gate, int64_t ldg, const void* up, int64
     a.u_ld = checkpoint_up->ld_codes;
     a.u_lds = checkpoint_up->ld_scales;
   }
-  int sms = 0;
-  if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_swiglu(a, dtype, vec, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_swiglu(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
 taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy, const taco_fp8_tensor* checkpoint_gate,
@@ -334,7 +335,7 @@ taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy, const taco_fp
   if (M < 0 || F < 1 || M > kMaxSide || F > kMaxSide) return TACO_ERR_SHAPE;
   if (!checkpoint_gate || !checkpoint_up) return TACO_ERR_NULL;
   Region in[5], out[2];
-  bool vec = true;
+  int vec = kVec32;
   TACO_TRY(check_matrix(dy, M, F, lddy, dtype, &in[0], &vec));
   TACO_TRY(check_fp8(checkpoint_gate, M, F, false, &in[1], &in[2]));
   TACO_TRY(check_fp8(checkpoint_up, M, F, false, &in[3], &in[4]));
@@ -362,9 +363,7 @@ taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy, const taco_fp
   a.dup = dup;
   a.lddg = lddg;
   a.lddu = lddu;
-  int sms = 0;
-  if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_swiglu_backward(a, dtype, vec, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_swiglu_backward(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
 taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, const void* add, int64_t ldadd,
@@ -376,7 +375,7 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   TACO_TRY(check_fp8(a, a->rows, a->cols, true, &in[0], &in[1]));
   TACO_TRY(check_fp8(b, b->rows, b->cols, true, &in[2], &in[3]));
   const int64_t M = a->rows, N = b->rows;
-  bool vec_add = true, vec_out = true;
+  int vec_add = kVec32, vec_out = kVec32;
   if (add) TACO_TRY(check_matrix(add, M, N, ldadd, dtype, &in[4], &vec_add));
   if (N > 0) TACO_TRY(check_matrix(out, M, N, ldo, dtype, &o, &vec_out));
   TACO_TRY(check_apart(in, 5, &o, 1, &o));
@@ -400,9 +399,9 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   m.ldadd = ldadd;
   m.out = out;
   m.ldo = ldo;
-  m.vec_add = vec_add;
+  m.vec_add = vec_add != kVecNone;
   // a tensor map wants a row stride of 16 bytes even where there is one row
-  m.tma_out = vec_out && (ldo * elem(dtype)) % 16 == 0;
+  m.tma_out = vec_out != kVecNone && (ldo * elem(dtype)) % 16 == 0;
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
   return done(launch_matmul(m, dtype, sms, static_cast<cudaStream_t>(stream)));

@@ -10,6 +10,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "taco_device.cuh"
 #include "taco_launch.h"
@@ -44,37 +45,56 @@ __device__ __forceinline__ float fp8_scale(uint32_t b) {
   return __uint_as_float(b == 0u ? 0x400000u : b << 23);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// Largest magnitude (as bits) of 8 values.
-__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
-  uint32_t m = 0;
+// max(|a|, |b|, |c|), NaN if any of them is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Largest magnitude of N values (N even), NaN if any is.
+template <int N>
+__device__ __forceinline__ float amax_of(const float (&v)[N]) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+  for (int i = 0; i < N; i += 2) m = amax3(m, v[i], v[i + 1]);
   return m;
 }
-// Largest over the LANES consecutive lanes of an aligned group.
+// Largest over the LANES consecutive lanes of an aligned group, as bits.
 template <int LANES>
-__device__ __forceinline__ uint32_t group_umax(uint32_t v) {
+__device__ __forceinline__ uint32_t group_umax(float v) {
+  uint32_t b = __float_as_uint(v);
 #pragma unroll
-  for (int m = 1; m < LANES; m <<= 1) v = max(v, __shfl_xor_sync(kFullMask, v, m));
-  return v;
+  for (int m = 1; m < LANES; m <<= 1) b = max(b, __shfl_xor_sync(kFullMask, b, m));
+  return b;
 }
 
-// Eight codes of v * inv, element 0 in the low byte.
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
-  return make_uint2(e4m3x4_from_f32(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                    e4m3x4_from_f32(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-}
-// Eight codes -> fp32 values times s (a power of two: exact).
-__device__ __forceinline__ void decode8(uint2 c, float s, float (&v)[8]) {
+// Lanes that share a block of 128 columns, 16 columns each.
+constexpr int kBlockLanes = 8;
+
+// Sixteen codes of v * inv, element 0 in the low byte.
+__device__ __forceinline__ uint4 codes16(const float (&v)[16], float inv) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? c.x : c.y;
-    const f2 p = e4m3x2_to_f2((i & 1) ? w >> 16 : w);
-    v[2 * i] = p.x * s;
-    v[2 * i + 1] = p.y * s;
+    const f2 s{inv, inv};
+    const f2 a = mul2(f2{v[4 * i], v[4 * i + 1]}, s), b = mul2(f2{v[4 * i + 2], v[4 * i + 3]}, s);
+    w[i] = e4m3x4_from_f32(a.x, a.y, b.x, b.y);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Four codes -> fp32 values times s (a power of two: exact).
+__device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
+  const f2 ss{s, s}, a = mul2(e4m3x2_to_f2(w & 0xffffu), ss), b = mul2(e4m3x2_to_f2(w >> 16), ss);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
+__device__ __forceinline__ void decode16(uint4 c, float s, float (&v)[16]) {
+  decode4(c.x, s, v);
+  decode4(c.y, s, v + 4);
+  decode4(c.z, s, v + 8);
+  decode4(c.w, s, v + 12);
 }
 
 // ------------------------------------------------------- element types ----
@@ -86,78 +106,174 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return 
 template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
-// The elements of 8 consecutive columns; n (0 .. 8) of them exist, the others
-// read as 0. VEC: p is 16-byte aligned.
+// Sixteen consecutive elements of a row, as they lie in memory.
 template <typename T>
-struct alignas(16) Pack8 {
-  T v[8];
+struct Row16 {
+  uint32_t w[4 * sizeof(T)];
 };
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
-  if (VEC && n == 8) {
-    Pack8<T> q;
-    const uint4* s = reinterpret_cast<const uint4*>(p);
-    uint4* d = reinterpret_cast<uint4*>(&q);
+template <typename T>
+__device__ __forceinline__ void unpack(const Row16<T>& r, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(q) / 16); ++i) d[i] = s[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(q.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (std::is_same<T, float>::value) {
+      v[2 * i] = __uint_as_float(r.w[2 * i]);
+      v[2 * i + 1] = __uint_as_float(r.w[2 * i + 1]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = bf16_lo(r.w[i]);
+      v[2 * i + 1] = bf16_hi(r.w[i]);
+    }
   }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
-  if (VEC && n == 8) {
-    Pack8<T> q;
+template <typename T>
+__device__ __forceinline__ Row16<T> pack(const float (&v)[16]) {
+  Row16<T> r;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q.v[i] = from_f32<T>(v[i]);
-    const uint4* s = reinterpret_cast<const uint4*>(&q);
-    uint4* d = reinterpret_cast<uint4*>(p);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(q) / 16); ++i) d[i] = s[i];
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (std::is_same<T, float>::value) {
+      r.w[2 * i] = __float_as_uint(v[2 * i]);
+      r.w[2 * i + 1] = __float_as_uint(v[2 * i + 1]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      r.w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  return r;
+}
+// Eight 32-bit words to and from global memory: one 32-byte access where p
+// allows it (wide), else two of 16 bytes. Streamed data is kept out of L1.
+__device__ __forceinline__ void load_words8(const void* p, bool wide, uint32_t* w) {
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "l"(static_cast<const char*>(p) + 16 * i));
+  }
+}
+__device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t* w) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                 :: "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(static_cast<char*>(p) + 16 * i) =
+          make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+}
+// The elements of 16 consecutive columns, of which n (0 .. 16) exist; the
+// others read as zero. VEC: p is 16-byte aligned, and 32-byte aligned if wide.
+template <typename T, bool VEC>
+__device__ __forceinline__ Row16<T> load16(const T* p, int n, bool wide) {
+  Row16<T> r;
+  if (VEC && n == 16) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) load_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
+  } else {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+    r = pack<T>(v);
+  }
+  return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store16(T* p, int n, bool wide, const Row16<T>& r) {
+  if (VEC && n == 16) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) store_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
+  } else {
+    float v[16];
+    unpack<T>(r, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
       if (i < n) p[i] = from_f32<T>(v[i]);
   }
 }
-// Codes of 8 consecutive columns: rows of codes start at multiples of 16
-// bytes, so a full group is 8-byte aligned; a partial one is written byte by
-// byte and leaves what lies behind the row alone.
-__device__ __forceinline__ void store_codes8(uint8_t* p, int n, uint2 c) {
-  if (n == 8) {
-    *reinterpret_cast<uint2*>(p) = c;
+// Codes of 16 consecutive columns: rows of codes start at multiples of 16
+// bytes, so a full group is one access; a partial one goes byte by byte and
+// leaves what lies behind the row alone.
+__device__ __forceinline__ void store_codes16(uint8_t* p, int n, uint4 c) {
+  if (n == 16) {
+    *reinterpret_cast<uint4*>(p) = c;
   } else {
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
   }
 }
-__device__ __forceinline__ uint2 load_codes8(const uint8_t* p, int n) {
-  if (n == 8) return *reinterpret_cast<const uint2*>(p);
-  uint2 c = make_uint2(0, 0);
+__device__ __forceinline__ uint4 load_codes16(const uint8_t* p, int n) {
+  if (n == 16) {
+    uint4 c;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w) : "l"(p));
+    return c;
+  }
+  uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) (i < 4 ? c.x : c.y) |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-  return c;
+  for (int i = 0; i < 16; ++i)
+    if (i < n) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 8 consecutive entries of a weight vector of any element type.
+// 16 consecutive entries of a vector of any element type, kept in L1.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_vector16(const T* p, int n, float (&v)[16]) {
+  if (VEC && n == 16) {
+    Row16<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+      *reinterpret_cast<uint4*>(r.w + 4 * i) = *reinterpret_cast<const uint4*>(p + 4 * i * (4 / sizeof(T)));
+    unpack<T>(r, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+  }
+}
 template <bool VEC>
-__device__ __forceinline__ void load_weight8(const void* w, int dtype, int64_t col, int n, float (&v)[8]) {
+__device__ __forceinline__ void load_weight16(const void* w, int dtype, int64_t col, int n, float (&v)[16]) {
   if (dtype == TACO_DTYPE_F32)
-    load8<float, VEC>(static_cast<const float*>(w) + col, n, v);
+    load_vector16<float, VEC>(static_cast<const float*>(w) + col, n, v);
   else if (dtype == TACO_DTYPE_BF16)
-    load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w) + col, n, v);
+    load_vector16<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w) + col, n, v);
   else
-    load8<__half, VEC>(static_cast<const __half*>(w) + col, n, v);
+    load_vector16<__half, VEC>(static_cast<const __half*>(w) + col, n, v);
 }
 
-__device__ __forceinline__ int clamp8(int64_t left) {
-  return left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left));
+__device__ __forceinline__ int clamp16(int64_t left) {
+  return left < 0 ? 0 : (left > 16 ? 16 : static_cast<int>(left));
 }
+
+// Quantises 16 columns of a block whose 8 lanes all call this (n of the
+// columns exist, the others hold zeros) and writes codes and scale byte.
+__device__ __forceinline__ void quantize16(const float (&v)[16], int n, uint8_t* codes, uint8_t* scale, int lane8) {
+  const uint32_t b = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(v)));
+  if (n > 0) {
+    store_codes16(codes, n, codes16(v, fp8_inverse_scale(b)));
+    if (lane8 == 0) *scale = static_cast<uint8_t>(b);
+  }
+}
+
+// Quotient by a divisor fixed per launch: floor(n / d) = high half of
+// n * (floor(2^64 / d) + 1) for n d < 2^64.
+struct Divider {
+  uint64_t magic;
+  uint64_t d;
+  explicit Divider(uint64_t d_ = 1) : magic(d_ == 1 ? 0 : ~uint64_t{0} / d_ + 1), d(d_) {}
+  __device__ __forceinline__ uint64_t quotient(uint64_t n) const { return d == 1 ? n : __umul64hi(n, magic); }
+};
 
 // Sum over a CTA of WARPS warps (WARPS a runtime count <= 32); `red` holds one
 // float per warp. Every thread gets the same sum, added in the same order.

@@ -10,8 +10,8 @@
 //             g = dy w,  c = mean(g xh)
 //             dx = rstd (g - xh c) + dh,   dw = sum over rows of dy xh
 //
-// One CTA takes a row at a time; thread t holds the 8-column chunks t, t + T,
-// ... in registers, so a row is read once and a block of 128 columns is 16
+// A CTA takes a row at a time; thread t holds the 16-column chunks t, t + T,
+// ... in registers, so a row is read once and a block of 128 columns is 8
 // consecutive lanes. Sums are fp32.
 
 #include "fp8_block.cuh"
@@ -21,97 +21,126 @@ namespace taco {
 namespace {
 
 template <typename T, int NC, bool VEC>
-__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
-  __shared__ float red[32];
-  const int warps = blockDim.x >> 5;
-  const T* x = static_cast<const T*>(a.x);
-  const T* res = static_cast<const T*>(a.residual);
-  T* hout = static_cast<T*>(a.h);
+__global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
+  __shared__ float red[16];
+  const int warps = blockDim.x >> 5, lane8 = threadIdx.x & 7;
   grid_launch_dependents();
   grid_dependency_wait();
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    float v[NC][8];
-    float sum = 0.0f;
+  const int64_t row = blockIdx.x;
+  Row16<T> h[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+    h[c] = load16<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + col, clamp16(a.H - col), wide);
+  }
+  if (a.residual) {
+    Row16<T> r[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 8 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
-      const int n = clamp8(a.H - col);
-      load8<T, VEC>(x + row * a.ldx + col, n, v[c]);
-      if (res) {
-        float r[8];
-        load8<T, VEC>(res + row * a.ldr + col, n, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = to_f32(from_f32<T>(v[c][i] + r[i]));
-        store8<T, VEC>(hout + row * a.ldh + col, n, v[c]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(v[c][i], v[c][i], sum);
+      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      r[c] = load16<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr + col, clamp16(a.H - col), wide);
     }
-    sum = cta_sum(sum, red, warps);
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 8 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
-      const int n = clamp8(a.H - col);
-      if (a.ck_codes) {
-        const uint32_t b = fp8_scale_byte(group_umax<16>(amax8(v[c])));
-        if (n > 0) {
-          store_codes8(a.ck_codes + row * a.ck_ld + col, n, codes8(v[c], fp8_inverse_scale(b)));
-          if ((threadIdx.x & 15) == 0)
-            a.ck_scales[row * a.ck_lds + col / kFp8Block] = static_cast<uint8_t>(b);
-        }
-      }
-      float w[8], y[8];
-      load_weight8<VEC>(a.weight, a.weight_dtype, col, n, w);
+      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      float x[16], y[16];
+      unpack<T>(h[c], x);
+      unpack<T>(r[c], y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = v[c][i] * rstd * w[i];
-      const uint32_t b = fp8_scale_byte(group_umax<16>(amax8(y)));
-      if (n > 0) {
-        store_codes8(a.codes + row * a.ldc + col, n, codes8(y, fp8_inverse_scale(b)));
-        if ((threadIdx.x & 15) == 0) a.scales[row * a.lds + col / kFp8Block] = static_cast<uint8_t>(b);
-      }
+      for (int i = 0; i < 16; ++i) x[i] += y[i];
+      h[c] = pack<T>(x);
+      store16<T, VEC>(static_cast<T*>(a.h) + row * a.ldh + col, clamp16(a.H - col), wide, h[c]);
     }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float v[16];
+    unpack<T>(h[c], v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
+  }
+  sum = cta_sum(sum, red, warps);
+  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.eps);
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+    const int n = clamp16(a.H - col);
+    float v[16], w[16];
+    unpack<T>(h[c], v);
+    if (a.ck_codes)
+      quantize16(v, n, a.ck_codes + row * a.ck_ld + col, a.ck_scales + row * a.ck_lds + col / kFp8Block, lane8);
+    load_weight16<VEC>(a.weight, a.weight_dtype, col, n, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] *= v[i] * rstd;
+    quantize16(w, n, a.codes + row * a.ldc + col, a.scales + row * a.lds + col / kFp8Block, lane8);
   }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the backward pass; the
-// CTA's column sums of dy xh go to its row of `partial`.
-template <typename T, int NC, bool VEC>
-__global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs a) {
-  __shared__ float red[32];
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the backward pass, the next
+// row's loads in flight while one is worked on; the CTA's column sums of
+// dy xh go to its row of `partial`.
+template <typename T, bool H>
+struct BackwardRow {
+  Row16<T> dy, dh;
+  Row16<T> h;      // H
+  uint4 codes;     // !H
+  uint32_t scale;
+};
+
+template <typename T, int NC, bool VEC, bool H>
+__global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs a, bool wide) {
+  __shared__ float red[16];
   const int warps = blockDim.x >> 5;
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* h = static_cast<const T*>(a.h);
-  const T* dh = static_cast<const T*>(a.dh);
-  T* dx = static_cast<T*>(a.dx);
-  float dw[NC][8];
+  float dw[NC][16];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = 0.0f;
+    for (int i = 0; i < 16; ++i) dw[c][i] = 0.0f;
   grid_launch_dependents();
   grid_dependency_wait();
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    float g[NC][8], xh[NC][8];
-    float sum = 0.0f;
-    const float rstd = a.rstd[row];
+  BackwardRow<T, H> next[NC];
+  float next_rstd = 0.0f;
+  const auto fetch = [&](int64_t row) {
+    next_rstd = a.rstd[row];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 8 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
-      const int n = clamp8(a.H - col);
-      load8<T, VEC>(dy + row * a.lddy + col, n, g[c]);
-      if (h) {
-        load8<T, VEC>(h + row * a.ldh + col, n, xh[c]);
-      } else if (n > 0) {
-        const uint32_t b = a.ck_scales[row * a.ck_lds + col / kFp8Block];
-        decode8(load_codes8(a.ck_codes + row * a.ck_ld + col, n), fp8_scale(b), xh[c]);
+      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      const int n = clamp16(a.H - col);
+      next[c].dy = load16<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy + col, n, wide);
+      if (H) {
+        next[c].h = load16<T, VEC>(static_cast<const T*>(a.h) + row * a.ldh + col, n, wide);
+      } else {
+        next[c].codes = load_codes16(a.ck_codes + row * a.ck_ld + col, n);
+        next[c].scale = n > 0 ? a.ck_scales[row * a.ck_lds + col / kFp8Block] : kScaleOne;
       }
-      float w[8];
-      load_weight8<VEC>(a.weight, a.weight_dtype, col, n, w);
+      if (a.dh) next[c].dh = load16<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh + col, n, wide);
+    }
+  };
+  if (blockIdx.x < a.M) fetch(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+    BackwardRow<T, H> cur[NC];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xh[c][i] = n > 0 ? xh[c][i] * rstd : 0.0f;
+    for (int c = 0; c < NC; ++c) cur[c] = next[c];
+    const float rstd = next_rstd;
+    if (row + gridDim.x < a.M) fetch(row + gridDim.x);
+    float g[NC][16], xh[NC][16];
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      const int n = clamp16(a.H - col);
+      unpack<T>(cur[c].dy, g[c]);
+      if (H)
+        unpack<T>(cur[c].h, xh[c]);
+      else
+        decode16(cur[c].codes, fp8_scale(cur[c].scale), xh[c]);
+      float w[16];
+      load_weight16<VEC>(a.weight, a.weight_dtype, col, n, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        xh[c][i] = n == 16 || i < n ? xh[c][i] * rstd : 0.0f;
         dw[c][i] = fmaf(g[c][i], xh[c][i], dw[c][i]);
         g[c][i] *= w[i];
         sum = fmaf(g[c][i], xh[c][i], sum);
@@ -120,87 +149,83 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs a) 
     const float mean = cta_sum(sum, red, warps) / static_cast<float>(a.H);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 8 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
-      const int n = clamp8(a.H - col);
-      float r[8];
+      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = rstd * fmaf(-xh[c][i], mean, g[c][i]);
-      if (dh) {
-        float d[8];
-        load8<T, VEC>(dh + row * a.lddh + col, n, d);
+      for (int i = 0; i < 16; ++i) g[c][i] = rstd * fmaf(-xh[c][i], mean, g[c][i]);
+      if (a.dh) {
+        float d[16];
+        unpack<T>(cur[c].dh, d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] += d[i];
+        for (int i = 0; i < 16; ++i) g[c][i] += d[i];
       }
-      store8<T, VEC>(dx + row * a.lddx + col, n, r);
+      store16<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx + col, clamp16(a.H - col), wide, pack<T>(g[c]));
     }
   }
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t col = 8 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
-    const int n = clamp8(a.H - col);
+    const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+    const int n = clamp16(a.H - col);
     float* p = a.partial + blockIdx.x * a.H + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (i < n) p[i] = dw[c][i];
   }
 }
 
-// dw = the sum of the G rows of partial sums, in order.
-__global__ void norm_dw_kernel(const float* partial, int G, int64_t H, float* dw) {
+// dw = the sum of the G rows of partial sums, in a fixed order: a CTA takes 32
+// columns, warp w adds rows w, w + 8, ..., and the 8 sums meet in order.
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int G, int64_t H, float* dw) {
+  __shared__ float part[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (col >= H) return;
   float s = 0.0f;
-  for (int g = 0; g < G; ++g) s += partial[g * H + col];
-  dw[col] = s;
+  if (col < H) {
+#pragma unroll 8
+    for (int g = warp; g < G; g += 8) s += partial[g * H + col];
+  }
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && col < H) {
+    s = part[0][lane];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    dw[col] = s;
+  }
 }
 
-// Threads and chunks per thread for H columns.
+// Threads and 16-column chunks per thread for H columns: at most 512 threads.
 void norm_shape(int64_t H, int* threads, int* nc) {
-  const int64_t chunks = (H + 7) / 8;
-  *nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+  const int64_t chunks = (H + 15) / 16;
+  *nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
   const int64_t t = (chunks + *nc - 1) / *nc;
   *threads = static_cast<int>((t + 31) / 32 * 32);
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_norm_t(const NormArgs& a, int sms, cudaStream_t st) {
-  (void)sms;
-  int threads, nc;
-  norm_shape(a.H, &threads, &nc);
-  const int64_t most = 1 << 30;
-  const dim3 grid(static_cast<unsigned>(a.M < most ? a.M : most));
-  switch (nc) {
-    case 1: return launch_dependent(norm_kernel<T, 1, VEC>, grid, threads, 0, st, a);
-    case 2: return launch_dependent(norm_kernel<T, 2, VEC>, grid, threads, 0, st, a);
-    case 4: return launch_dependent(norm_kernel<T, 4, VEC>, grid, threads, 0, st, a);
-    default: return launch_dependent(norm_kernel<T, 8, VEC>, grid, threads, 0, st, a);
-  }
+template <typename T, int NC>
+cudaError_t launch_norm_t(const NormArgs& a, int threads, int vec, cudaStream_t st) {
+  return launch_dependent(vec ? norm_kernel<T, NC, true> : norm_kernel<T, NC, false>,
+                          dim3(static_cast<unsigned>(a.M)), threads, 0, st, a, vec == kVec32);
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int grid, cudaStream_t st) {
-  int threads, nc;
-  norm_shape(a.H, &threads, &nc);
-  cudaError_t e = cudaSuccess;
-  if (grid > 0) switch (nc) {
-    case 1: e = launch_dependent(norm_backward_kernel<T, 1, VEC>, dim3(grid), threads, 0, st, a); break;
-    case 2: e = launch_dependent(norm_backward_kernel<T, 2, VEC>, dim3(grid), threads, 0, st, a); break;
-    case 4: e = launch_dependent(norm_backward_kernel<T, 4, VEC>, dim3(grid), threads, 0, st, a); break;
-    default: e = launch_dependent(norm_backward_kernel<T, 8, VEC>, dim3(grid), threads, 0, st, a); break;
-  }
-  if (e != cudaSuccess) return e;
-  return launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((a.H + 127) / 128)), 128, 0, st,
-                          static_cast<const float*>(a.partial), grid, a.H, a.dw);
+template <typename T, int NC, bool H>
+cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, int vec, int grid, cudaStream_t st) {
+  return launch_dependent(vec ? norm_backward_kernel<T, NC, true, H> : norm_backward_kernel<T, NC, false, H>,
+                          dim3(grid), threads, 0, st, a, vec == kVec32);
 }
 
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {
+cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st) {
+  (void)sms;
+  int threads, nc;
+  norm_shape(a.H, &threads, &nc);
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? launch_norm_t<T, true>(a, sms, st) : launch_norm_t<T, false>(a, sms, st);
+    return nc == 1   ? launch_norm_t<T, 1>(a, threads, vec, st)
+           : nc == 2 ? launch_norm_t<T, 2>(a, threads, vec, st)
+                     : launch_norm_t<T, 4>(a, threads, vec, st);
   });
 }
 
@@ -210,13 +235,24 @@ int norm_backward_ctas(int64_t M, int sms) {
   return static_cast<int>(M < most ? M : most);
 }
 
-cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, bool vec, int grid,
-                                 cudaStream_t st) {
-  return with_dtype(dtype, [&](auto t) {
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, int grid, cudaStream_t st) {
+  int threads, nc;
+  norm_shape(a.H, &threads, &nc);
+  const auto launch = [&](auto t, auto held) {
     using T = decltype(t);
-    return vec ? launch_norm_backward_t<T, true>(a, grid, st)
-               : launch_norm_backward_t<T, false>(a, grid, st);
-  });
+    constexpr bool H = decltype(held)::value;
+    return nc == 1   ? launch_norm_backward_t<T, 1, H>(a, threads, vec, grid, st)
+           : nc == 2 ? launch_norm_backward_t<T, 2, H>(a, threads, vec, grid, st)
+                     : launch_norm_backward_t<T, 4, H>(a, threads, vec, grid, st);
+  };
+  if (grid > 0) {
+    const cudaError_t e = with_dtype(dtype, [&](auto t) {
+      return a.h ? launch(t, std::true_type{}) : launch(t, std::false_type{});
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32)), 256, 0, st,
+                          static_cast<const float*>(a.partial), grid, a.H, a.dw);
 }
 
 }  // namespace taco

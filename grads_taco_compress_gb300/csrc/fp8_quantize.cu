@@ -4,8 +4,12 @@
 // block or per 128 x 128 tile. The source is bf16, f16, f32 or itself an FP8
 // block tensor.
 //
-// Rows alone: 16 lanes take one row's block, 8 columns each. With the
-// transpose: one CTA takes a 128 x 128 tile through shared memory.
+// Rows alone: a warp takes 512 columns of one row, 8 lanes a block of 128.
+// With the transpose (or tiles): one CTA takes a 128 x 128 tile, each thread 4
+// consecutive rows of 16 columns, which stay in registers. The largest
+// magnitudes of the columns meet in shared memory; the transposed codes go
+// through it too, 4 rows of a column to a word, so that they leave as whole
+// 128-byte rows.
 
 #include "fp8_block.cuh"
 
@@ -17,145 +21,147 @@ constexpr int kThreads = 256;
 
 struct Fp8Source {};   // the source is codes and scales
 
+// 16 columns of a row as fp32 (of which n exist).
 template <typename T, bool VEC>
-__device__ __forceinline__ void read8(const QuantizeArgs& a, int64_t row, int64_t col, int n, float (&v)[8]) {
+__device__ __forceinline__ void read16(const QuantizeArgs& a, int64_t row, int64_t col, int n, bool wide,
+                                       float (&v)[16]) {
   if constexpr (std::is_same<T, Fp8Source>::value) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (n > 0)
-      decode8(load_codes8(static_cast<const uint8_t*>(a.x) + row * a.ldx + col, n),
-              fp8_scale(a.x_scales[(row / a.x_tile) * a.x_lds + col / kFp8Block]), v);
-  } else {
-    load8<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + col, n, v);
-  }
-}
-
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a) {
-  const int lane = threadIdx.x & 15;
-  const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (kThreads / 16);
-  const int64_t total = a.M * kb;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 5) * 2;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  for (int64_t pair = first; pair < total; pair += groups) {
-    const int64_t blk = pair + ((threadIdx.x >> 4) & 1);
-    const int64_t row = blk / kb, k = blk - row * kb;
-    const int64_t col = k * kFp8Block + 8 * lane;
-    const int n = blk < total ? clamp8(a.K - col) : 0;
-    float v[8];
-    read8<T, VEC>(a, row, col, n, v);
-    const uint32_t b = fp8_scale_byte(group_umax<16>(amax8(v)));
+    uint4 c = make_uint4(0, 0, 0, 0);
+    float s = 1.0f;
     if (n > 0) {
-      store_codes8(a.codes + row * a.ldc + col, n, codes8(v, fp8_inverse_scale(b)));
-      if (lane == 0) a.scales[row * a.lds + k] = static_cast<uint8_t>(b);
+      c = load_codes16(static_cast<const uint8_t*>(a.x) + row * a.ldx + col, n);
+      s = fp8_scale(a.x_scales[(a.x_tile == 1 ? row : row / kFp8Block) * a.x_lds + col / kFp8Block]);
     }
+    decode16(c, s, v);
+    if (n < 16) {   // a NaN scale must not reach columns that do not exist
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i >= n) v[i] = 0.0f;
+    }
+  } else {
+    unpack<T>(load16<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + col, n, wide), v);
   }
 }
 
-// Words of a tile's row in shared memory: 128 values and one of padding, so
-// that 32 lanes reading down a column hit 32 banks.
-constexpr int kPitch = kFp8Block + 1;
-constexpr size_t kTileSmem = sizeof(float) * kFp8Block * kPitch;
-
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) quantize_tile_kernel(QuantizeArgs a) {
-  extern __shared__ float tile[];   // [128][kPitch]
-  __shared__ uint32_t tile_max;
-  const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
-  const int64_t rb = blockIdx.x / kb, cb = blockIdx.x - rb * kb;   // this tile's row and column of tiles
-  const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
-  const int lane = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  if (threadIdx.x == 0) tile_max = 0;
-  __syncthreads();
+__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a, Divider per_row, bool wide) {
+  const int lane8 = threadIdx.x & 7;
+  const uint64_t w = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t row = per_row.quotient(w);
+  const int64_t k = static_cast<int64_t>(w - row * per_row.d) * 4 + ((threadIdx.x >> 3) & 3);
+  const int64_t col = k * kFp8Block + 16 * lane8;
   grid_launch_dependents();
   grid_dependency_wait();
-  uint32_t m = 0;
-  for (int r = slot; r < kFp8Block; r += kThreads / 16) {
-    const int n = r0 + r < a.M ? clamp8(a.K - c0 - 8 * lane) : 0;
-    float v[8];
-    read8<T, VEC>(a, r0 + r, c0 + 8 * lane, n, v);
+  if (row >= a.M) return;   // whole warps
+  const int n = clamp16(a.K - col);
+  float v[16];
+  read16<T, VEC>(a, row, col, n, wide, v);
+  quantize16(v, n, a.codes + row * a.ldc + col, a.scales + row * a.lds + k, lane8);
+}
+
+// Word of the transposed tile that holds rows 4 r4 .. 4 r4 + 3 of column c: 32
+// words a column, in the order r4 ^ 4 (c / 16 % 8). A warp writes one column
+// of each of its 8 lane groups at a time, 4 words apiece: 32 banks.
+__device__ __forceinline__ int tile_word(int c, int r4) { return c * 32 + (r4 ^ (4 * ((c >> 4) & 7))); }
+
+template <typename T, bool VEC, bool TILE, bool TRANSPOSE>
+__global__ void __launch_bounds__(kThreads) quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
+  __shared__ __align__(16) uint32_t words[TRANSPOSE ? kFp8Block * 32 : 4];
+  __shared__ uint32_t col_max[kFp8Block];   // TILE: entry 0 is the tile's
+  const int64_t rb = per_row.quotient(blockIdx.x);
+  const int64_t cb = blockIdx.x - rb * static_cast<int64_t>(per_row.d);
+  const int lane8 = threadIdx.x & 7, r4 = threadIdx.x >> 3;
+  const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
+  const int64_t row = r0 + 4 * r4, col = c0 + 16 * lane8;
+  if (threadIdx.x < kFp8Block) col_max[threadIdx.x] = 0;
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  float v[4][16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile[r * kPitch + 8 * lane + i] = v[i];
-    const uint32_t top = group_umax<16>(amax8(v));
-    m = max(m, top);
-    if (a.codes && a.tile == 1 && n > 0) {
-      const uint32_t b = fp8_scale_byte(top);
-      store_codes8(a.codes + (r0 + r) * a.ldc + c0 + 8 * lane, n, codes8(v, fp8_inverse_scale(b)));
-      if (lane == 0) a.scales[(r0 + r) * a.lds + cb] = static_cast<uint8_t>(b);
+  for (int i = 0; i < 4; ++i) read16<T, VEC>(a, row + i, col, row + i < a.M ? clamp16(a.K - col) : 0, wide, v[i]);
+  __syncthreads();
+
+  if (TILE) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = amax3(m, amax_of(v[i]), 0.0f);
+    const uint32_t top = group_umax<32>(m);
+    if ((threadIdx.x & 31) == 0) atomicMax(&col_max[0], top);
+  } else {
+    if (a.codes) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        quantize16(v[i], row + i < a.M ? clamp16(a.K - col) : 0, a.codes + (row + i) * a.ldc + col,
+                   a.scales + (row + i) * a.lds + cb, lane8);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      // the lanes 8 apart hold other rows of the same column
+      uint32_t m = __float_as_uint(amax3(amax3(0.0f, v[0][e], v[1][e]), v[2][e], v[3][e]));
+      m = max(m, __shfl_xor_sync(kFullMask, m, 8));
+      m = max(m, __shfl_xor_sync(kFullMask, m, 16));
+      if ((threadIdx.x & 31) < 8) atomicMax(&col_max[16 * lane8 + e], m);
     }
   }
-  if (a.tile != 1) atomicMax(&tile_max, m);
   __syncthreads();
-  if (a.tile != 1) {
-    const uint32_t b = fp8_scale_byte(tile_max);
+  if (TILE) {
+    const uint32_t b = fp8_scale_byte(col_max[0]);
+    const float inv = fp8_inverse_scale(b);
     if (threadIdx.x == 0) {
       if (a.codes) a.scales[rb * a.lds + cb] = static_cast<uint8_t>(b);
-      if (a.t_codes) a.t_scales[cb * a.t_lds + rb] = static_cast<uint8_t>(b);
+      if (TRANSPOSE) a.t_scales[cb * a.t_lds + rb] = static_cast<uint8_t>(b);
     }
-    if (a.codes)
-      for (int r = slot; r < kFp8Block; r += kThreads / 16) {
-        const int n = r0 + r < a.M ? clamp8(a.K - c0 - 8 * lane) : 0;
-        float v[8];
+    if (a.codes) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = tile[r * kPitch + 8 * lane + i];
-        store_codes8(a.codes + (r0 + r) * a.ldc + c0 + 8 * lane, n, codes8(v, fp8_inverse_scale(b)));
-      }
+      for (int i = 0; i < 4; ++i)
+        store_codes16(a.codes + (row + i) * a.ldc + col, row + i < a.M ? clamp16(a.K - col) : 0, codes16(v[i], inv));
+    }
   }
-  if (!a.t_codes) return;
-  // the transpose: 16 lanes take one column, 8 rows each
-  for (int c = slot; c < kFp8Block; c += kThreads / 16) {
-    const int n = c0 + c < a.K ? clamp8(a.M - r0 - 8 * lane) : 0;
-    float v[8];
+  if (!TRANSPOSE) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = tile[(8 * lane + i) * kPitch + c];
-    const uint32_t b = fp8_scale_byte(a.tile == 1 ? group_umax<16>(amax8(v)) : tile_max);
-    store_codes8(a.t_codes + (c0 + c) * a.t_ldc + r0 + 8 * lane, n, codes8(v, fp8_inverse_scale(b)));
-    if (a.tile == 1 && lane == 0 && n > 0) a.t_scales[(c0 + c) * a.t_lds + rb] = static_cast<uint8_t>(b);
+  for (int e = 0; e < 16; ++e) {
+    const int c = 16 * lane8 + e;
+    const float inv = fp8_inverse_scale(fp8_scale_byte(col_max[TILE ? 0 : c]));
+    words[tile_word(c, r4)] = e4m3x4_from_f32(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv);
+  }
+  if (!TILE && threadIdx.x < kFp8Block && c0 + threadIdx.x < a.K)
+    a.t_scales[(c0 + threadIdx.x) * a.t_lds + rb] = static_cast<uint8_t>(fp8_scale_byte(col_max[threadIdx.x]));
+  __syncthreads();
+  // 8 lanes write the 128 codes of one column, 16 each
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = 32 * i + r4;
+    const int n = c0 + c < a.K ? clamp16(a.M - r0 - 16 * lane8) : 0;
+    const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(c, 4 * lane8)]);
+    store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, n, w);
   }
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_t(const QuantizeArgs& a, int sms, cudaStream_t st) {
-  const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
+cudaError_t launch_t(const QuantizeArgs& a, bool wide, cudaStream_t st) {
   if (!a.t_codes && a.tile == 1) {
-    const int64_t want = (a.M * kb + kThreads / 16 - 1) / (kThreads / 16);
-    const int64_t most = 8 * static_cast<int64_t>(sms);
-    return launch_dependent(quantize_rows_kernel<T, VEC>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                            kThreads, 0, st, a);
+    const Divider per_row((a.K + 4 * kFp8Block - 1) / (4 * kFp8Block));
+    const int64_t warps = a.M * static_cast<int64_t>(per_row.d);
+    return launch_dependent(quantize_rows_kernel<T, VEC>,
+                            dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32))), kThreads, 0,
+                            st, a, per_row, wide);
   }
-  const dim3 grid(static_cast<unsigned>(kb * ((a.M + kFp8Block - 1) / kFp8Block)));
-  return launch_dependent(quantize_tile_kernel<T, VEC>, grid, kThreads, kTileSmem, st, a);
-}
-
-template <typename F>
-void each_tile_kernel(F&& f) {
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<__nv_bfloat16, true>));
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<__nv_bfloat16, false>));
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<__half, true>));
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<__half, false>));
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<float, true>));
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<float, false>));
-  f(reinterpret_cast<const void*>(quantize_tile_kernel<Fp8Source, true>));
+  const Divider per_row((a.K + kFp8Block - 1) / kFp8Block);
+  const dim3 grid(static_cast<unsigned>(per_row.d * ((a.M + kFp8Block - 1) / kFp8Block)));
+  auto k = a.tile == 1    ? quantize_tile_kernel<T, VEC, false, true>
+           : a.t_codes ? quantize_tile_kernel<T, VEC, true, true>
+                       : quantize_tile_kernel<T, VEC, true, false>;
+  return launch_dependent(k, grid, kThreads, 0, st, a, per_row, wide);
 }
 
 }  // namespace
 
-cudaError_t prepare_quantize() {
-  cudaError_t e = cudaSuccess;
-  each_tile_kernel([&](const void* k) {
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTileSmem));
-  });
-  return e;
-}
-
-cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, bool vec, int sms, cudaStream_t st) {
-  if (a.x_scales) return launch_t<Fp8Source, true>(a, sms, st);
+cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, int vec, cudaStream_t st) {
+  if (a.x_scales) return launch_t<Fp8Source, true>(a, false, st);
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? launch_t<T, true>(a, sms, st) : launch_t<T, false>(a, sms, st);
+    return vec ? launch_t<T, true>(a, vec == kVec32, st) : launch_t<T, false>(a, false, st);
   });
 }
 

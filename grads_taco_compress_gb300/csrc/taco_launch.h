@@ -149,8 +149,9 @@ cudaError_t selftest_fault(unsigned int* bits, bool clear);
 
 // ---- FP8 block tensors (fp8_*.cu) ----
 // Pointers to elements are void* of the TACO_DTYPE_* given beside the struct;
-// ld* are elements between rows, of codes and scales bytes. `vec`: every such
-// pointer is 16-byte aligned and every row of it starts on 16 bytes.
+// ld* are elements between rows, of codes and scales bytes. `vec`: all their
+// rows start on 32 bytes, on 16, or aligned to their elements only.
+constexpr int kVecNone = 0, kVec16 = 1, kVec32 = 2;
 struct NormArgs {
   const void* x;
   const void* residual;     // may be null (then h is not written)
@@ -241,15 +242,14 @@ struct MatmulArgs {
   bool tma_out;             // out's rows all start on 16 bytes, as tensor copies need
 };
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
+cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st);
 // Most CTAs, and so rows of partial sums, of the norm's backward pass.
 constexpr int64_t kNormMaxPartials = 512;
 int norm_backward_ctas(int64_t M, int sms);
-cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, bool vec, int grid, cudaStream_t st);
-cudaError_t launch_swiglu(const SwigluArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
-cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
-cudaError_t prepare_quantize();
-cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, bool vec, int sms, cudaStream_t st);
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, int grid, cudaStream_t st);
+cudaError_t launch_swiglu(const SwigluArgs& a, int dtype, int vec, cudaStream_t st);
+cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int dtype, int vec, cudaStream_t st);
+cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, int vec, cudaStream_t st);
 cudaError_t prepare_matmul();
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, cudaStream_t st);
 cudaError_t matmul_fault(unsigned int* bits, bool clear);
