@@ -10,9 +10,11 @@
 // beyond the tensors read as zero codes (the tensor copies fill them in) with
 // scale 1.
 //
-// CTA = 8 warps, one output tile of 128 x 128:
-//   warp 0     TMA producer: stages of 128 columns, [128 rows x 128 bytes] of
-//              A and of B, 128-byte swizzle;
+// Two kernels: pairs of CTAs on 256-row tiles (matmul_pair_kernel) and, for few
+// rows of A, the roles of A and B exchanged and K split over a cluster
+// (matmul_few_kernel). Both have 8 warps:
+//   warp 0     TMA producer: stages of 128 columns, rows of 128 bytes in the
+//              128-byte swizzle;
 //   warp 1     owns the tensor memory; one lane copies the scales to tensor
 //              memory, issues the MMAs and commits each stage;
 //   warp 2     scales: every 4 stages (512 columns) one 32-bit word per row of
@@ -31,27 +33,7 @@ namespace {
 __device__ unsigned int g_fp8_matmul_fault;
 
 constexpr int kThreads = 256;
-constexpr int kTileM = 128, kTileN = 128;
-constexpr int kStages = 6;
-constexpr int kChunk = 4;                               // stages per word of scales
-constexpr int kScaleBufs = 3;
-constexpr uint32_t kStageBytes = (kTileM + kTileN) * kFp8Block;
-constexpr uint32_t kScaleBytes = (kTileM + kTileN) * 4;
-constexpr uint32_t kSmemStages = 0;
-constexpr uint32_t kSmemScales = kStages * kStageBytes;
-constexpr uint32_t kSmemBars = kSmemScales + kScaleBufs * kScaleBytes;
-constexpr uint32_t kFull = kSmemBars, kEmpty = kFull + 8 * kStages;
-constexpr uint32_t kSFull = kEmpty + 8 * kStages, kSEmpty = kSFull + 8 * kScaleBufs;
-constexpr uint32_t kDone = kSEmpty + 8 * kScaleBufs, kSlot = kDone + 8, kAbort = kSlot + 4;
-constexpr uint32_t kSmemBytes = kAbort + 4 + 1024;
-constexpr uint32_t kTmemCols = 256;
-// Scale words of three chunks in tensor memory, so that a copy never meets an
-// MMA that still reads the words it replaces: when stage i's operands have
-// landed, the MMAs of stage i - kStages are done, and those of the chunk three
-// before the one that stage i begins ended with stage i - 9.
-constexpr int kTmemScaleBufs = 3;
-static_assert(4 * kTmemScaleBufs - 3 >= kStages, "scale words replaced too early");
-constexpr uint32_t kColScales = kTileN;
+constexpr int kChunk = 4;   // stages (blocks of 128 columns) per word of scales
 
 // Instruction descriptor of kind::mxf8f6f4 with E4M3 operands, K-major, E8M0
 // scales: N >> 3 at bits 17-22, scale type at bit 23, M >> 7 at bits 27-28;
@@ -59,7 +41,6 @@ constexpr uint32_t kColScales = kTileN;
 constexpr uint32_t mx_desc(uint32_t m, uint32_t n) {
   return ((n >> 3) << 17) | (1u << 23) | ((m >> 7) << 27);
 }
-constexpr uint32_t kDesc = mx_desc(kTileM, kTileN);
 constexpr uint32_t kDescPair256 = mx_desc(256, 256), kDescPair128 = mx_desc(256, 128);
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
@@ -128,148 +109,28 @@ __device__ __forceinline__ void add_row(float* v, const T* p, int64_t left, bool
   }
 }
 
-// The scale word of one row for chunk q (bytes beyond the last block are
-// whatever the row's padding holds and are never used).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int64_t ld, int64_t row, int64_t rows,
-                                               int tile, int64_t q) {
-  if (row >= rows) return 0x7f7f7f7fu;
-  return *reinterpret_cast<const uint32_t*>(s + (tile == 1 ? row : row / kFp8Block) * ld + 4 * q);
+// The scale words of one row for chunks 4 g .. 4 g + 3 (16 blocks). Bytes
+// beyond the row's last block are whatever lies there and are never used. vec:
+// the rows of scales start on 16 bytes.
+struct ScaleRows {
+  const uint8_t* p;
+  int64_t ld, rows;
+  int tile, chunks;
+  bool vec;
+  __device__ __forceinline__ uint4 at(int64_t row, int g) const {
+    if (row >= rows) return make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+    const uint8_t* s = p + (tile == 1 ? row : row / kFp8Block) * ld + 16 * g;
+    if (vec) return *reinterpret_cast<const uint4*>(s);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(s);
+    const int n = chunks - 4 * g;
+    return make_uint4(w[0], n > 1 ? w[1] : 0u, n > 2 ? w[2] : 0u, n > 3 ? w[3] : 0u);
+  }
+};
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 1)
-matmul_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a) {
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  volatile uint32_t* abort_flag =
-      reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + kAbort);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tiles_n = (a.N + kTileN - 1) / kTileN;
-  const int64_t m0 = blockIdx.x / tiles_n * kTileM, n0 = blockIdx.x % tiles_n * kTileN;
-  const int kb = static_cast<int>((a.K + kFp8Block - 1) / kFp8Block);
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(base + kFull + 8 * s, 1);
-      mbar_init(base + kEmpty + 8 * s, 1);
-    }
-    for (int s = 0; s < kScaleBufs; ++s) {
-      mbar_init(base + kSFull + 8 * s, 1);
-      mbar_init(base + kSEmpty + 8 * s, 1);
-    }
-    mbar_init(base + kDone, 1);
-    *abort_flag = 0u;
-    fence_mbar_init();
-  }
-  if (warp == 1) tmem_alloc(base + kSlot, kTmemCols);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = lds_u32(base + kSlot);
-  grid_launch_dependents();
-  grid_dependency_wait();
-
-  if (warp == 0) {
-    if (lane == 0) {
-      prefetch_map(&maps.a);
-      prefetch_map(&maps.b);
-      uint64_t policy;
-      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
-      int i = 0;
-      for (; i < kb; ++i) {
-        const int s = i % kStages;
-        if (!wait_here(base + kEmpty + 8 * s, ((i / kStages) & 1u) ^ 1u, abort_flag)) break;
-        const uint32_t st = base + kSmemStages + s * kStageBytes;
-        mbar_arrive_expect_tx(base + kFull + 8 * s, kStageBytes);
-        tma_load_2d(st, &maps.a, i * kFp8Block, static_cast<int>(m0), base + kFull + 8 * s, policy);
-        tma_load_2d(st + kTileM * kFp8Block, &maps.b, i * kFp8Block, static_cast<int>(n0),
-                    base + kFull + 8 * s, policy);
-      }
-      if (i < kb)   // copies still in flight land before the CTA exits
-        for (int j = i > kStages ? i - kStages : 0; j < i; ++j)
-          mbar_wait(base + kFull + 8 * (j % kStages), (j / kStages) & 1u);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int i = 0; i < kb && ok; ++i) {
-        const int s = i % kStages, q = i / kChunk, j = i % kChunk, sb = q % kScaleBufs;
-        ok = wait_here(base + kFull + 8 * s, (i / kStages) & 1u, abort_flag);
-        if (ok && j == 0) ok = wait_here(base + kSFull + 8 * sb, (q / kScaleBufs) & 1u, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sfa = tmem + kColScales + 8 * (q % kTmemScaleBufs), sfb = sfa + 4;
-        if (j == 0) {
-          const uint32_t sc = base + kSmemScales + sb * kScaleBytes;
-          tmem_copy_scales(sfa, sc);
-          tmem_copy_scales(sfb, sc + 4 * kTileM);
-          mma_commit(base + kSEmpty + 8 * sb);
-        }
-        const uint32_t st = base + kSmemStages + s * kStageBytes;
-        const uint32_t idesc = kDesc | (static_cast<uint32_t>(j) << 29) | (static_cast<uint32_t>(j) << 4);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_mx(tmem, umma_desc(st + 32 * kk, kSwizzle128, 1024),
-                 umma_desc(st + kTileM * kFp8Block + 32 * kk, kSwizzle128, 1024), idesc, sfa,
-                 sfb, (i | kk) != 0);
-        mma_commit(base + kEmpty + 8 * s);
-      }
-      mma_commit(base + kDone);
-      mbar_wait(base + kDone, 0);   // nothing in flight when the tensor memory is freed
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    const int chunks = (kb + kChunk - 1) / kChunk;
-    bool ok = true;
-    for (int q = 0; q < chunks && ok; ++q) {
-      const int sb = q % kScaleBufs;
-      ok = wait_here(base + kSEmpty + 8 * sb, ((q / kScaleBufs) & 1u) ^ 1u, abort_flag);
-      ok = __all_sync(kFullMask, ok);
-      if (!ok) break;
-      const uint32_t sc = base + kSmemScales + sb * kScaleBytes;
-#pragma unroll
-      for (int r = 0; r < kTileM; r += 32)
-        asm volatile("st.shared.u32 [%0], %1;" :: "r"(sc + lane * 16 + r / 8),
-                     "r"(scale_word(a.sa, a.lda_s, m0 + r + lane, a.M, a.tile_a, q)) : "memory");
-#pragma unroll
-      for (int r = 0; r < kTileN; r += 32)
-        asm volatile("st.shared.u32 [%0], %1;" :: "r"(sc + 4 * kTileM + lane * 16 + r / 8),
-                     "r"(scale_word(a.sb, a.ldb_s, n0 + r + lane, a.N, a.tile_b, q)) : "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(base + kSFull + 8 * sb);
-    }
-  } else if (warp >= 4) {
-    const int quad = warp & 3;
-    const int64_t m = m0 + quad * 32 + lane;
-    const bool got = wait_here(base + kDone, 0, abort_flag) && *abort_flag == 0u;
-    tc_fence_after();
-    const bool all = __all_sync(kFullMask, got);
-    if (all)
-      for (int c = 0; c < kTileN; c += 16) {
-        float v[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
-        tmem_wait_ld();
-        reg_fence16(v);
-        if (m < a.M)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int64_t n = n0 + c + i;
-            if (n < a.N) {
-              float r = v[i];
-              if (a.add) r += to_f32(static_cast<const T*>(a.add)[m * a.ldadd + n]);
-              static_cast<T*>(a.out)[m * a.ldo + n] = from_f32<T>(r);
-            }
-          }
-      }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
+__device__ __forceinline__ void sts_words(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  sts128(addr, make_uint4(a, b, c, d));
 }
 
 // ------------------------------------------------------------ CTA pairs ----
@@ -311,6 +172,11 @@ __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatil
       return false;
     }
   }
+}
+__device__ __forceinline__ void tma_load_2d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -530,42 +396,53 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------------------- scales ----
-    // Words of the next chunk are read before the buffer they go to is free.
-    uint32_t wa[4], wb[TN / 32];
-    auto fetch = [&](int64_t t, int q) {
+    // The words of 4 chunks are read together, 4 chunks ahead of their use.
+    const ScaleRows ra{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa}, rb{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb};
+    uint4 na[4], nb[TN / 32];
+    const auto fetch = [&](int64_t t, int g) {
       int64_t mt, nt;
       tm.at(t, mt, nt);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        wa[r] = scale_word(a.sa, a.lda_s, mt * 256 + rank * 128 + r * 32 + lane, a.M, a.tile_a, q);
+      for (int r = 0; r < 4; ++r) na[r] = ra.at(mt * 256 + rank * 128 + r * 32 + lane, g);
 #pragma unroll
-      for (int r = 0; r < TN / 32; ++r)
-        wb[r] = scale_word(a.sb, a.ldb_s, nt * TN + r * 32 + lane, a.N, a.tile_b, q);
+      for (int r = 0; r < TN / 32; ++r) nb[r] = rb.at(nt * TN + r * 32 + lane, g);
     };
+    const int groups = (chunks + 3) / 4;
     uint32_t q = 0;
     int64_t t = pair;
-    int k = 0;
+    int g = 0;
+    bool ok = true;
     if (t < tiles) fetch(t, 0);
-    while (t < tiles) {
-      const uint32_t sb = q & 1u;
-      const bool ok = wait_pair(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
-      if (!__all_sync(kFullMask, ok)) break;
-      const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(sc), "r"(wa[0]), "r"(wa[1]), "r"(wa[2]), "r"(wa[3])
-                   : "memory");
+    while (t < tiles && ok) {
+      uint4 wa[4], wb[TN / 32];
 #pragma unroll
-      for (int g = 0; g < TN / 128; ++g)
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(sc + 512 * (g + 1)), "r"(wb[4 * g]),
-                     "r"(wb[4 * g + 1]), "r"(wb[4 * g + 2]), "r"(wb[4 * g + 3]) : "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(in_cta(base + S::sfull + 8 * sb, 0));
-      ++q;
-      if (++k == chunks) {
-        k = 0;
+      for (int r = 0; r < 4; ++r) wa[r] = na[r];
+#pragma unroll
+      for (int r = 0; r < TN / 32; ++r) wb[r] = nb[r];
+      const int here = chunks - 4 * g;
+      if (++g == groups) {
+        g = 0;
         t += pairs;
       }
-      if (t < tiles) fetch(t, k);
+      if (t < tiles) fetch(t, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= here) break;
+        const uint32_t sb = q & 1u;
+        ok = wait_pair(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
+        ok = __all_sync(kFullMask, ok);
+        if (!ok) break;
+        const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
+        sts_words(sc, word_of(wa[0], j), word_of(wa[1], j), word_of(wa[2], j), word_of(wa[3], j));
+#pragma unroll
+        for (int n = 0; n < TN / 128; ++n)
+          sts_words(sc + 512 * (n + 1), word_of(wb[4 * n], j), word_of(wb[4 * n + 1], j), word_of(wb[4 * n + 2], j),
+                    word_of(wb[4 * n + 3], j));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(in_cta(base + S::sfull + 8 * sb, 0));
+        ++q;
+      }
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------- epilogue ----
@@ -671,6 +548,236 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
   }
 }
 
+// -------------------------------------------------------------- few rows ----
+// C with few rows of A ("tokens"): the 128 rows of one MMA are rows of B
+// (weights), TT tokens its columns, and the blocks of K are split over the CTAs
+// of a cluster, each of which reads its own part of the weights once. The
+// partial sums meet through distributed shared memory: every CTA adds the
+// parts of its tokens in the order of the splits and writes them.
+template <int TT>
+struct Few {
+  static constexpr uint32_t kW = 128 * kFp8Block, kX = TT * kFp8Block, kStage = kW + kX;
+  static constexpr int kStages = TT <= 16 ? 10 : TT == 32 ? 9 : TT == 64 ? 7 : 6;
+  static constexpr uint32_t kScale = 1024;                 // words of 128 weight rows and 128 token rows
+  static constexpr uint32_t stages = 0;                    // and then the partial sums, [token][128] fp32
+  static constexpr uint32_t scales = kStages * kStage;
+  static constexpr uint32_t full = scales + 2 * kScale;
+  static constexpr uint32_t empty = full + 8 * kStages;
+  static constexpr uint32_t sfull = empty + 8 * kStages;
+  static constexpr uint32_t sempty = sfull + 16;
+  static constexpr uint32_t tfull = sempty + 16;
+  static constexpr uint32_t tempty = tfull + 16;
+  static constexpr uint32_t done = tempty + 16;
+  static constexpr uint32_t slot = done + 8;
+  static constexpr uint32_t abort_flag = slot + 4;
+  static constexpr uint32_t bytes = abort_flag + 4 + 1024;
+  static_assert(bytes <= 232448 && kStages * kStage >= TT * 128 * 4, "shared memory per CTA");
+  static constexpr uint32_t kTmemCols = TT <= 16 ? 64 : TT == 32 ? 128 : TT == 64 ? 256 : 512;
+  static constexpr uint32_t kColScales = 2 * TT;
+  static_assert(kColScales + 16 <= kTmemCols, "tensor memory");
+};
+
+template <typename T, int TT>
+__global__ void __launch_bounds__(kThreads, 1)
+matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int splits) {
+  using S = Few<TT>;
+  constexpr bool kSeg = std::is_same<T, float>::value;
+  constexpr uint32_t kDesc = ((TT >> 3) << 17) | (1u << 23) | (1u << 27);   // mx_desc(128, TT)
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  volatile uint32_t* abort_flag =
+      reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + S::abort_flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x / splits) * 128;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * TT;
+  const int kb = static_cast<int>((a.K + kFp8Block - 1) / kFp8Block);
+  const int k0 = static_cast<int>(static_cast<int64_t>(kb) * rank / splits);
+  const int k1 = static_cast<int>(static_cast<int64_t>(kb) * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(base + S::full + 8 * s, 1);
+      mbar_init(base + S::empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(base + S::sfull + 8 * s, 1);
+      mbar_init(base + S::sempty + 8 * s, 1);
+      mbar_init(base + S::tfull + 8 * s, 1);
+      mbar_init(base + S::tempty + 8 * s, 4);
+    }
+    mbar_init(base + S::done, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(base + S::slot, S::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = lds_u32(base + S::slot);
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  bool failed = false;
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_map(&maps.a);
+      prefetch_map(&maps.b);
+      int i = 0;
+      bool ok = true;
+      for (int k = k0; k < k1; ++k, ++i) {
+        const int s = i % S::kStages;
+        ok = wait_here(base + S::empty + 8 * s, ((i / S::kStages) & 1u) ^ 1u, abort_flag);
+        if (!ok) break;
+        const uint32_t st = base + S::stages + s * S::kStage, bar = base + S::full + 8 * s;
+        mbar_arrive_expect_tx(bar, S::kStage);
+        tma_load_2d_plain(st, &maps.b, k * kFp8Block, static_cast<int>(n0), bar);
+        tma_load_2d_plain(st + S::kW, &maps.a, k * kFp8Block, static_cast<int>(m0), bar);
+      }
+      if (!ok)   // copies still in flight land before the CTA goes on
+        for (int j = i > S::kStages ? i - S::kStages : 0; j < i; ++j)
+          mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t i = 0, q = 0, u = 0;
+      bool ok = true;
+      for (int k = k0; k < k1 && ok; ++k, ++i) {
+        const uint32_t s = i % S::kStages, sb = q & 1u, j = k % kChunk;
+        const bool first = kSeg ? i % kSegment == 0 : i == 0;
+        const bool last = k + 1 == k1 || (kSeg && (i + 1) % kSegment == 0);
+        if (first && u >= 2) ok = wait_here(base + S::tempty + 8 * (u & 1u), ((u - 2) >> 1) & 1u, abort_flag);
+        if (ok && (j == 0 || i == 0)) ok = wait_here(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
+        if (ok) ok = wait_here(base + S::full + 8 * s, (i / S::kStages) & 1u, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sfw = tmem + S::kColScales + 8 * sb, sfx = sfw + 4;
+        if (j == 0 || i == 0) {
+          const uint32_t sc = base + S::scales + sb * S::kScale;
+          tmem_copy_scales(sfw, sc);
+          tmem_copy_scales(sfx, sc + 512);
+        }
+        const uint32_t st = base + S::stages + s * S::kStage;
+        const uint32_t idesc = kDesc | (j << 29) | (j << 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_mx(tmem + (u & 1u) * TT, umma_desc(st + 32 * kk, kSwizzle128, 1024),
+                 umma_desc(st + S::kW + 32 * kk, kSwizzle128, 1024), idesc, sfw, sfx, !first || kk > 0);
+        mma_commit(base + S::empty + 8 * s);
+        if (j == kChunk - 1 || k + 1 == k1) {
+          mma_commit(base + S::sempty + 8 * sb);
+          ++q;
+        }
+        if (last) {
+          mma_commit(base + S::tfull + 8 * (u & 1u));
+          ++u;
+        }
+      }
+      mma_commit(base + S::done);
+      mbar_wait(base + S::done, 0);   // nothing in flight when the stages and the tensor memory are reused
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    const int chunks = (kb + kChunk - 1) / kChunk;
+    const ScaleRows rw{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb}, rx{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa};
+    const uint4 one = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+    uint4 nw[4], nx[4];
+    const auto fetch = [&](int g) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) nw[r] = rw.at(n0 + r * 32 + lane, g);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) nx[r] = r * 32 < TT ? rx.at(m0 + r * 32 + lane, g) : one;
+    };
+    const int c0 = k0 / kChunk, c1 = (k1 + kChunk - 1) / kChunk;   // chunks of this split
+    uint32_t q = 0;
+    bool ok = true;
+    fetch(c0 / 4);
+    for (int g = c0 / 4; 4 * g < c1 && ok; ++g) {
+      uint4 ww[4], wx[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        ww[r] = nw[r];
+        wx[r] = nx[r];
+      }
+      if (4 * (g + 1) < c1) fetch(g + 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (4 * g + j < c0 || 4 * g + j >= c1) continue;
+        const uint32_t sb = q & 1u;
+        ok = wait_here(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
+        ok = __all_sync(kFullMask, ok);
+        if (!ok) break;
+        const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
+        sts_words(sc, word_of(ww[0], j), word_of(ww[1], j), word_of(ww[2], j), word_of(ww[3], j));
+        sts_words(sc + 512, word_of(wx[0], j), word_of(wx[1], j), word_of(wx[2], j), word_of(wx[3], j));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(base + S::sfull + 8 * sb);
+        ++q;
+      }
+    }
+  } else if (warp >= 4) {
+    const int quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int segments = kSeg ? (k1 - k0 + kSegment - 1) / kSegment : 1;
+    float sum[TT];
+    for (int u = 0; u < segments; ++u) {
+      bool ok = wait_here(base + S::tfull + 8 * (u & 1), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) {
+        failed = true;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < TT; c += 16) {
+        float v[16];
+        tmem_ld16(tmem + lanes + (u & 1) * TT + c, v);
+        tmem_wait_ld();
+        reg_fence16(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[c + i] = u == 0 ? v[i] : sum[c + i] + v[i];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + S::tempty + 8 * (u & 1));
+    }
+    // every MMA of this CTA has read its stages: they take the partial sums
+    if (!failed) {
+#pragma unroll
+      for (int c = 0; c < TT; ++c)
+        asm volatile("st.shared.f32 [%0], %1;" :: "r"(base + S::stages + 4 * (c * 128 + quad * 32 + lane)), "f"(sum[c])
+                     : "memory");
+    }
+  }
+  __syncwarp();
+  cluster_sync();   // every split's sums are written
+  if (warp >= 4 && !failed) {
+    const int64_t n = n0 + (warp - 4) * 32 + lane;
+    const int rows = static_cast<int>(a.M - m0 < TT ? a.M - m0 : TT);
+    for (int c = rank; c < rows; c += splits) {
+      float s = 0.0f;
+      for (int r = 0; r < splits; ++r) {
+        float v;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(v) : "r"(in_cta(base + S::stages + 4 * (c * 128 + (warp - 4) * 32 + lane), r)));
+        s = r == 0 ? v : s + v;
+      }
+      if (n < a.N) {
+        if (a.add) s += to_f32(static_cast<const T*>(a.add)[(m0 + c) * a.ldadd + n]);
+        static_cast<T*>(a.out)[(m0 + c) * a.ldo + n] = from_f32<T>(s);
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
 bool encode_codes(EncodeTiled encode, CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t cols,
                   int64_t ld, int box_rows) {
   const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -701,22 +808,30 @@ bool encode_out(EncodeTiled encode, CUtensorMap* map, const MatmulArgs& a) {
 
 cudaError_t prepare_matmul() {
   cudaError_t e = cudaSuccess;
-  const auto set = [&](const void* k, uint32_t bytes) {
+  const auto set = [&](auto k, uint32_t bytes) {
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(bytes));
   };
-  set(reinterpret_cast<const void*>(matmul_kernel<__nv_bfloat16>), kSmemBytes);
-  set(reinterpret_cast<const void*>(matmul_kernel<__half>), kSmemBytes);
-  set(reinterpret_cast<const void*>(matmul_kernel<float>), kSmemBytes);
-  set(reinterpret_cast<const void*>(matmul_pair_kernel<__nv_bfloat16, 256>), Pair<256>::bytes);
-  set(reinterpret_cast<const void*>(matmul_pair_kernel<__half, 256>), Pair<256>::bytes);
-  set(reinterpret_cast<const void*>(matmul_pair_kernel<float, 128>), Pair<128>::bytes);
+  set(matmul_pair_kernel<__nv_bfloat16, 256>, Pair<256>::bytes);
+  set(matmul_pair_kernel<__half, 256>, Pair<256>::bytes);
+  set(matmul_pair_kernel<float, 128>, Pair<128>::bytes);
+  const auto few = [&](auto t) {
+    using T = decltype(t);
+    set(matmul_few_kernel<T, 16>, Few<16>::bytes);
+    set(matmul_few_kernel<T, 32>, Few<32>::bytes);
+    set(matmul_few_kernel<T, 64>, Few<64>::bytes);
+    set(matmul_few_kernel<T, 128>, Few<128>::bytes);
+  };
+  few(__nv_bfloat16{});
+  few(__half{});
+  few(float{});
   return e;
 }
 
 // One 256 x TN tile per CTA pair, at most one pair per two SMs.
 template <typename T, int TN>
-cudaError_t launch_pair(EncodeTiled encode, MatmulArgs a, int sms, cudaStream_t st) {
+cudaError_t launch_pair(EncodeTiled encode, const MatmulArgs& a, int sms, cudaStream_t st) {
   MatmulMaps maps;
   if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, 128) ||
       !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, TN / 2))
@@ -729,22 +844,46 @@ cudaError_t launch_pair(EncodeTiled encode, MatmulArgs a, int sms, cudaStream_t 
                           Pair<TN>::bytes, st, maps, out, a);
 }
 
+template <typename T, int TT>
+cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cudaStream_t st) {
+  MatmulMaps maps;
+  if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, TT) ||
+      !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, 128))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128 * splits), static_cast<unsigned>((a.M + TT - 1) / TT));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Few<TT>::bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_few_kernel<T, TT>, maps, a, splits);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, cudaStream_t st) {
   EncodeTiled encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
-  if (a.M > 64) {
-    if (dtype == TACO_DTYPE_F32) return launch_pair<float, 128>(encode, a, sms, st);
-    return dtype == TACO_DTYPE_BF16 ? launch_pair<__nv_bfloat16, 256>(encode, a, sms, st)
-                                    : launch_pair<__half, 256>(encode, a, sms, st);
-  }
-  MatmulMaps maps;
-  if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, kTileM) ||
-      !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, kTileN))
-    return cudaErrorInvalidValue;
-  const int64_t tiles = ((a.M + kTileM - 1) / kTileM) * ((a.N + kTileN - 1) / kTileN);
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return launch_dependent(matmul_kernel<T>, dim3(static_cast<unsigned>(tiles)), kThreads, kSmemBytes, st, maps, a);
+    if (a.M > 128) return launch_pair<T, std::is_same<T, float>::value ? 128 : 256>(encode, a, sms, st);
+    const int64_t tiles_n = (a.N + 127) / 128, kb = (a.K + kFp8Block - 1) / kFp8Block;
+    int64_t splits = sms / tiles_n;
+    if (splits > kb) splits = kb;
+    if (splits > 8) splits = 8;
+    if (splits < 1) splits = 1;
+    const int s = static_cast<int>(splits);
+    return a.M <= 16   ? launch_few<T, 16>(encode, a, s, st)
+           : a.M <= 32 ? launch_few<T, 32>(encode, a, s, st)
+           : a.M <= 64 ? launch_few<T, 64>(encode, a, s, st)
+                       : launch_few<T, 128>(encode, a, s, st);
   });
 }
 

@@ -238,6 +238,7 @@ struct MatmulArgs {
   int64_t ldadd;
   void* out;
   int64_t ldo;
+  bool vec_sa, vec_sb;      // the scales' rows all start on 16 bytes
   bool vec_add;             // add's rows all start on 16 bytes
   bool tma_out;             // out's rows all start on 16 bytes, as tensor copies need
 };

@@ -73,17 +73,27 @@ def _stream_of(stream, t: torch.Tensor) -> int:
 
 
 def fp8_empty(*shape: int, tile: int = 1, device="cuda") -> Fp8Tensor:
-    """An uninitialised FP8 block tensor [..., rows, cols]."""
+    """An uninitialised FP8 block tensor [rows, cols] or [planes, rows, cols]."""
     *lead, rows, cols = shape
-    kb = -(-cols // BLOCK)
-    ld, lds = _up(cols, 16), _up(kb, 4)
-    codes = torch.empty((*lead, rows, ld), dtype=torch.uint8, device=device)
-    scales = torch.empty((*lead, -(-rows // tile), lds), dtype=torch.uint8, device=device)
-    return Fp8Tensor(codes if ld == cols else codes[..., :cols], scales if lds == kb else scales[..., :kb])
+    kb, srows = -(-cols // BLOCK), -(-rows // tile)
+    ld, lds = _up(cols, 16), _up(kb, 16)
+    codes = torch.empty_strided((*lead, rows, cols), (rows * ld, ld, 1)[-len(shape):], dtype=torch.uint8, device=device)
+    scales = torch.empty_strided((*lead, srows, kb), (srows * lds, lds, 1)[-len(shape):], dtype=torch.uint8,
+                                 device=device)
+    return Fp8Tensor(codes, scales)
 
 
-def _describe(t: Fp8Tensor, what: str) -> _Fp8Struct:
-    """Checks an FP8 block tensor and describes it to the library."""
+def _new(rows: int, cols: int, tile: int, device) -> tuple[Fp8Tensor, _Fp8Struct]:
+    """fp8_empty and its description."""
+    t = fp8_empty(rows, cols, tile=tile, device=device)
+    codes, scales = t
+    return t, _Fp8Struct(codes.data_ptr(), scales.data_ptr(), _up(cols, 16), _up(-(-cols // BLOCK), 16), rows, cols,
+                         tile)
+
+
+def _describe(t: Fp8Tensor, what: str, one_row_tile: int = 1) -> _Fp8Struct:
+    """Checks an FP8 block tensor and describes it to the library. The scales
+    of a single row have the same shape in both tilings: one_row_tile then."""
     codes, scales = t
     shape, strides, sshape, sstrides = codes.shape, codes.stride(), scales.shape, scales.stride()
     if len(shape) != 2 or len(sshape) != 2 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
@@ -92,7 +102,7 @@ def _describe(t: Fp8Tensor, what: str) -> _Fp8Struct:
         raise ValueError(f"{what} must be CUDA tensors")
     rows, cols = shape
     srows, kb = sshape
-    tile = 1 if srows == rows else BLOCK
+    tile = BLOCK if srows != rows else one_row_tile if rows == 1 else 1
     if srows != -(-rows // tile) or kb != -(-cols // BLOCK):
         raise ValueError(f"{what}: scales {tuple(sshape)} do not fit codes {tuple(shape)}")
     if (cols > 1 and strides[1] != 1) or (kb > 1 and sstrides[1] != 1):
@@ -139,16 +149,19 @@ def taco_fp8_quantize(x, rows: bool = True, cols: bool = False, tile: int = 1, o
     else:
         ld = _matrix(x, "x")
         (M, K), dev = x.shape, x.device
-    if rows and out is None:
-        out = fp8_empty(M, K, tile=tile, device=dev)
-    if cols and out_t is None:
-        out_t = fp8_empty(K, M, tile=tile, device=dev)
-    out, out_t = out if rows else None, out_t if cols else None
-    a = None if out is None else _describe(out, "out")
-    b = None if out_t is None else _describe(out_t, "out_t")
-    for d in (a, b):
-        if d is not None and d.rows == 1:   # the shapes of both tilings are the same
-            d.tile_rows = tile
+    a = b = None
+    if not rows:
+        out = None
+    elif out is None:
+        out, a = _new(M, K, tile, dev)
+    else:
+        a = _describe(out, "out", tile)
+    if not cols:
+        out_t = None
+    elif out_t is None:
+        out_t, b = _new(K, M, tile, dev)
+    else:
+        b = _describe(out_t, "out_t", tile)
     if source is not None:
         st = _lib().taco_fp8_requantize(ctypes.byref(source), _ref(a), _ref(b),
                                         _stream_of(stream, x.codes))
@@ -176,17 +189,24 @@ def taco_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Ten
     if residual is not None:
         ldr = _matrix(residual, "residual", x.shape, x.dtype)
         if h is None:
-            h = torch.empty((M, H), dtype=x.dtype, device=x.device)
-        ldh = _matrix(h, "h", x.shape, x.dtype)
+            h, ldh = torch.empty((M, H), dtype=x.dtype, device=x.device), H
+        else:
+            ldh = _matrix(h, "h", x.shape, x.dtype)
     elif h is not None:
         raise ValueError("h is an output of the residual's addition: pass residual too")
     if out is None:
-        out = fp8_empty(M, H, device=x.device)
+        out, y = _new(M, H, 1, x.device)
+    else:
+        y = _describe(out, "out")
     if rstd is None:
         rstd = torch.empty(M, dtype=torch.float32, device=x.device)
-    _vector(rstd, "rstd", M, torch.float32)
-    ck = fp8_empty(M, H, device=x.device) if checkpoint is True else (checkpoint or None)
-    y, c = _describe(out, "out"), None if ck is None else _describe(ck, "checkpoint")
+    else:
+        _vector(rstd, "rstd", M, torch.float32)
+    ck = c = None
+    if checkpoint is True:
+        ck, c = _new(M, H, 1, x.device)
+    elif checkpoint:
+        ck, c = checkpoint, _describe(checkpoint, "checkpoint")
     st = _lib().taco_rms_norm_fp8(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), DTYPES[weight.dtype],
                                   DTYPES[x.dtype], M, H, float(eps), _ptr(h), ldh, _ptr(rstd), ctypes.byref(y),
                                   _ref(c), _stream_of(stream, x))
@@ -212,11 +232,13 @@ def taco_rms_norm_fp8_backward(dy: torch.Tensor, saved, weight: torch.Tensor, rs
         held, ldh = saved, _matrix(saved, "h", dy.shape, dy.dtype)
     lddh = 0 if dh is None else _matrix(dh, "dh", dy.shape, dy.dtype)
     if dx is None:
-        dx = torch.empty((M, H), dtype=dy.dtype, device=dy.device)
-    lddx = _matrix(dx, "dx", dy.shape, dy.dtype)
+        dx, lddx = torch.empty((M, H), dtype=dy.dtype, device=dy.device), H
+    else:
+        lddx = _matrix(dx, "dx", dy.shape, dy.dtype)
     if dw is None:
         dw = torch.empty(H, dtype=torch.float32, device=dy.device)
-    _vector(dw, "dw", H, torch.float32)
+    else:
+        _vector(dw, "dw", H, torch.float32)
     if workspace is None:
         workspace = torch.empty(_lib().taco_rms_norm_workspace_bytes(M, H), dtype=torch.uint8, device=dy.device)
     st = _lib().taco_rms_norm_fp8_backward(
@@ -237,10 +259,12 @@ def taco_swiglu_fp8(gate_up: torch.Tensor, checkpoint: bool | Fp8Tensor = False,
         raise ValueError("gate_up must have an even number of columns")
     F = F2 // 2
     if out is None:
-        out = fp8_empty(M, F, device=gate_up.device)
-    ck = fp8_empty(2, M, F, device=gate_up.device) if checkpoint is True else (checkpoint or None)
-    y, g, u = _describe(out, "out"), None, None
-    if ck is not None:
+        out, y = _new(M, F, 1, gate_up.device)
+    else:
+        y = _describe(out, "out")
+    ck = g = u = None
+    if checkpoint:
+        ck = fp8_empty(2, M, F, device=gate_up.device) if checkpoint is True else checkpoint
         g, u = _planes(ck)
     p = _ptr(gate_up)
     st = _lib().taco_swiglu_fp8(p, ld, p + F * gate_up.element_size(), ld, DTYPES[gate_up.dtype], M, F,
@@ -249,10 +273,14 @@ def taco_swiglu_fp8(gate_up: torch.Tensor, checkpoint: bool | Fp8Tensor = False,
     return out, ck
 
 
-def _planes(ck: Fp8Tensor):
-    if ck.codes.dim() != 3 or ck.scales.dim() != 3 or ck.codes.shape[0] != 2 or ck.scales.shape[0] != 2:
+def _planes(ck: Fp8Tensor) -> tuple[_Fp8Struct, _Fp8Struct]:
+    """Checks a gated activation's checkpoint and describes its two planes."""
+    codes, scales = ck
+    if codes.dim() != 3 or scales.dim() != 3 or codes.shape[0] != 2 or scales.shape[0] != 2:
         raise ValueError("the checkpoint of a gated activation is [2, M, F]: gate, up")
-    return tuple(_describe(Fp8Tensor(ck.codes[i], ck.scales[i]), "checkpoint") for i in (0, 1))
+    g = _describe(Fp8Tensor(codes[0], scales[0]), "checkpoint")
+    return g, _Fp8Struct(codes.data_ptr() + codes.stride(0), scales.data_ptr() + scales.stride(0), g.ld_codes,
+                         g.ld_scales, g.rows, g.cols, g.tile_rows)
 
 
 def taco_swiglu_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor, out: torch.Tensor | None = None,
@@ -262,8 +290,9 @@ def taco_swiglu_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor, out: torch
     M, F = dy.shape
     g, u = _planes(checkpoint)
     if out is None:
-        out = torch.empty((M, 2 * F), dtype=dy.dtype, device=dy.device)
-    ldo = _matrix(out, "out", (M, 2 * F), dy.dtype)
+        out, ldo = torch.empty((M, 2 * F), dtype=dy.dtype, device=dy.device), 2 * F
+    else:
+        ldo = _matrix(out, "out", (M, 2 * F), dy.dtype)
     p = _ptr(out)
     st = _lib().taco_swiglu_fp8_backward(_ptr(dy), lddy, ctypes.byref(g), ctypes.byref(u), DTYPES[dy.dtype], M, F,
                                          p, ldo, p + F * dy.element_size(), ldo, _stream_of(stream, dy))
@@ -279,8 +308,9 @@ def taco_matmul_fp8(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     x, w = _describe(a, "a"), _describe(b, "b")
     M, N = x.rows, w.rows
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
-    ldo = _matrix(out, "out", (M, N))
+        out, ldo = torch.empty((M, N), dtype=out_dtype, device=a.codes.device), max(N, 1)
+    else:
+        ldo = _matrix(out, "out", (M, N))
     ldadd = 0 if add is None else _matrix(add, "add", (M, N), out.dtype)
     st = _lib().taco_matmul_fp8(ctypes.byref(x), ctypes.byref(w), _ptr(add), ldadd, _ptr(out), ldo,
                                 DTYPES[out.dtype], _stream_of(stream, out))

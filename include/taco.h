@@ -365,8 +365,10 @@ taco_status taco_e4m3_decode_f32(const uint8_t* in, float* out, int64_t n, void*
  * aligned, ld_codes % 16 == 0), rows of scales at multiples of 4 (scales
  * 4-byte aligned, ld_scales % 4 == 0). ld_codes >= cols, and ld_scales >=
  * ceil(cols / 128). Bytes between the end of a row and the next row are
- * never written; a product may read them, in the scales' rows only, and
- * makes no use of them. rows == 0 is valid everywhere; cols >= 1.
+ * never written; a product reads scales by whole aligned words (of 4 bytes,
+ * or of 16 where rows of scales start on 16), so it may read up to 15 bytes
+ * behind a row's last scale, and makes no use of them. rows == 0 is valid
+ * everywhere; cols >= 1.
  *
  * Plain matrices are bf16, f16 or f32 (dtype) with contiguous columns and ld
  * elements between rows (ld >= cols), aligned to their element; rows that all
