@@ -109,6 +109,19 @@ __device__ __forceinline__ void add_row(float* v, const T* p, int64_t left, bool
   }
 }
 
+// One lane of a converged warp, always the same. The warps that issue copies
+// and MMAs run their loops with all lanes, so that counters, addresses and
+// descriptors stay in uniform registers, and only the instruction itself is
+// left to this lane: with the whole loop in one lane the operands of every MMA
+// went through vector registers and the issue, not the tensor cores, set the
+// pace (1000 cycles a stage at either tile width).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(kFullMask, v, 0); }
+
 // The scale words of one row for chunks 4 g .. 4 g + 3 (16 blocks). Bytes
 // beyond the row's last block are whatever lies there and are never used. vec:
 // the rows of scales start on 16 bytes.
@@ -150,28 +163,6 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
-// wait_or_abort for barriers that the other CTA of the pair arrives on.
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1u;
-      atomicOr(&g_fp8_matmul_fault, kFaultFp8MatmulWait);
-      return false;
-    }
-  }
 }
 __device__ __forceinline__ void tma_load_2d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -275,7 +266,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + S::abort_flag);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const TileMap tm{(a.M + 255) / 256, (a.N + TN - 1) / TN};
@@ -306,92 +297,104 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
   __syncthreads();
   cluster_sync();   // the other CTA's barriers are initialised
   tc_fence_after();
-  const uint32_t tmem = lds_u32(base + S::slot);
+  const uint32_t tmem = uniform(lds_u32(base + S::slot));
   grid_launch_dependents();
   grid_dependency_wait();
 
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer ----
-    if (lane == 0) {
+    const bool leader = elect_one();
+    if (leader) {
       prefetch_map(&maps.a);
       prefetch_map(&maps.b);
-      uint32_t i = 0;
-      bool ok = true;
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        int64_t mt, nt;
-        tm.at(t, mt, nt);
-        const int row_a = static_cast<int>(mt * 256 + rank * 128);
-        const int row_b = static_cast<int>(nt * TN + rank * (TN / 2));
-        for (int k = 0; k < kb; ++k, ++i) {
-          const uint32_t s = i % S::kStages, ph = (i / S::kStages) & 1u;
-          if (!wait_pair(base + S::empty + 8 * s, ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          // both CTAs' copies count on the even CTA's barrier
-          const uint32_t bar = in_cta(base + S::full + 8 * s, 0);
+    }
+    // both CTAs' copies count on the even CTA's barriers
+    const uint32_t full0 = uniform(in_cta(base + S::full, 0));
+    uint32_t s = 0, ph = 0, issued = 0;
+    bool ok = true;
+    for (int64_t t = pair; t < tiles && ok; t += pairs) {
+      int64_t mt, nt;
+      tm.at(t, mt, nt);
+      const int row_a = static_cast<int>(mt * 256 + rank * 128);
+      const int row_b = static_cast<int>(nt * TN + rank * (TN / 2));
+      for (int k = 0; k < kb; ++k) {
+        ok = wait_here(base + S::empty + 8 * s, ph ^ 1u, abort_flag);
+        ok = __all_sync(kFullMask, ok);
+        if (!ok) break;
+        const uint32_t st = base + S::stages + s * S::kStage, bar = full0 + 8 * s;
+        if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(base + S::full + 8 * s, 2 * S::kStage);
-          const uint32_t st = base + S::stages + s * S::kStage;
           tma_load_pair(st, &maps.a, k * kFp8Block, row_a, bar);
           tma_load_pair(st + S::kA, &maps.b, k * kFp8Block, row_b, bar);
         }
+        ++issued;
+        if (++s == S::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      if (!ok && rank == 0) {   // copies still in flight land before the CTAs exit
-        const uint32_t first = i > static_cast<uint32_t>(S::kStages) ? i - S::kStages : 0u;
-        for (uint32_t j = first; j < i; ++j) mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
-      }
+    }
+    if (!ok && rank == 0) {   // copies still in flight land before the CTAs exit
+      const uint32_t first = issued > static_cast<uint32_t>(S::kStages) ? issued - S::kStages : 0u;
+      for (uint32_t j = first; j < issued; ++j) mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer ----
-    if (lane == 0 && rank == 0) {
-      uint32_t i = 0, q = 0, u = 0;   // stages, scale chunks and accumulators used so far
+    if (rank == 0) {
+      const bool leader = elect_one();
+      const uint64_t adesc0 = umma_desc(base + S::stages, kSwizzle128, 1024);
+      const uint64_t bdesc0 = umma_desc(base + S::stages + S::kA, kSwizzle128, 1024);
+      uint32_t s = 0, ph = 0, q = 0, u = 0;   // stage and its phase; scale chunks and accumulators used so far
       bool ok = true;
       for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        for (int k = 0; k < kb && ok; ++k, ++i) {
-          const int j = k % kChunk;
-          const uint32_t s = i % S::kStages, sb = q & 1u;
+        for (int k = 0; k < kb; ++k) {
+          const uint32_t j = k % kChunk, sb = q & 1u;
           const bool first = kSeg ? k % kSegment == 0 : k == 0;
           const bool last = k + 1 == kb || (kSeg && (k + 1) % kSegment == 0);
           if (first) {
             // the accumulator is free, and so are the columns it shares
             const uint32_t before = TN == 256 ? 1u : 2u;
             if (u >= before)
-              ok = wait_pair(base + S::tempty + 8 * ((u - before) & 1u), ((u - before) >> 1) & 1u, abort_flag);
+              ok = wait_here(base + S::tempty + 8 * ((u - before) & 1u), ((u - before) >> 1) & 1u, abort_flag);
           }
-          if (ok && j == 0) ok = wait_pair(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
-          if (ok) ok = wait_pair(base + S::full + 8 * s, (i / S::kStages) & 1u, abort_flag);
+          if (ok && j == 0) ok = wait_here(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
+          if (ok) ok = wait_here(base + S::full + 8 * s, ph, abort_flag);
+          ok = __all_sync(kFullMask, ok);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sfa = tmem + S::kColScales + sb * S::kScaleCols, sfb = sfa + 4;
-          if (j == 0) {
-            const uint32_t sc = base + S::scales + sb * S::kScale;
-            tmem_copy_scales_pair(sfa, sc);
-#pragma unroll
-            for (int g = 0; g < TN / 128; ++g) tmem_copy_scales_pair(sfb + 4 * g, sc + 512 * (g + 1));
-          }
-          const uint32_t st = base + S::stages + s * S::kStage;
           const uint32_t d = tmem + (u & 1u) * S::kAcc1;
-          const uint32_t idesc =
-              (TN == 256 ? kDescPair256 : kDescPair128) | (static_cast<uint32_t>(j) << 29) | (static_cast<uint32_t>(j) << 4);
+          const uint32_t idesc = (TN == 256 ? kDescPair256 : kDescPair128) | (j << 29) | (j << 4);
+          const uint64_t adesc = adesc0 + s * (S::kStage >> 4), bdesc = bdesc0 + s * (S::kStage >> 4);
+          const uint32_t sc = base + S::scales + sb * S::kScale;
+          const bool end = j == kChunk - 1 || k + 1 == kb;
+          if (leader) {
+            if (j == 0) {
+              tmem_copy_scales_pair(sfa, sc);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_mx_pair(d, umma_desc(st + 32 * kk, kSwizzle128, 1024), umma_desc(st + S::kA + 32 * kk, kSwizzle128, 1024),
-                        idesc, sfa, sfb, !first || kk > 0);
-          commit_pair(base + S::empty + 8 * s);
-          if (j == kChunk - 1 || k + 1 == kb) {
-            commit_pair(base + S::sempty + 8 * sb);   // the scale words, in shared and in tensor memory
-            ++q;
+              for (int g = 0; g < TN / 128; ++g) tmem_copy_scales_pair(sfb + 4 * g, sc + 512 * (g + 1));
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)   // 32 columns: 2 units of 16 bytes further on
+              mma_mx_pair(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, sfa, sfb, !first || kk > 0);
+            commit_pair(base + S::empty + 8 * s);
+            if (end) commit_pair(base + S::sempty + 8 * sb);   // the scale words, in shared and in tensor memory
+            if (last) commit_pair(base + S::tfull + 8 * (u & 1u));
           }
-          if (last) {
-            commit_pair(base + S::tfull + 8 * (u & 1u));
-            ++u;
+          if (end) ++q;
+          if (last) ++u;
+          if (++s == S::kStages) {
+            s = 0;
+            ph ^= 1u;
           }
         }
       }
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                   :: "r"(base + S::done) : "memory");
-      mbar_wait(base + S::done, 0);   // nothing in flight when the tensor memory is freed
+      if (leader) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     :: "r"(base + S::done) : "memory");
+        mbar_wait(base + S::done, 0);   // nothing in flight when the tensor memory is freed
+      }
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -429,7 +432,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       for (int j = 0; j < 4; ++j) {
         if (j >= here) break;
         const uint32_t sb = q & 1u;
-        ok = wait_pair(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
+        ok = wait_here(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
         ok = __all_sync(kFullMask, ok);
         if (!ok) break;
         const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
@@ -464,7 +467,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
         for (int c = 0; c < TN; ++c) sum[c] = 0.0f;
         for (int g = 0; g < segments && ok; ++g, ++u) {
-          ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+          ok = wait_here(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
           ok = __all_sync(kFullMask, ok);
           if (!ok) break;
           tc_fence_after();
@@ -481,7 +484,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           if (lane == 0) arrive_cluster(tempty[u & 1u]);
         }
       } else {
-        ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+        ok = wait_here(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
         ok = __all_sync(kFullMask, ok);
       }
       if (!ok) break;
@@ -587,7 +590,7 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(smem_raw + (base - smem_u32(smem_raw)) + S::abort_flag);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int64_t n0 = static_cast<int64_t>(blockIdx.x / splits) * 128;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * TT;
@@ -614,66 +617,72 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = lds_u32(base + S::slot);
+  const uint32_t tmem = uniform(lds_u32(base + S::slot));
   grid_launch_dependents();
   grid_dependency_wait();
 
   bool failed = false;
   if (warp == 0) {
-    if (lane == 0) {
+    const bool leader = elect_one();
+    if (leader) {
       prefetch_map(&maps.a);
       prefetch_map(&maps.b);
-      int i = 0;
-      bool ok = true;
-      for (int k = k0; k < k1; ++k, ++i) {
-        const int s = i % S::kStages;
-        ok = wait_here(base + S::empty + 8 * s, ((i / S::kStages) & 1u) ^ 1u, abort_flag);
-        if (!ok) break;
-        const uint32_t st = base + S::stages + s * S::kStage, bar = base + S::full + 8 * s;
+    }
+    int i = 0;
+    bool ok = true;
+    for (int k = k0; k < k1; ++k, ++i) {
+      const int s = i % S::kStages;
+      ok = wait_here(base + S::empty + 8 * s, ((i / S::kStages) & 1u) ^ 1u, abort_flag);
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) break;
+      const uint32_t st = base + S::stages + s * S::kStage, bar = base + S::full + 8 * s;
+      if (leader) {
         mbar_arrive_expect_tx(bar, S::kStage);
         tma_load_2d_plain(st, &maps.b, k * kFp8Block, static_cast<int>(n0), bar);
         tma_load_2d_plain(st + S::kW, &maps.a, k * kFp8Block, static_cast<int>(m0), bar);
       }
-      if (!ok)   // copies still in flight land before the CTA goes on
-        for (int j = i > S::kStages ? i - S::kStages : 0; j < i; ++j)
-          mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
     }
+    if (!ok)   // copies still in flight land before the CTA goes on
+      for (int j = i > S::kStages ? i - S::kStages : 0; j < i; ++j)
+        mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t i = 0, q = 0, u = 0;
-      bool ok = true;
-      for (int k = k0; k < k1 && ok; ++k, ++i) {
-        const uint32_t s = i % S::kStages, sb = q & 1u, j = k % kChunk;
-        const bool first = kSeg ? i % kSegment == 0 : i == 0;
-        const bool last = k + 1 == k1 || (kSeg && (i + 1) % kSegment == 0);
-        if (first && u >= 2) ok = wait_here(base + S::tempty + 8 * (u & 1u), ((u - 2) >> 1) & 1u, abort_flag);
-        if (ok && (j == 0 || i == 0)) ok = wait_here(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
-        if (ok) ok = wait_here(base + S::full + 8 * s, (i / S::kStages) & 1u, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sfw = tmem + S::kColScales + 8 * sb, sfx = sfw + 4;
-        if (j == 0 || i == 0) {
-          const uint32_t sc = base + S::scales + sb * S::kScale;
+    const bool leader = elect_one();
+    const uint64_t wdesc0 = umma_desc(base + S::stages, kSwizzle128, 1024);
+    const uint64_t xdesc0 = umma_desc(base + S::stages + S::kW, kSwizzle128, 1024);
+    uint32_t i = 0, q = 0, u = 0;
+    bool ok = true;
+    for (int k = k0; k < k1; ++k, ++i) {
+      const uint32_t s = i % S::kStages, sb = q & 1u, j = k % kChunk;
+      const bool first = kSeg ? i % kSegment == 0 : i == 0;
+      const bool last = k + 1 == k1 || (kSeg && (i + 1) % kSegment == 0);
+      const bool begin = j == 0 || i == 0, end = j == kChunk - 1 || k + 1 == k1;
+      if (first && u >= 2) ok = wait_here(base + S::tempty + 8 * (u & 1u), ((u - 2) >> 1) & 1u, abort_flag);
+      if (ok && begin) ok = wait_here(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
+      if (ok) ok = wait_here(base + S::full + 8 * s, (i / S::kStages) & 1u, abort_flag);
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t sfw = tmem + S::kColScales + 8 * sb, sfx = sfw + 4;
+      const uint32_t sc = base + S::scales + sb * S::kScale;
+      const uint64_t wdesc = wdesc0 + s * (S::kStage >> 4), xdesc = xdesc0 + s * (S::kStage >> 4);
+      const uint32_t idesc = kDesc | (j << 29) | (j << 4);
+      if (leader) {
+        if (begin) {
           tmem_copy_scales(sfw, sc);
           tmem_copy_scales(sfx, sc + 512);
         }
-        const uint32_t st = base + S::stages + s * S::kStage;
-        const uint32_t idesc = kDesc | (j << 29) | (j << 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_mx(tmem + (u & 1u) * TT, umma_desc(st + 32 * kk, kSwizzle128, 1024),
-                 umma_desc(st + S::kW + 32 * kk, kSwizzle128, 1024), idesc, sfw, sfx, !first || kk > 0);
+          mma_mx(tmem + (u & 1u) * TT, wdesc + 2 * kk, xdesc + 2 * kk, idesc, sfw, sfx, !first || kk > 0);
         mma_commit(base + S::empty + 8 * s);
-        if (j == kChunk - 1 || k + 1 == k1) {
-          mma_commit(base + S::sempty + 8 * sb);
-          ++q;
-        }
-        if (last) {
-          mma_commit(base + S::tfull + 8 * (u & 1u));
-          ++u;
-        }
+        if (end) mma_commit(base + S::sempty + 8 * sb);
+        if (last) mma_commit(base + S::tfull + 8 * (u & 1u));
       }
+      if (end) ++q;
+      if (last) ++u;
+    }
+    if (leader) {
       mma_commit(base + S::done);
       mbar_wait(base + S::done, 0);   // nothing in flight when the stages and the tensor memory are reused
     }
