@@ -17,7 +17,7 @@
 //              128-byte swizzle;
 //   warp 1     owns the tensor memory; one lane copies the scales to tensor
 //              memory, issues the MMAs and commits each stage;
-//   warp 2     scales: every 4 stages (512 columns) one 32-bit word per row of
+//   warp 2     (and 3, in pairs) scales: every 4 stages (512 columns) one 32-bit word per row of
 //              A and B, byte j the scale of stage j, in the order that
 //              tcgen05.cp 32x128b spreads over the tensor memory;
 //   warps 4-7  epilogue: lane = row, tensor memory to registers to C.
@@ -55,7 +55,13 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
   const uint64_t desc = umma_desc(saddr, 0, 128);   // no swizzle, 8 rows of 16 bytes per group
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
 }
+// wait_or_abort, with the first tries free of the timer: reading it between
+// two tries cost more than most waits last.
+constexpr int kFreeTries = 256;
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < kFreeTries; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   return wait_or_abort(bar, parity, abort_flag, &g_fp8_matmul_fault, kFaultFp8MatmulWait);
 }
 
@@ -161,8 +167,13 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// An arrival on the other CTA's barrier at CTA scope: what it announces is read
+// by this SM's own tensor core or memory system (scale words, after the proxy
+// fence) or is tensor memory (after the tcgen05 fence), never by the other
+// CTA's threads. A release at cluster scope waits for the warp's loads in
+// flight (148 -> 140 us at 16384 x 4096 x 3584 without).
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -193,6 +204,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
       :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
 // 32 consecutive fp32 columns of this thread's lane, without the wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   tmem_ld16(taddr, v);
@@ -218,6 +233,12 @@ struct TileMap {
   }
 };
 
+// Chunks whose scale words may wait in shared memory. The warps that bring them
+// stall for the latency of their loads at every release to the other CTA; eight
+// chunks (32 stages) cover it (two, released with the MMAs that use them: 155
+// us instead of 127 at 16384 x 4096 x 3584).
+constexpr int kScaleBufs = 8;
+
 template <int TN>
 struct Pair {
   static constexpr int kStages = TN == 256 ? 6 : 8;
@@ -226,11 +247,12 @@ struct Pair {
   static constexpr uint32_t stages = 0;
   static constexpr uint32_t staging = kStages * kStage;    // 4 epilogue warps x 4 KB
   static constexpr uint32_t scales = staging + 4 * 4096;
-  static constexpr uint32_t full = scales + 2 * kScale;
+  static constexpr uint32_t full = scales + kScaleBufs * kScale;
   static constexpr uint32_t empty = full + 8 * kStages;
-  static constexpr uint32_t sfull = empty + 8 * kStages;
-  static constexpr uint32_t sempty = sfull + 16;
-  static constexpr uint32_t tfull = sempty + 16;
+  static constexpr uint32_t sfull = empty + 8 * kStages;      // scale words of a chunk are in shared memory
+  static constexpr uint32_t sempty = sfull + 8 * kScaleBufs;  // and were copied to tensor memory
+  static constexpr uint32_t sdone = sempty + 8 * kScaleBufs;  // the chunk's MMAs are done: its set of scale columns is free
+  static constexpr uint32_t tfull = sdone + 16;
   static constexpr uint32_t tempty = tfull + 16;
   static constexpr uint32_t done = tempty + 16;
   static constexpr uint32_t slot = done + 8;
@@ -279,9 +301,12 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       mbar_init(base + S::full + 8 * s, 1);
       mbar_init(base + S::empty + 8 * s, 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(base + S::sfull + 8 * s, 2);    // the scale warps of both CTAs
+    for (int s = 0; s < kScaleBufs; ++s) {
+      mbar_init(base + S::sfull + 8 * s, 2);    // one scale warp of each CTA
       mbar_init(base + S::sempty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(base + S::sdone + 8 * s, 1);
       mbar_init(base + S::tfull + 8 * s, 1);
       mbar_init(base + S::tempty + 8 * s, 8);   // 4 epilogue warps of both CTAs
     }
@@ -349,7 +374,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       bool ok = true;
       for (int64_t t = pair; t < tiles && ok; t += pairs) {
         for (int k = 0; k < kb; ++k) {
-          const uint32_t j = k % kChunk, sb = q & 1u;
+          const uint32_t j = k % kChunk, sb = q % kScaleBufs;
           const bool first = kSeg ? k % kSegment == 0 : k == 0;
           const bool last = k + 1 == kb || (kSeg && (k + 1) % kSegment == 0);
           if (first) {
@@ -358,12 +383,15 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
             if (u >= before)
               ok = wait_here(base + S::tempty + 8 * ((u - before) & 1u), ((u - before) >> 1) & 1u, abort_flag);
           }
-          if (ok && j == 0) ok = wait_here(base + S::sfull + 8 * sb, (q >> 1) & 1u, abort_flag);
+          if (ok && j == 0) {
+            ok = wait_here(base + S::sfull + 8 * sb, (q / kScaleBufs) & 1u, abort_flag);
+            if (ok && q >= 2) ok = wait_here(base + S::sdone + 8 * (q & 1u), ((q - 2) >> 1) & 1u, abort_flag);
+          }
           if (ok) ok = wait_here(base + S::full + 8 * s, ph, abort_flag);
           ok = __all_sync(kFullMask, ok);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sfa = tmem + S::kColScales + sb * S::kScaleCols, sfb = sfa + 4;
+          const uint32_t sfa = tmem + S::kColScales + (q & 1u) * S::kScaleCols, sfb = sfa + 4;
           const uint32_t d = tmem + (u & 1u) * S::kAcc1;
           const uint32_t idesc = (TN == 256 ? kDescPair256 : kDescPair128) | (j << 29) | (j << 4);
           const uint64_t adesc = adesc0 + s * (S::kStage >> 4), bdesc = bdesc0 + s * (S::kStage >> 4);
@@ -374,12 +402,13 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
               tmem_copy_scales_pair(sfa, sc);
 #pragma unroll
               for (int g = 0; g < TN / 128; ++g) tmem_copy_scales_pair(sfb + 4 * g, sc + 512 * (g + 1));
+              commit_pair(base + S::sempty + 8 * sb);
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 32 columns: 2 units of 16 bytes further on
               mma_mx_pair(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, sfa, sfb, !first || kk > 0);
             commit_pair(base + S::empty + 8 * s);
-            if (end) commit_pair(base + S::sempty + 8 * sb);   // the scale words, in shared and in tensor memory
+            if (end) commit_here(base + S::sdone + 8 * (q & 1u));
             if (last) commit_pair(base + S::tfull + 8 * (u & 1u));
           }
           if (end) ++q;
@@ -391,18 +420,29 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
         }
       }
       if (leader) {
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                     :: "r"(base + S::done) : "memory");
+        commit_here(base + S::done);
         mbar_wait(base + S::done, 0);   // nothing in flight when the tensor memory is freed
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp <= 3) {
     // ---------------------------------------------------------- scales ----
-    // The words of 4 chunks are read together, 4 chunks ahead of their use.
+    // The words of 4 chunks (a group) are read together; the two warps take
+    // the pair's groups in turn and read their next one ahead of its use.
     const ScaleRows ra{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa}, rb{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb};
+    const int groups = (chunks + 3) / 4;
     uint4 na[4], nb[TN / 32];
-    const auto fetch = [&](int64_t t, int g) {
+    int64_t t = pair;      // group g of tile t, whose first chunk is number q of the pair
+    int g = 0;
+    uint32_t q = 0;
+    const auto advance = [&]() {
+      q += chunks - 4 * g < 4 ? chunks - 4 * g : 4;
+      if (++g == groups) {
+        g = 0;
+        t += pairs;
+      }
+    };
+    const auto fetch = [&]() {
       int64_t mt, nt;
       tm.at(t, mt, nt);
 #pragma unroll
@@ -410,29 +450,25 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
       for (int r = 0; r < TN / 32; ++r) nb[r] = rb.at(nt * TN + r * 32 + lane, g);
     };
-    const int groups = (chunks + 3) / 4;
-    uint32_t q = 0;
-    int64_t t = pair;
-    int g = 0;
     bool ok = true;
-    if (t < tiles) fetch(t, 0);
+    if (warp == 3) advance();
+    if (t < tiles) fetch();
     while (t < tiles && ok) {
       uint4 wa[4], wb[TN / 32];
 #pragma unroll
       for (int r = 0; r < 4; ++r) wa[r] = na[r];
 #pragma unroll
       for (int r = 0; r < TN / 32; ++r) wb[r] = nb[r];
+      const uint32_t q0 = q;
       const int here = chunks - 4 * g;
-      if (++g == groups) {
-        g = 0;
-        t += pairs;
-      }
-      if (t < tiles) fetch(t, g);
+      advance();
+      if (t < tiles) advance();
+      if (t < tiles) fetch();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= here) break;
-        const uint32_t sb = q & 1u;
-        ok = wait_here(base + S::sempty + 8 * sb, ((q >> 1) & 1u) ^ 1u, abort_flag);
+        const uint32_t sb = (q0 + j) % kScaleBufs, ph = ((q0 + j) / kScaleBufs) & 1u;
+        ok = wait_here(base + S::sempty + 8 * sb, ph ^ 1u, abort_flag);
         ok = __all_sync(kFullMask, ok);
         if (!ok) break;
         const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
@@ -444,7 +480,6 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_cluster(in_cta(base + S::sfull + 8 * sb, 0));
-        ++q;
       }
     }
   } else if (warp >= 4) {
