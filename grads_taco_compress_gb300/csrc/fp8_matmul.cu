@@ -13,12 +13,12 @@
 // Two kernels: pairs of CTAs on 256-row tiles (matmul_pair_kernel) and, for few
 // rows of A, the roles of A and B exchanged and K split over a cluster
 // (matmul_few_kernel). Both have 8 warps:
-//   warp 0     TMA producer: stages of 128 columns, rows of 128 bytes in the
-//              128-byte swizzle;
+//   warp 0     TMA producer: blocks of 128 columns of K, rows of 128 bytes in
+//              the 128-byte swizzle;
 //   warp 1     owns the tensor memory; one lane copies the scales to tensor
 //              memory, issues the MMAs and commits each stage;
-//   warp 2     (and 3, in pairs) scales: every 4 stages (512 columns) one 32-bit word per row of
-//              A and B, byte j the scale of stage j, in the order that
+//   warp 2     (and 3, in pairs) scales: every chunk of 4 blocks (512 columns) one 32-bit word per
+//              row of A and B, byte j the scale of block j, in the order that
 //              tcgen05.cp 32x128b spreads over the tensor memory;
 //   warps 4-7  epilogue: lane = row, tensor memory to registers to C.
 // Every wait is bounded in time with a CTA-wide abort flag.
@@ -33,7 +33,7 @@ namespace {
 __device__ unsigned int g_fp8_matmul_fault;
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 4;   // stages (blocks of 128 columns) per word of scales
+constexpr int kChunk = 4;   // blocks of 128 columns per word of scales
 
 // Instruction descriptor of kind::mxf8f6f4 with E4M3 operands, K-major, E8M0
 // scales: N >> 3 at bits 17-22, scale type at bit 23, M >> 7 at bits 27-28;
@@ -235,14 +235,16 @@ struct TileMap {
 
 // Chunks whose scale words may wait in shared memory. The warps that bring them
 // stall for the latency of their loads at every release to the other CTA; eight
-// chunks (32 stages) cover it (two, released with the MMAs that use them: 155
+// chunks (32 blocks) cover it (two, released with the MMAs that use them: 155
 // us instead of 127 at 16384 x 4096 x 3584).
 constexpr int kScaleBufs = 8;
 
 template <int TN>
 struct Pair {
-  static constexpr int kStages = TN == 256 ? 6 : 8;
-  static constexpr uint32_t kA = 128 * kFp8Block, kB = TN / 2 * kFp8Block, kStage = kA + kB;
+  // A stage is two blocks of K: with one, the issuing warp's barrier traffic
+  // (140 ns a stage with nothing else to do) is longer than the MMAs at TN = 128.
+  static constexpr int kStages = TN == 256 ? 3 : 4;
+  static constexpr uint32_t kA = 128 * kFp8Block, kB = TN / 2 * kFp8Block, kBlock = kA + kB, kStage = 2 * kBlock;
   static constexpr uint32_t kScale = (128 + TN) * 4;       // scale words of one chunk
   static constexpr uint32_t stages = 0;
   static constexpr uint32_t staging = kStages * kStage;    // 4 epilogue warps x 4 KB
@@ -272,7 +274,7 @@ struct Pair {
 // half of B's TN rows and accumulator rows 128 r .. ; the even CTA issues the
 // MMAs of both. Persistent: pair p takes tiles p, p + pairs, ...; a tile's
 // epilogue overlaps the next one's MMAs. SEG: the sum over K is formed in
-// segments of kSegment stages, each started from zero in tensor memory, that
+// segments of kSegment blocks, each started from zero in tensor memory, that
 // the epilogue adds in registers: the tensor cores cut, not round, what falls
 // below an accumulator's last bit, and a long sum drifts.
 constexpr int kSegment = 8;
@@ -342,15 +344,20 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       tm.at(t, mt, nt);
       const int row_a = static_cast<int>(mt * 256 + rank * 128);
       const int row_b = static_cast<int>(nt * TN + rank * (TN / 2));
-      for (int k = 0; k < kb; ++k) {
+      for (int k = 0; k < kb; k += 2) {
         ok = wait_here(base + S::empty + 8 * s, ph ^ 1u, abort_flag);
         ok = __all_sync(kFullMask, ok);
         if (!ok) break;
         const uint32_t st = base + S::stages + s * S::kStage, bar = full0 + 8 * s;
         if (leader) {
-          if (rank == 0) mbar_arrive_expect_tx(base + S::full + 8 * s, 2 * S::kStage);
+          const bool two = k + 1 < kb;
+          if (rank == 0) mbar_arrive_expect_tx(base + S::full + 8 * s, two ? 2 * S::kStage : S::kStage);
           tma_load_pair(st, &maps.a, k * kFp8Block, row_a, bar);
           tma_load_pair(st + S::kA, &maps.b, k * kFp8Block, row_b, bar);
+          if (two) {
+            tma_load_pair(st + S::kBlock, &maps.a, (k + 1) * kFp8Block, row_a, bar);
+            tma_load_pair(st + S::kBlock + S::kA, &maps.b, (k + 1) * kFp8Block, row_b, bar);
+          }
         }
         ++issued;
         if (++s == S::kStages) {
@@ -373,10 +380,10 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       uint32_t s = 0, ph = 0, q = 0, u = 0;   // stage and its phase; scale chunks and accumulators used so far
       bool ok = true;
       for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        for (int k = 0; k < kb; ++k) {
+        for (int k = 0; k < kb; k += 2) {
           const uint32_t j = k % kChunk, sb = q % kScaleBufs;
           const bool first = kSeg ? k % kSegment == 0 : k == 0;
-          const bool last = k + 1 == kb || (kSeg && (k + 1) % kSegment == 0);
+          const bool last = k + 2 >= kb || (kSeg && (k + 2) % kSegment == 0);
           if (first) {
             // the accumulator is free, and so are the columns it shares
             const uint32_t before = TN == 256 ? 1u : 2u;
@@ -396,7 +403,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           const uint32_t idesc = (TN == 256 ? kDescPair256 : kDescPair128) | (j << 29) | (j << 4);
           const uint64_t adesc = adesc0 + s * (S::kStage >> 4), bdesc = bdesc0 + s * (S::kStage >> 4);
           const uint32_t sc = base + S::scales + sb * S::kScale;
-          const bool end = j == kChunk - 1 || k + 1 == kb;
+          const bool end = j == kChunk - 2 || k + 2 >= kb;
           if (leader) {
             if (j == 0) {
               tmem_copy_scales_pair(sfa, sc);
@@ -407,6 +414,12 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 32 columns: 2 units of 16 bytes further on
               mma_mx_pair(d, adesc + 2 * kk, bdesc + 2 * kk, idesc, sfa, sfb, !first || kk > 0);
+            if (k + 1 < kb) {
+              const uint32_t next = idesc + ((1u << 29) | (1u << 4));   // the scale words' next byte
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_mx_pair(d, adesc + (S::kBlock >> 4) + 2 * kk, bdesc + (S::kBlock >> 4) + 2 * kk, next, sfa, sfb, 1u);
+            }
             commit_pair(base + S::empty + 8 * s);
             if (end) commit_here(base + S::sdone + 8 * (q & 1u));
             if (last) commit_pair(base + S::tfull + 8 * (u & 1u));
