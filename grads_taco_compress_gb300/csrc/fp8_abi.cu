@@ -402,6 +402,7 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   m.vec_sa = addr(a->scales) % 16 == 0 && a->ld_scales % 16 == 0;
   m.vec_sb = addr(b->scales) % 16 == 0 && b->ld_scales % 16 == 0;
   m.vec_add = vec_add != kVecNone;
+  m.tma_add = vec_add != kVecNone && (ldadd * elem(dtype)) % 16 == 0;
   // a tensor map wants a row stride of 16 bytes even where there is one row
   m.tma_out = vec_out != kVecNone && (ldo * elem(dtype)) % 16 == 0;
   int sms = 0;

@@ -243,12 +243,16 @@ template <int TN>
 struct Pair {
   // A stage is two blocks of K: with one, the issuing warp's barrier traffic
   // (140 ns a stage with nothing else to do) is longer than the MMAs at TN = 128.
-  static constexpr int kStages = TN == 256 ? 3 : 4;
+  static constexpr int kStages = 3;
   static constexpr uint32_t kA = 128 * kFp8Block, kB = TN / 2 * kFp8Block, kBlock = kA + kB, kStage = 2 * kBlock;
   static constexpr uint32_t kScale = (128 + TN) * 4;       // scale words of one chunk
   static constexpr uint32_t stages = 0;
-  static constexpr uint32_t staging = kStages * kStage;    // 4 epilogue warps x 4 KB
-  static constexpr uint32_t scales = staging + 4 * 4096;
+  // Staging of the outputs, boxes of 32 rows x 128 bytes: one for each of the 4
+  // epilogue warps, and at TN = 128 (f32) all 4 of a warp's rows, which `add`
+  // is copied to while the sums are formed.
+  static constexpr uint32_t kBoxes = TN == 128 ? 4 : 1;
+  static constexpr uint32_t staging = kStages * kStage;
+  static constexpr uint32_t scales = staging + 4 * kBoxes * 4096;
   static constexpr uint32_t full = scales + kScaleBufs * kScale;
   static constexpr uint32_t empty = full + 8 * kStages;
   static constexpr uint32_t sfull = empty + 8 * kStages;      // scale words of a chunk are in shared memory
@@ -256,7 +260,8 @@ struct Pair {
   static constexpr uint32_t sdone = sempty + 8 * kScaleBufs;  // the chunk's MMAs are done: its set of scale columns is free
   static constexpr uint32_t tfull = sdone + 16;
   static constexpr uint32_t tempty = tfull + 16;
-  static constexpr uint32_t done = tempty + 16;
+  static constexpr uint32_t added = tempty + 16;              // `add` has landed in a warp's staging
+  static constexpr uint32_t done = added + 32;
   static constexpr uint32_t slot = done + 8;
   static constexpr uint32_t abort_flag = slot + 4;
   static constexpr uint32_t bytes = abort_flag + 4 + 1024;
@@ -282,7 +287,7 @@ constexpr int kSegment = 8;
 template <typename T, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constant__ CUtensorMap out_map,
-                   MatmulArgs a) {
+                   const __grid_constant__ CUtensorMap add_map, MatmulArgs a) {
   using S = Pair<TN>;
   constexpr bool kSeg = std::is_same<T, float>::value;
   static_assert(!kSeg || TN == 128, "the segments' sum is held in registers");
@@ -312,6 +317,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       mbar_init(base + S::tfull + 8 * s, 1);
       mbar_init(base + S::tempty + 8 * s, 8);   // 4 epilogue warps of both CTAs
     }
+    for (int w = 0; w < 4; ++w) mbar_init(base + S::added + 8 * w, 1);
     mbar_init(base + S::done, 1);
     *abort_flag = 0u;
     fence_mbar_init();
@@ -499,16 +505,29 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     // -------------------------------------------------------- epilogue ----
     const int quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t staging = base + S::staging + quad * 4096;
+    const uint32_t staging = base + S::staging + quad * (S::kBoxes * 4096);
+    const bool tma_add = kSeg && a.add && a.tma_add;
     const uint32_t tempty[2] = {in_cta(base + S::tempty, 0), in_cta(base + S::tempty + 8, 0)};
     constexpr int kCols = 128 / static_cast<int>(sizeof(T));   // columns of one 128-byte staging row
     if (lane == 0 && a.tma_out) prefetch_map(&out_map);
-    uint32_t u = 0;
+    if (lane == 0 && tma_add) prefetch_map(&add_map);
+    uint32_t u = 0, adds = 0;
     bool ok = true;
     for (int64_t t = pair; t < tiles && ok; t += pairs) {
       int64_t mt, nt;
       tm.at(t, mt, nt);
       const int64_t m0 = mt * 256 + rank * 128 + quad * 32, n0 = nt * TN;
+      const int boxes = m0 >= a.M ? 0 : static_cast<int>(a.N - n0 < TN ? (a.N - n0 + kCols - 1) / kCols : TN / kCols);
+      if (kSeg && lane == 0) {
+        bulk_wait_read<0>();   // the last tile's stores have read the staging
+        if (tma_add && boxes > 0) {
+          const uint32_t bar = base + S::added + 8 * quad;
+          mbar_arrive_expect_tx(bar, boxes * 4096);
+          for (int c = 0; c < boxes; ++c)
+            tma_load_2d_plain(staging + c * 4096, &add_map, static_cast<int>(n0) + c * kCols, static_cast<int>(m0), bar);
+        }
+      }
+      __syncwarp();
       float sum[kSeg ? TN : 1];
       if constexpr (kSeg) {
         const int segments = (kb + kSegment - 1) / kSegment;
@@ -535,6 +554,11 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
         ok = wait_here(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
         ok = __all_sync(kFullMask, ok);
       }
+      if (tma_add && boxes > 0) {
+        // the copy ends in bounded time whether or not the sums arrived
+        const bool landed = wait_here(base + S::added + 8 * quad, adds++ & 1u, abort_flag);
+        ok = __all_sync(kFullMask, landed) && ok;
+      }
       if (!ok) break;
       if constexpr (!kSeg) tc_fence_after();
       const uint32_t acc = tmem + lanes + (u & 1u) * S::kAcc1;
@@ -559,17 +583,32 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           }
         }
         const int64_t m = m0 + lane, n = n0 + static_cast<int64_t>(chunk) * kCols;
-        if (a.add && m < a.M) add_row<T, kCols>(v, static_cast<const T*>(a.add) + m * a.ldadd + n, a.N - n, a.vec_add);
         // staging: 32 rows of 128 bytes, 16-byte pieces permuted by row & 7
-        if (lane == 0) bulk_wait_read<0>();   // the last store has read it
-        __syncwarp();
+        const uint32_t box = staging + (kSeg ? c * 4096 : 0), row = box + lane * 128;
+        if (tma_add) {
+          if constexpr (kSeg)
 #pragma unroll
-        for (int p = 0; p < 8; ++p) sts128(staging + lane * 128 + 16 * (p ^ (lane & 7)), pack16<T>(v + p * (kCols / 8)));
+            for (int p = 0; p < 8; ++p) {
+              const uint4 w = lds128(row + 16 * (p ^ (lane & 7)));
+              v[4 * p] += __uint_as_float(w.x);
+              v[4 * p + 1] += __uint_as_float(w.y);
+              v[4 * p + 2] += __uint_as_float(w.z);
+              v[4 * p + 3] += __uint_as_float(w.w);
+            }
+        } else if (a.add && m < a.M) {
+          add_row<T, kCols>(v, static_cast<const T*>(a.add) + m * a.ldadd + n, a.N - n, a.vec_add);
+        }
+        if (!kSeg) {
+          if (lane == 0) bulk_wait_read<0>();   // the last store has read it
+          __syncwarp();
+        }
+#pragma unroll
+        for (int p = 0; p < 8; ++p) sts128(row + 16 * (p ^ (lane & 7)), pack16<T>(v + p * (kCols / 8)));
         if (a.tma_out) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && m0 < a.M && n < a.N) {
-            tma_store_2d(&out_map, staging, static_cast<int>(n), static_cast<int>(m0));
+            tma_store_2d(&out_map, box, static_cast<int>(n), static_cast<int>(m0));
             bulk_commit();
           }
         } else {
@@ -580,9 +619,10 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
             for (int e = lane; e < kCols; e += 32)
               if (n + e < a.N)
-                p[e] = load_staged<T>(staging + r * 128 + 16 * (((e * static_cast<int>(sizeof(T))) >> 4) ^ (r & 7)) +
+                p[e] = load_staged<T>(box + r * 128 + 16 * (((e * static_cast<int>(sizeof(T))) >> 4) ^ (r & 7)) +
                                       ((e * sizeof(T)) & 15));
           }
+          if (kSeg) fence_proxy_async_smem();   // the next tile's `add` is copied over what was read here
           __syncwarp();
         }
       }
@@ -846,17 +886,17 @@ bool encode_codes(EncodeTiled encode, CUtensorMap* map, const uint8_t* p, int64_
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [32 rows x 128 bytes] boxes of the output.
+// [32 rows x 128 bytes] boxes of a matrix of the output's shape and type.
 template <typename T>
-bool encode_out(EncodeTiled encode, CUtensorMap* map, const MatmulArgs& a) {
+bool encode_out(EncodeTiled encode, CUtensorMap* map, const MatmulArgs& a, const void* p, int64_t ld) {
   const cuuint64_t dim[2] = {static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.M)};
-  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(a.ldo) * sizeof(T)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld) * sizeof(T)};
   const cuuint32_t box[2] = {128 / sizeof(T), 32};
   const cuuint32_t unit[2] = {1, 1};
   const CUtensorMapDataType type = std::is_same<T, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return encode(map, type, 2, a.out, dim, stride, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return encode(map, type, 2, const_cast<void*>(p), dim, stride, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -893,12 +933,13 @@ cudaError_t launch_pair(EncodeTiled encode, const MatmulArgs& a, int sms, cudaSt
   if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, 128) ||
       !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, TN / 2))
     return cudaErrorInvalidValue;
-  CUtensorMap out = maps.a;
-  if (a.tma_out && !encode_out<T>(encode, &out, a)) return cudaErrorInvalidValue;
+  CUtensorMap out = maps.a, add = maps.a;
+  if (a.tma_out && !encode_out<T>(encode, &out, a, a.out, a.ldo)) return cudaErrorInvalidValue;
+  if (a.add && a.tma_add && !encode_out<T>(encode, &add, a, a.add, a.ldadd)) return cudaErrorInvalidValue;
   const int64_t tiles = ((a.M + 255) / 256) * ((a.N + TN - 1) / TN);
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
   return launch_dependent(matmul_pair_kernel<T, TN>, dim3(static_cast<unsigned>(2 * pairs)), kThreads,
-                          Pair<TN>::bytes, st, maps, out, a);
+                          Pair<TN>::bytes, st, maps, out, add, a);
 }
 
 template <typename T, int TT>

@@ -240,7 +240,7 @@ struct MatmulArgs {
   int64_t ldo;
   bool vec_sa, vec_sb;      // the scales' rows all start on 16 bytes
   bool vec_add;             // add's rows all start on 16 bytes
-  bool tma_out;             // out's rows all start on 16 bytes, as tensor copies need
+  bool tma_add, tma_out;    // and its row stride is one a tensor copy takes; the same of out
 };
 
 cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st);
