@@ -21,26 +21,66 @@ constexpr int kThreads = 256;
 
 struct Fp8Source {};   // the source is codes and scales
 
-// 16 columns of a row as fp32 (of which n exist).
+// 16 columns of a row as they lie in memory (of which n exist, the others are
+// zero).
+struct Fp8Row16 {
+  uint4 codes;
+  uint32_t scale, n;
+};
+template <typename T>
+struct RowOf {
+  using type = Row16<T>;
+};
+template <>
+struct RowOf<Fp8Source> {
+  using type = Fp8Row16;
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void read16(const QuantizeArgs& a, int64_t row, int64_t col, int n, bool wide,
-                                       float (&v)[16]) {
+__device__ __forceinline__ typename RowOf<T>::type read16(const QuantizeArgs& a, int64_t row, int64_t col, int n,
+                                                          bool wide) {
   if constexpr (std::is_same<T, Fp8Source>::value) {
-    uint4 c = make_uint4(0, 0, 0, 0);
-    float s = 1.0f;
+    Fp8Row16 r{make_uint4(0, 0, 0, 0), kScaleOne, static_cast<uint32_t>(n)};
     if (n > 0) {
-      c = load_codes16(static_cast<const uint8_t*>(a.x) + row * a.ldx + col, n);
-      s = fp8_scale(a.x_scales[(a.x_tile == 1 ? row : row / kFp8Block) * a.x_lds + col / kFp8Block]);
+      r.codes = load_codes16(static_cast<const uint8_t*>(a.x) + row * a.ldx + col, n);
+      r.scale = a.x_scales[(a.x_tile == 1 ? row : row / kFp8Block) * a.x_lds + col / kFp8Block];
     }
-    decode16(c, s, v);
-    if (n < 16) {   // a NaN scale must not reach columns that do not exist
+    return r;
+  } else {
+    return load16<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + col, n, wide);
+  }
+}
+// Columns 4 q .. 4 q + 3 of them as fp32.
+template <typename T>
+__device__ __forceinline__ void values4(const typename RowOf<T>::type& r, int q, float* v) {
+  if constexpr (std::is_same<T, Fp8Source>::value) {
+    decode4(q == 0 ? r.codes.x : q == 1 ? r.codes.y : q == 2 ? r.codes.z : r.codes.w, fp8_scale(r.scale), v);
+    if (r.scale == kScaleNan) {   // which must not reach columns that do not exist
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i >= n) v[i] = 0.0f;
+      for (int i = 0; i < 4; ++i)
+        if (4 * q + i >= static_cast<int>(r.n)) v[i] = 0.0f;
+    }
+  } else if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r.w[4 * q + i]);
+  } else if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[2 * q + i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
     }
   } else {
-    unpack<T>(load16<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + col, n, wide), v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = bf16_lo(r.w[2 * q + i]);
+      v[2 * i + 1] = bf16_hi(r.w[2 * q + i]);
+    }
   }
+}
+template <typename T>
+__device__ __forceinline__ void values16(const typename RowOf<T>::type& r, float (&v)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) values4<T>(r, q, v + 4 * q);
 }
 
 template <typename T, bool VEC>
@@ -55,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a,
   if (row >= a.M) return;   // whole warps
   const int n = clamp16(a.K - col);
   float v[16];
-  read16<T, VEC>(a, row, col, n, wide, v);
+  values16<T>(read16<T, VEC>(a, row, col, n, wide), v);
   quantize16(v, n, a.codes + row * a.ldc + col, a.scales + row * a.lds + k, lane8);
 }
 
@@ -64,10 +104,61 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a,
 // of each of its 8 lane groups at a time, 4 words apiece: 32 banks.
 __device__ __forceinline__ int tile_word(int c, int r4) { return c * 32 + (r4 ^ (4 * ((c >> 4) & 7))); }
 
+// Folds the largest magnitudes of a thread's 16 columns over its 4 rows, and
+// over the 4 lanes of the warp that hold other rows of the same columns, into
+// col_max (fp32 bits). 16-bit types stay packed: with the sign cleared their
+// order is that of unsigned integers, NaN above infinity.
+template <typename T>
+__device__ __forceinline__ void fold_columns(const typename RowOf<T>::type (&r)[4], uint32_t* col_max, int lane8) {
+  const bool writes = (threadIdx.x & 31) < 8;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      constexpr uint32_t kAbs = 0x7fff7fffu;
+      uint32_t w = __vmaxu2(__vimax3_u16x2(r[0].w[i] & kAbs, r[1].w[i] & kAbs, r[2].w[i] & kAbs), r[3].w[i] & kAbs);
+      w = __vmaxu2(w, __shfl_xor_sync(kFullMask, w, 8));
+      w = __vmaxu2(w, __shfl_xor_sync(kFullMask, w, 16));
+      uint32_t lo = w << 16, hi = w & 0xffff0000u;
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        lo = __float_as_uint(f.x);
+        hi = __float_as_uint(f.y);
+      }
+      if (writes) {
+        atomicMax(&col_max[16 * lane8 + 2 * i], lo);
+        atomicMax(&col_max[16 * lane8 + 2 * i + 1], hi);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) values4<T>(r[i], q, v[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w = __float_as_uint(amax3(amax3(0.0f, v[0][e], v[1][e]), v[2][e], v[3][e]));
+        w = max(w, __shfl_xor_sync(kFullMask, w, 8));
+        w = max(w, __shfl_xor_sync(kFullMask, w, 16));
+        if (writes) atomicMax(&col_max[16 * lane8 + 4 * q + e], w);
+      }
+    }
+  }
+}
+
+// CTAs per SM that the tile kernel's registers are held to (bf16, rows and
+// transpose of 8192 x 4096: 2: 54 us, 4: 33 us; more, and more for the wider
+// sources and the tiles, spill).
+template <typename T, bool TILE>
+constexpr int tile_ctas() {
+  return std::is_same<T, float>::value ? 2 : std::is_same<T, Fp8Source>::value || TILE ? 3 : 4;
+}
+
 template <typename T, bool VEC, bool TILE, bool TRANSPOSE>
-__global__ void __launch_bounds__(kThreads) quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
+__global__ void __launch_bounds__(kThreads, (tile_ctas<T, TILE>())) quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
   __shared__ __align__(16) uint32_t words[TRANSPOSE ? kFp8Block * 32 : 4];
   __shared__ uint32_t col_max[kFp8Block];   // TILE: entry 0 is the tile's
+  __shared__ __align__(16) float col_inv[kFp8Block];
   const int64_t rb = per_row.quotient(blockIdx.x);
   const int64_t cb = blockIdx.x - rb * static_cast<int64_t>(per_row.d);
   const int lane8 = threadIdx.x & 7, r4 = threadIdx.x >> 3;
@@ -77,32 +168,32 @@ __global__ void __launch_bounds__(kThreads) quantize_tile_kernel(QuantizeArgs a,
   grid_launch_dependents();
   grid_dependency_wait();
 
-  float v[4][16];
+  typename RowOf<T>::type r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) read16<T, VEC>(a, row + i, col, row + i < a.M ? clamp16(a.K - col) : 0, wide, v[i]);
+  for (int i = 0; i < 4; ++i) r[i] = read16<T, VEC>(a, row + i, col, row + i < a.M ? clamp16(a.K - col) : 0, wide);
   __syncthreads();
 
   if (TILE) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = amax3(m, amax_of(v[i]), 0.0f);
+    for (int i = 0; i < 4; ++i) {
+      float v[16];
+      values16<T>(r[i], v);
+      m = amax3(m, amax_of(v), 0.0f);
+    }
     const uint32_t top = group_umax<32>(m);
     if ((threadIdx.x & 31) == 0) atomicMax(&col_max[0], top);
   } else {
     if (a.codes) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        quantize16(v[i], row + i < a.M ? clamp16(a.K - col) : 0, a.codes + (row + i) * a.ldc + col,
+      for (int i = 0; i < 4; ++i) {
+        float v[16];
+        values16<T>(r[i], v);
+        quantize16(v, row + i < a.M ? clamp16(a.K - col) : 0, a.codes + (row + i) * a.ldc + col,
                    a.scales + (row + i) * a.lds + cb, lane8);
+      }
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      // the lanes 8 apart hold other rows of the same column
-      uint32_t m = __float_as_uint(amax3(amax3(0.0f, v[0][e], v[1][e]), v[2][e], v[3][e]));
-      m = max(m, __shfl_xor_sync(kFullMask, m, 8));
-      m = max(m, __shfl_xor_sync(kFullMask, m, 16));
-      if ((threadIdx.x & 31) < 8) atomicMax(&col_max[16 * lane8 + e], m);
-    }
+    fold_columns<T>(r, col_max, lane8);
   }
   __syncthreads();
   if (TILE) {
@@ -114,27 +205,48 @@ __global__ void __launch_bounds__(kThreads) quantize_tile_kernel(QuantizeArgs a,
     }
     if (a.codes) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        store_codes16(a.codes + (row + i) * a.ldc + col, row + i < a.M ? clamp16(a.K - col) : 0, codes16(v[i], inv));
+      for (int i = 0; i < 4; ++i) {
+        float v[16];
+        values16<T>(r[i], v);
+        store_codes16(a.codes + (row + i) * a.ldc + col, row + i < a.M ? clamp16(a.K - col) : 0, codes16(v, inv));
+      }
     }
   }
-  if (!TRANSPOSE) return;
+  if constexpr (TRANSPOSE) {
+    float tile_inv = 0.0f;
+    if (TILE) {
+      tile_inv = fp8_inverse_scale(fp8_scale_byte(col_max[0]));
+    } else {
+      if (threadIdx.x < kFp8Block) {
+        const uint32_t b = fp8_scale_byte(col_max[threadIdx.x]);
+        col_inv[threadIdx.x] = fp8_inverse_scale(b);
+        if (c0 + threadIdx.x < a.K) a.t_scales[(c0 + threadIdx.x) * a.t_lds + rb] = static_cast<uint8_t>(b);
+      }
+      __syncthreads();
+    }
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int c = 16 * lane8 + e;
-    const float inv = fp8_inverse_scale(fp8_scale_byte(col_max[TILE ? 0 : c]));
-    words[tile_word(c, r4)] = e4m3x4_from_f32(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv);
-  }
-  if (!TILE && threadIdx.x < kFp8Block && c0 + threadIdx.x < a.K)
-    a.t_scales[(c0 + threadIdx.x) * a.t_lds + rb] = static_cast<uint8_t>(fp8_scale_byte(col_max[threadIdx.x]));
-  __syncthreads();
-  // 8 lanes write the 128 codes of one column, 16 each
+    for (int q = 0; q < 4; ++q) {
+      float v[4][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = 32 * i + r4;
-    const int n = c0 + c < a.K ? clamp16(a.M - r0 - 16 * lane8) : 0;
-    const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(c, 4 * lane8)]);
-    store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, n, w);
+      for (int i = 0; i < 4; ++i) values4<T>(r[i], q, v[i]);
+      float inv4[4];
+      if (!TILE) *reinterpret_cast<float4*>(inv4) = *reinterpret_cast<const float4*>(&col_inv[16 * lane8 + 4 * q]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 16 * lane8 + 4 * q + e;
+        const float inv = TILE ? tile_inv : inv4[e];
+        words[tile_word(c, r4)] = e4m3x4_from_f32(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv);
+      }
+    }
+    __syncthreads();
+    // 8 lanes write the 128 codes of one column, 16 each
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = 32 * i + r4;
+      const int n = c0 + c < a.K ? clamp16(a.M - r0 - 16 * lane8) : 0;
+      const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(c, 4 * lane8)]);
+      store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, n, w);
+    }
   }
 }
 
