@@ -97,6 +97,7 @@ cudaError_t device_sms(int* sms) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(g_once[dev], [dev]() {
     cudaError_t err = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess) err = prepare_norm();
     if (err == cudaSuccess) err = prepare_matmul();
     g_err[dev] = err;
   });
@@ -284,7 +285,7 @@ taco_status taco_rms_norm_fp8_backward(const void* dy, int64_t lddy, const taco_
   a.dw = dw;
   int sms = 0;
   if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_norm_backward(a, dtype, vec, norm_backward_ctas(M, sms), static_cast<cudaStream_t>(stream)));
+  return done(launch_norm_backward(a, dtype, vec, norm_backward_ctas(M, H, sms), static_cast<cudaStream_t>(stream)));
 }
 
 taco_status taco_swiglu_fp8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int dtype, int64_t M,

@@ -275,8 +275,9 @@ struct Divider {
   __device__ __forceinline__ uint64_t quotient(uint64_t n) const { return d == 1 ? n : __umul64hi(n, magic); }
 };
 
-// Sum over a CTA of WARPS warps (WARPS a runtime count <= 32); `red` holds one
-// float per warp. Every thread gets the same sum, added in the same order.
+// Sum over the CTA's `warps` warps, added in the same order in every thread.
+// `red` holds one float per warp and must not be the buffer of the call before
+// (a thread may still be reading that one).
 __device__ __forceinline__ float cta_sum(float v, float* red, int warps) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
@@ -284,8 +285,19 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int warps) {
   __syncthreads();
   float s = 0.0f;
   for (int i = 0; i < warps; ++i) s += red[i];
-  __syncthreads();   // `red` may be written again
   return s;
+}
+
+// 16 bytes global -> shared, of which the first `bytes` (0 .. 16) are read and
+// the others zero-filled; src 16-byte aligned.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of this thread have landed.
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
 // ------------------------------------------------------------- launches ----

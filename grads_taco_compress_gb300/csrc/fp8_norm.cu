@@ -78,21 +78,29 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
   }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the backward pass, the next
-// row's loads in flight while one is worked on; the CTA's column sums of
-// dy xh go to its row of `partial`.
-template <typename T, bool H>
-struct BackwardRow {
-  Row16<T> dy, dh;
-  Row16<T> h;      // H
-  uint4 codes;     // !H
-  uint32_t scale;
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the backward pass; the CTA's
+// column sums of dy xh go to its row of `partial`. Each thread copies its own
+// columns of the next DEPTH - 1 rows to shared memory while it works on one
+// (rows that do not start on 16 bytes are loaded as they come: DEPTH 0), so the
+// copies need no barrier and what is in flight costs no registers.
+template <typename T, int NC, bool H>
+struct BackwardStage {
+  static constexpr int kT = sizeof(T);                  // 16-byte pieces of 16 columns
+  static constexpr int kSaved = H ? kT : 1;
+  static constexpr int kPieces = 2 * kT + kSaved;       // dy, dh, saved
+  static constexpr size_t bytes(int threads) { return static_cast<size_t>(16) * NC * kPieces * threads; }
 };
 
-template <typename T, int NC, bool VEC, bool H>
+template <typename T, int NC, int DEPTH, bool H>
 __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs a, bool wide) {
-  __shared__ float red[16];
+  using S = BackwardStage<T, NC, H>;
+  constexpr bool VEC = DEPTH > 0;
+  constexpr int kBufs = VEC ? DEPTH : 1;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float red[2][16];
   const int warps = blockDim.x >> 5;
+  const uint32_t slot = smem_u32(ring) + 16 * threadIdx.x;
+  const uint32_t pitch = 16 * blockDim.x;
   float dw[NC][16];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
@@ -100,75 +108,136 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs a, 
     for (int i = 0; i < 16; ++i) dw[c][i] = 0.0f;
   grid_launch_dependents();
   grid_dependency_wait();
-  BackwardRow<T, H> next[NC];
-  float next_rstd = 0.0f;
-  const auto fetch = [&](int64_t row) {
-    next_rstd = a.rstd[row];
+
+  const auto column = [&](int c) { return 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x); };
+  // piece p of chunk c of a row in stage s
+  const auto place = [&](int s, int c, int p) { return slot + ((s * NC + c) * S::kPieces + p) * pitch; };
+  const auto begin_copy = [&](int64_t row, int s) {
+    if (row < a.M) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
-      const int n = clamp16(a.H - col);
-      next[c].dy = load16<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy + col, n, wide);
-      if (H) {
-        next[c].h = load16<T, VEC>(static_cast<const T*>(a.h) + row * a.ldh + col, n, wide);
-      } else {
-        next[c].codes = load_codes16(a.ck_codes + row * a.ck_ld + col, n);
-        next[c].scale = n > 0 ? a.ck_scales[row * a.ck_lds + col / kFp8Block] : kScaleOne;
+      for (int c = 0; c < NC; ++c) {
+        const int64_t col = column(c);
+        const int n = clamp16(a.H - col);
+        const auto copy = [&](const void* base, int64_t ld, int first, int pieces, int es) {
+          const char* p = static_cast<const char*>(base) + (row * ld + (n ? col : 0)) * es;
+#pragma unroll
+          for (int i = 0; i < pieces; ++i) {
+            const int left = n * es - 16 * i;
+            copy_async16(place(s, c, first + i), p + (left > 0 ? 16 * i : 0), left < 0 ? 0 : left > 16 ? 16 : left);
+          }
+        };
+        copy(a.dy, a.lddy, 0, S::kT, sizeof(T));
+        if (a.dh) copy(a.dh, a.lddh, S::kT, S::kT, sizeof(T));
+        if (H)
+          copy(a.h, a.ldh, 2 * S::kT, S::kT, sizeof(T));
+        else
+          copy(a.ck_codes, a.ck_ld, 2 * S::kT, 1, 1);
       }
-      if (a.dh) next[c].dh = load16<T, VEC>(static_cast<const T*>(a.dh) + row * a.lddh + col, n, wide);
     }
+    copy_async_commit();
   };
-  if (blockIdx.x < a.M) fetch(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    BackwardRow<T, H> cur[NC];
+  const auto staged = [&](int s, int c, int first) {
+    Row16<T> r;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) cur[c] = next[c];
+    for (int i = 0; i < S::kT; ++i) {
+      const uint4 w = lds128(place(s, c, first + i));
+      r.w[4 * i] = w.x;
+      r.w[4 * i + 1] = w.y;
+      r.w[4 * i + 2] = w.z;
+      r.w[4 * i + 3] = w.w;
+    }
+    return r;
+  };
+  // read a row ahead: they are one byte and one word
+  uint32_t next_scale[NC];
+  float next_rstd = 0.0f;
+  const auto peek = [&](int64_t row) {
+    if (row >= a.M) return;
+    next_rstd = a.rstd[row];
+    if (!H)
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        next_scale[c] = column(c) < a.H ? a.ck_scales[row * a.ck_lds + column(c) / kFp8Block] : kScaleOne;
+  };
+
+  if (VEC)
+    for (int s = 0; s < DEPTH - 1; ++s) begin_copy(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  peek(blockIdx.x);
+  float w[16];   // in registers for the whole call where a thread has one chunk
+  if (NC == 1) load_weight16<VEC>(a.weight, a.weight_dtype, column(0), clamp16(a.H - column(0)), w);
+  int s = 0;
+  uint32_t turn = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1u) {
+    if (VEC) begin_copy(row + static_cast<int64_t>(DEPTH - 1) * gridDim.x, (s + DEPTH - 1) % kBufs);
+    uint32_t scale[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) scale[c] = next_scale[c];
     const float rstd = next_rstd;
-    if (row + gridDim.x < a.M) fetch(row + gridDim.x);
+    peek(row + gridDim.x);
+    if (VEC) copy_async_wait<VEC ? DEPTH - 1 : 0>();
     float g[NC][16], xh[NC][16];
     float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      const int64_t col = column(c);
       const int n = clamp16(a.H - col);
-      unpack<T>(cur[c].dy, g[c]);
-      if (H)
-        unpack<T>(cur[c].h, xh[c]);
-      else
-        decode16(cur[c].codes, fp8_scale(cur[c].scale), xh[c]);
-      float w[16];
-      load_weight16<VEC>(a.weight, a.weight_dtype, col, n, w);
+      if (VEC) {
+        unpack<T>(staged(s, c, 0), g[c]);
+        if (H)
+          unpack<T>(staged(s, c, 2 * S::kT), xh[c]);
+        else
+          decode16(lds128(place(s, c, 2 * S::kT)), fp8_scale(scale[c]), xh[c]);
+      } else {
+        unpack<T>(load16<T, false>(static_cast<const T*>(a.dy) + row * a.lddy + col, n, false), g[c]);
+        if (H)
+          unpack<T>(load16<T, false>(static_cast<const T*>(a.h) + row * a.ldh + col, n, false), xh[c]);
+        else
+          decode16(load_codes16(a.ck_codes + row * a.ck_ld + col, n), fp8_scale(scale[c]), xh[c]);
+      }
+      if (NC > 1) load_weight16<VEC>(a.weight, a.weight_dtype, col, n, w);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        xh[c][i] = n == 16 || i < n ? xh[c][i] * rstd : 0.0f;
+        // columns that do not exist are 0, or NaN in a block whose scale is:
+        // there the row's sum is NaN by those that do
+        xh[c][i] *= rstd;
         dw[c][i] = fmaf(g[c][i], xh[c][i], dw[c][i]);
         g[c][i] *= w[i];
         sum = fmaf(g[c][i], xh[c][i], sum);
       }
     }
-    const float mean = cta_sum(sum, red, warps) / static_cast<float>(a.H);
+    const float mean = cta_sum(sum, red[turn], warps) / static_cast<float>(a.H);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      const int64_t col = column(c);
+      const int n = clamp16(a.H - col);
 #pragma unroll
       for (int i = 0; i < 16; ++i) g[c][i] = rstd * fmaf(-xh[c][i], mean, g[c][i]);
       if (a.dh) {
         float d[16];
-        unpack<T>(cur[c].dh, d);
+        unpack<T>(VEC ? staged(s, c, S::kT)
+                      : load16<T, false>(static_cast<const T*>(a.dh) + row * a.lddh + col, n, false), d);
 #pragma unroll
         for (int i = 0; i < 16; ++i) g[c][i] += d[i];
       }
-      store16<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx + col, clamp16(a.H - col), wide, pack<T>(g[c]));
+      store16<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx + col, n, wide, pack<T>(g[c]));
     }
+    s = s + 1 == kBufs ? 0 : s + 1;
   }
+  if (VEC) copy_async_wait<0>();
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+    const int64_t col = column(c);
     const int n = clamp16(a.H - col);
     float* p = a.partial + blockIdx.x * a.H + col;
+    if (n == 16 && a.H % 4 == 0) {   // every CTA's row of partial sums starts on 16 bytes
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) p[i] = dw[c][i];
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(dw[c][i], dw[c][i + 1], dw[c][i + 2], dw[c][i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) p[i] = dw[c][i];
+    }
   }
 }
 
@@ -209,10 +278,41 @@ cudaError_t launch_norm_t(const NormArgs& a, int threads, int vec, cudaStream_t 
                           dim3(static_cast<unsigned>(a.M)), threads, 0, st, a, vec == kVec32);
 }
 
+// Shared memory that a CTA's ring of rows may take: two CTAs per SM, else one.
+constexpr size_t kRingTwo = 112 * 1024, kRingOne = 226 * 1024;
+constexpr int kMaxThreads = 512;
+
+// The ring's depth for a stage of this size (0: no ring) and its bytes.
+int ring_depth(size_t stage, bool vec) { return !vec ? 0 : 4 * stage <= kRingTwo ? 4 : 2 * stage <= kRingOne ? 2 : 0; }
+
+template <typename T, int NC, bool H, typename F>
+auto with_backward_kernel(int depth, F&& f) {
+  return depth == 4   ? f(norm_backward_kernel<T, NC, 4, H>)
+         : depth == 2 ? f(norm_backward_kernel<T, NC, 2, H>)
+                      : f(norm_backward_kernel<T, NC, 0, H>);
+}
+
 template <typename T, int NC, bool H>
 cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, int vec, int grid, cudaStream_t st) {
-  return launch_dependent(vec ? norm_backward_kernel<T, NC, true, H> : norm_backward_kernel<T, NC, false, H>,
-                          dim3(grid), threads, 0, st, a, vec == kVec32);
+  const size_t stage = BackwardStage<T, NC, H>::bytes(threads);
+  const int depth = ring_depth(stage, vec != kVecNone);
+  return with_backward_kernel<T, NC, H>(depth, [&](auto k) {
+    return launch_dependent(k, dim3(grid), threads, depth * stage, st, a, vec == kVec32);
+  });
+}
+
+template <typename T, int NC, bool H>
+cudaError_t prepare_backward_t() {
+  cudaError_t e = cudaSuccess;
+  for (int depth : {2, 4})
+    if (e == cudaSuccess)
+      e = with_backward_kernel<T, NC, H>(depth, [&](auto k) {
+        const size_t most = depth * BackwardStage<T, NC, H>::bytes(kMaxThreads);
+        const size_t room = depth == 4 ? kRingTwo : kRingOne;
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(most < room ? most : room));
+      });
+  return e;
 }
 
 }  // namespace
@@ -229,8 +329,28 @@ cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStre
   });
 }
 
-int norm_backward_ctas(int64_t M, int sms) {
-  int64_t most = 2 * static_cast<int64_t>(sms);
+cudaError_t prepare_norm() {
+  cudaError_t e = cudaSuccess;
+  for (int dtype : {TACO_DTYPE_BF16, TACO_DTYPE_F16, TACO_DTYPE_F32})
+    if (e == cudaSuccess)
+      e = with_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        for (cudaError_t r : {prepare_backward_t<T, 1, true>(), prepare_backward_t<T, 1, false>(),
+                              prepare_backward_t<T, 2, true>(), prepare_backward_t<T, 2, false>(),
+                              prepare_backward_t<T, 4, true>(), prepare_backward_t<T, 4, false>()})
+          if (r != cudaSuccess) return r;
+        return cudaSuccess;
+      });
+  return e;
+}
+
+// CTAs of the backward pass: as many as stay resident (3, 2 or 1 per SM by
+// their threads), no more than rows, and no more than rows of partial sums.
+int norm_backward_ctas(int64_t M, int64_t H, int sms) {
+  int threads, nc;
+  norm_shape(H, &threads, &nc);
+  const int per_sm = threads <= 128 ? 3 : threads <= 256 ? 2 : 1;
+  int64_t most = static_cast<int64_t>(per_sm) * sms;
   if (most > kNormMaxPartials) most = kNormMaxPartials;
   return static_cast<int>(M < most ? M : most);
 }

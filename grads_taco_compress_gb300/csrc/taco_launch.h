@@ -246,7 +246,8 @@ struct MatmulArgs {
 cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st);
 // Most CTAs, and so rows of partial sums, of the norm's backward pass.
 constexpr int64_t kNormMaxPartials = 512;
-int norm_backward_ctas(int64_t M, int sms);
+cudaError_t prepare_norm();
+int norm_backward_ctas(int64_t M, int64_t H, int sms);
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, int grid, cudaStream_t st);
 cudaError_t launch_swiglu(const SwigluArgs& a, int dtype, int vec, cudaStream_t st);
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int dtype, int vec, cudaStream_t st);

@@ -84,11 +84,12 @@ def fp8_empty(*shape: int, tile: int = 1, device="cuda") -> Fp8Tensor:
 
 
 def _new(rows: int, cols: int, tile: int, device) -> tuple[Fp8Tensor, _Fp8Struct]:
-    """fp8_empty and its description."""
-    t = fp8_empty(rows, cols, tile=tile, device=device)
-    codes, scales = t
-    return t, _Fp8Struct(codes.data_ptr(), scales.data_ptr(), _up(cols, 16), _up(-(-cols // BLOCK), 16), rows, cols,
-                         tile)
+    """fp8_empty of a matrix, and its description."""
+    kb, srows = -(-cols // BLOCK), rows if tile == 1 else -(-rows // tile)
+    ld, lds = (cols + 15) & -16, (kb + 15) & -16
+    codes = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.uint8, device=device)
+    scales = torch.empty_strided((srows, kb), (lds, 1), dtype=torch.uint8, device=device)
+    return Fp8Tensor(codes, scales), _Fp8Struct(codes.data_ptr(), scales.data_ptr(), ld, lds, rows, cols, tile)
 
 
 def _describe(t: Fp8Tensor, what: str, one_row_tile: int = 1) -> _Fp8Struct:
