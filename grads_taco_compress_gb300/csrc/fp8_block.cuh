@@ -275,16 +275,19 @@ struct Divider {
   __device__ __forceinline__ uint64_t quotient(uint64_t n) const { return d == 1 ? n : __umul64hi(n, magic); }
 };
 
-// Sum over the CTA's `warps` warps, added in the same order in every thread.
-// `red` holds one float per warp and must not be the buffer of the call before
-// (a thread may still be reading that one).
-__device__ __forceinline__ float cta_sum(float v, float* red, int warps) {
+// Sum over the CTA's warps, added in the same order in every thread. `red`
+// holds 32 floats, zero beyond the warps, and must not be the buffer of the
+// call before (a thread may still be reading that one). WIDE: more than 16
+// warps may take part.
+template <bool WIDE>
+__device__ __forceinline__ float cta_sum(float v, float* red) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < warps; ++i) s += red[i];
+  float s = red[threadIdx.x & (WIDE ? 31 : 15)];
+#pragma unroll
+  for (int m = WIDE ? 16 : 8; m > 0; m >>= 1) s += __shfl_xor_sync(kFullMask, s, m);
   return s;
 }
 
@@ -292,6 +295,10 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int warps) {
 // the others zero-filled; src 16-byte aligned.
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// The same of 8 bytes.
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest N groups of this thread have landed.

@@ -22,8 +22,9 @@ namespace {
 
 template <typename T, int NC, bool VEC>
 __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
-  __shared__ float red[16];
-  const int warps = blockDim.x >> 5, lane8 = threadIdx.x & 7;
+  __shared__ float red[32];
+  const int lane8 = threadIdx.x & 7;
+  if (threadIdx.x < 32 && threadIdx.x >= blockDim.x >> 5) red[threadIdx.x] = 0.0f;
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t row = blockIdx.x;
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
   }
-  sum = cta_sum(sum, red, warps);
+  sum = cta_sum<false>(sum, red);
   const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.eps);
   if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
@@ -78,6 +79,98 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
   }
 }
 
+// The backward pass holds no block's maximum, so a thread takes 8 columns: twice
+// the warps of the forward's 16 at the same registers in all, and the row's
+// chain of loads, sum and stores needs them (two CTAs of 256 threads with 16
+// columns each, 4 warps a scheduler: 59 us at 8192 x 4096).
+template <typename T>
+struct Row8 {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void unpack8(const Row8<T>& r, f2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, float>::value) {
+      v[i] = f2{__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1])};
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+      v[i] = f2{f.x, f.y};
+    } else {
+      v[i] = f2{bf16_lo(r.w[i]), bf16_hi(r.w[i])};
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ Row8<T> pack8(const f2 (&v)[4]) {
+  Row8<T> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, float>::value) {
+      r.w[2 * i] = __float_as_uint(v[i].x);
+      r.w[2 * i + 1] = __float_as_uint(v[i].y);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(v[i].x, v[i].y);
+      r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      r.w[i] = pack_bf16x2(v[i].x, v[i].y);
+    }
+  }
+  return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, int n, const Row8<T>& r) {
+  if (VEC && n == 8) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+  } else {
+    f2 v[4];
+    unpack8<T>(r, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = from_f32<T>(i & 1 ? v[i >> 1].y : v[i >> 1].x);
+  }
+}
+// 8 entries of a vector or row, one by one where it is not aligned.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, int n, f2 (&v)[4]) {
+  Row8<T> r;
+  if (VEC && n == 8) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      *reinterpret_cast<uint4*>(r.w + 4 * i) = *reinterpret_cast<const uint4*>(p + 4 * i);
+    unpack8<T>(r, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = f2{2 * i < n ? to_f32(p[2 * i]) : 0.0f, 2 * i + 1 < n ? to_f32(p[2 * i + 1]) : 0.0f};
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_weight8(const void* w, int dtype, int64_t col, int n, f2 (&v)[4]) {
+  if (dtype == TACO_DTYPE_F32)
+    load8<float, VEC>(static_cast<const float*>(w) + col, n, v);
+  else if (dtype == TACO_DTYPE_BF16)
+    load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w) + col, n, v);
+  else
+    load8<__half, VEC>(static_cast<const __half*>(w) + col, n, v);
+}
+__device__ __forceinline__ void decode8(uint2 c, float s, f2 (&v)[4]) {
+  const f2 ss{s, s};
+  v[0] = mul2(e4m3x2_to_f2(c.x & 0xffffu), ss);
+  v[1] = mul2(e4m3x2_to_f2(c.x >> 16), ss);
+  v[2] = mul2(e4m3x2_to_f2(c.y & 0xffffu), ss);
+  v[3] = mul2(e4m3x2_to_f2(c.y >> 16), ss);
+}
+__device__ __forceinline__ uint2 load_codes8(const uint8_t* p, int n) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the backward pass; the CTA's
 // column sums of dy xh go to its row of `partial`. Each thread copies its own
 // columns of the next DEPTH - 1 rows to shared memory while it works on one
@@ -85,158 +178,194 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
 // copies need no barrier and what is in flight costs no registers.
 template <typename T, int NC, bool H>
 struct BackwardStage {
-  static constexpr int kT = sizeof(T);                  // 16-byte pieces of 16 columns
-  static constexpr int kSaved = H ? kT : 1;
-  static constexpr int kPieces = 2 * kT + kSaved;       // dy, dh, saved
-  static constexpr size_t bytes(int threads) { return static_cast<size_t>(16) * NC * kPieces * threads; }
+  // bytes of 8 columns: dy, dh, and h or codes
+  static constexpr int kRow = 8 * sizeof(T), kSaved = H ? kRow : 8;
+  static constexpr int kThread = 2 * kRow + kSaved;
+  static constexpr size_t bytes(int threads) { return static_cast<size_t>(NC) * kThread * threads; }
 };
 
 template <typename T, int NC, int DEPTH, bool H>
-__global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardArgs a, bool wide) {
+__global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a) {
   using S = BackwardStage<T, NC, H>;
   constexpr bool VEC = DEPTH > 0;
-  constexpr int kBufs = VEC ? DEPTH : 1;
+  constexpr int kPieces = S::kRow / 16;
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float red[2][16];
-  const int warps = blockDim.x >> 5;
-  const uint32_t slot = smem_u32(ring) + 16 * threadIdx.x;
-  const uint32_t pitch = 16 * blockDim.x;
-  float dw[NC][16];
+  __shared__ float red[2][32];
+  if (threadIdx.x < 32 && threadIdx.x >= blockDim.x >> 5) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.0f;
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  const uint32_t threads = blockDim.x, step = gridDim.x;
+
+  // Everything that does not change from row to row: this thread's columns and
+  // how many exist (columns beyond the row read from its start, zero bytes),
+  // its byte offsets in a row, and its place in a stage of the ring.
+  int64_t col[NC];
+  int n[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    col[c] = 8 * (static_cast<int64_t>(threadIdx.x) + c * threads);
+    const int64_t left = a.H - col[c];
+    n[c] = left < 0 ? 0 : left > 8 ? 8 : static_cast<int>(left);
+    if (n[c] == 0) col[c] = 0;
+  }
+  const uint32_t stage_bytes = NC * S::kThread * threads;
+  const uint32_t slot16 = smem_u32(ring) + 16 * threadIdx.x;
+  const uint32_t slot8 = smem_u32(ring) + 2 * S::kRow * threads + 8 * threadIdx.x;   // codes: after dy and dh
+  f2 dw[NC][4];
 #pragma unroll
   for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[c][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) dw[c][i] = f2{0.0f, 0.0f};
   grid_launch_dependents();
   grid_dependency_wait();
 
-  const auto column = [&](int c) { return 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x); };
-  // piece p of chunk c of a row in stage s
-  const auto place = [&](int s, int c, int p) { return slot + ((s * NC + c) * S::kPieces + p) * pitch; };
-  const auto begin_copy = [&](int64_t row, int s) {
-    if (row < a.M) {
+  const T* dy = static_cast<const T*>(a.dy) + blockIdx.x * a.lddy;
+  const T* dh = a.dh ? static_cast<const T*>(a.dh) + blockIdx.x * a.lddh : nullptr;
+  const T* h = H ? static_cast<const T*>(a.h) + blockIdx.x * a.ldh : nullptr;
+  const uint8_t* codes = H ? nullptr : a.ck_codes + blockIdx.x * a.ck_ld;
+  const uint8_t* scales = H ? nullptr : a.ck_scales + blockIdx.x * a.ck_lds;
+  T* dx = static_cast<T*>(a.dx) + blockIdx.x * a.lddx;
+  const int64_t dy_step = step * a.lddy, dh_step = step * a.lddh, h_step = step * a.ldh, codes_step = step * a.ck_ld,
+                scales_step = step * a.ck_lds, dx_step = step * a.lddx;
+
+  // dy, dh, h and codes run ahead of the row that is worked on by the ring's
+  // depth (VEC), scales and rstd by one row
+  int64_t ahead = blockIdx.x;
+  uint32_t put = 0, get = 0;   // byte offsets of the stages written and read next
+  const auto begin_copy = [&]() {
+    if (ahead < a.M) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int64_t col = column(c);
-        const int n = clamp16(a.H - col);
-        const auto copy = [&](const void* base, int64_t ld, int first, int pieces, int es) {
-          const char* p = static_cast<const char*>(base) + (row * ld + (n ? col : 0)) * es;
+        const uint32_t to = put + c * (S::kThread * threads);
+        const auto copy = [&](const T* from, int first) {
 #pragma unroll
-          for (int i = 0; i < pieces; ++i) {
-            const int left = n * es - 16 * i;
-            copy_async16(place(s, c, first + i), p + (left > 0 ? 16 * i : 0), left < 0 ? 0 : left > 16 ? 16 : left);
+          for (int i = 0; i < kPieces; ++i) {
+            constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+            const int left = n[c] - kPer * i;   // elements of this piece that exist
+            const int bytes = (left < 0 ? 0 : left > kPer ? kPer : left) * static_cast<int>(sizeof(T));
+            copy_async16(slot16 + to + (first + i) * 16 * threads, from + col[c] + (left > 0 ? kPer * i : 0), bytes);
           }
         };
-        copy(a.dy, a.lddy, 0, S::kT, sizeof(T));
-        if (a.dh) copy(a.dh, a.lddh, S::kT, S::kT, sizeof(T));
+        copy(dy, 0);
+        if (dh) copy(dh, kPieces);
         if (H)
-          copy(a.h, a.ldh, 2 * S::kT, S::kT, sizeof(T));
+          copy(h, 2 * kPieces);
         else
-          copy(a.ck_codes, a.ck_ld, 2 * S::kT, 1, 1);
+          copy_async8(slot8 + to, codes + col[c], n[c]);
       }
+      dy += dy_step;
+      if (dh) dh += dh_step;
+      if (H) h += h_step;
+      else codes += codes_step;
     }
+    ahead += step;
     copy_async_commit();
+    put = put + stage_bytes == DEPTH * stage_bytes ? 0 : put + stage_bytes;
   };
-  const auto staged = [&](int s, int c, int first) {
-    Row16<T> r;
+  const auto staged = [&](int c, int first, f2 (&v)[4]) {
+    Row8<T> r;
 #pragma unroll
-    for (int i = 0; i < S::kT; ++i) {
-      const uint4 w = lds128(place(s, c, first + i));
-      r.w[4 * i] = w.x;
-      r.w[4 * i + 1] = w.y;
-      r.w[4 * i + 2] = w.z;
-      r.w[4 * i + 3] = w.w;
+    for (int i = 0; i < kPieces; ++i) {
+      const uint4 q = lds128(slot16 + get + c * (S::kThread * threads) + (first + i) * 16 * threads);
+      r.w[4 * i] = q.x;
+      r.w[4 * i + 1] = q.y;
+      r.w[4 * i + 2] = q.z;
+      r.w[4 * i + 3] = q.w;
     }
-    return r;
+    unpack8<T>(r, v);
   };
-  // read a row ahead: they are one byte and one word
   uint32_t next_scale[NC];
   float next_rstd = 0.0f;
+  const float* rstds = a.rstd + blockIdx.x;
   const auto peek = [&](int64_t row) {
     if (row >= a.M) return;
-    next_rstd = a.rstd[row];
-    if (!H)
+    next_rstd = *rstds;
+    rstds += step;
+    if (!H) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        next_scale[c] = column(c) < a.H ? a.ck_scales[row * a.ck_lds + column(c) / kFp8Block] : kScaleOne;
+      for (int c = 0; c < NC; ++c) next_scale[c] = scales[static_cast<uint32_t>(col[c]) / kFp8Block];
+      scales += scales_step;
+    }
   };
 
   if (VEC)
-    for (int s = 0; s < DEPTH - 1; ++s) begin_copy(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+    for (int s = 0; s < DEPTH - 1; ++s) begin_copy();
   peek(blockIdx.x);
-  float w[16];   // in registers for the whole call where a thread has one chunk
-  if (NC == 1) load_weight16<VEC>(a.weight, a.weight_dtype, column(0), clamp16(a.H - column(0)), w);
-  int s = 0;
+  f2 w[4];   // in registers for the whole call where a thread has one chunk
+  if (NC == 1) load_weight8<VEC>(a.weight, a.weight_dtype, col[0], n[0], w);
   uint32_t turn = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1u) {
-    if (VEC) begin_copy(row + static_cast<int64_t>(DEPTH - 1) * gridDim.x, (s + DEPTH - 1) % kBufs);
-    uint32_t scale[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) scale[c] = next_scale[c];
+  for (int64_t row = blockIdx.x; row < a.M; row += step, turn ^= 1u) {
+    if (VEC) begin_copy();
+    float scale[NC];
     const float rstd = next_rstd;
-    peek(row + gridDim.x);
+    // a code times its scale is exact, so scale and rstd may be multiplied first
+#pragma unroll
+    for (int c = 0; c < NC; ++c) scale[c] = H ? rstd : fp8_scale(next_scale[c]) * rstd;
+    peek(row + step);
     if (VEC) copy_async_wait<VEC ? DEPTH - 1 : 0>();
-    float g[NC][16], xh[NC][16];
-    float sum = 0.0f;
+    f2 g[NC][4], xh[NC][4], part{0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = column(c);
-      const int n = clamp16(a.H - col);
-      if (VEC) {
-        unpack<T>(staged(s, c, 0), g[c]);
-        if (H)
-          unpack<T>(staged(s, c, 2 * S::kT), xh[c]);
+      if (VEC)
+        staged(c, 0, g[c]);
+      else
+        load8<T, false>(dy + col[c], n[c], g[c]);
+      if (H) {
+        if (VEC)
+          staged(c, 2 * kPieces, xh[c]);
         else
-          decode16(lds128(place(s, c, 2 * S::kT)), fp8_scale(scale[c]), xh[c]);
+          load8<T, false>(h + col[c], n[c], xh[c]);
       } else {
-        unpack<T>(load16<T, false>(static_cast<const T*>(a.dy) + row * a.lddy + col, n, false), g[c]);
-        if (H)
-          unpack<T>(load16<T, false>(static_cast<const T*>(a.h) + row * a.ldh + col, n, false), xh[c]);
-        else
-          decode16(load_codes16(a.ck_codes + row * a.ck_ld + col, n), fp8_scale(scale[c]), xh[c]);
+        decode8(VEC ? lds64(slot8 + get + c * (S::kThread * threads)) : load_codes8(codes + col[c], n[c]), scale[c], xh[c]);
       }
-      if (NC > 1) load_weight16<VEC>(a.weight, a.weight_dtype, col, n, w);
+      if (NC > 1) load_weight8<VEC>(a.weight, a.weight_dtype, col[c], n[c], w);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 4; ++i) {
         // columns that do not exist are 0, or NaN in a block whose scale is:
         // there the row's sum is NaN by those that do
-        xh[c][i] *= rstd;
-        dw[c][i] = fmaf(g[c][i], xh[c][i], dw[c][i]);
-        g[c][i] *= w[i];
-        sum = fmaf(g[c][i], xh[c][i], sum);
+        if (H) xh[c][i] = mul2(xh[c][i], f2{rstd, rstd});
+        dw[c][i] = fma2(g[c][i], xh[c][i], dw[c][i]);
+        g[c][i] = mul2(g[c][i], w[i]);
+        part = fma2(g[c][i], xh[c][i], part);
       }
     }
-    const float mean = cta_sum(sum, red[turn], warps) / static_cast<float>(a.H);
+    const float mean = cta_sum<true>(part.x + part.y, red[turn]) * inv_h;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = column(c);
-      const int n = clamp16(a.H - col);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) g[c][i] = rstd * fmaf(-xh[c][i], mean, g[c][i]);
+      f2 d[4];
       if (a.dh) {
-        float d[16];
-        unpack<T>(VEC ? staged(s, c, S::kT)
-                      : load16<T, false>(static_cast<const T*>(a.dh) + row * a.lddh + col, n, false), d);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[c][i] += d[i];
+        if (VEC)
+          staged(c, kPieces, d);
+        else
+          load8<T, false>(dh + col[c], n[c], d);
       }
-      store16<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx + col, n, wide, pack<T>(g[c]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g[c][i] = fma2(xh[c][i], f2{-mean, -mean}, g[c][i]);
+        g[c][i] = a.dh ? fma2(g[c][i], f2{rstd, rstd}, d[i]) : mul2(g[c][i], f2{rstd, rstd});
+      }
+      store8<T, VEC>(dx + col[c], n[c], pack8<T>(g[c]));
     }
-    s = s + 1 == kBufs ? 0 : s + 1;
+    dx += dx_step;
+    if (!VEC) {
+      dy += dy_step;
+      if (dh) dh += dh_step;
+      if (H) h += h_step;
+      else codes += codes_step;
+    }
+    get = get + stage_bytes == DEPTH * stage_bytes ? 0 : get + stage_bytes;
   }
   if (VEC) copy_async_wait<0>();
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t col = column(c);
-    const int n = clamp16(a.H - col);
-    float* p = a.partial + blockIdx.x * a.H + col;
-    if (n == 16 && a.H % 4 == 0) {   // every CTA's row of partial sums starts on 16 bytes
+    float* p = a.partial + blockIdx.x * a.H + col[c];
+    if (n[c] == 8 && a.H % 4 == 0) {   // every CTA's row of partial sums starts on 16 bytes
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<float4*>(p + i) = make_float4(dw[c][i], dw[c][i + 1], dw[c][i + 2], dw[c][i + 3]);
+      for (int i = 0; i < 4; i += 2)
+        *reinterpret_cast<float4*>(p + 2 * i) = make_float4(dw[c][i].x, dw[c][i].y, dw[c][i + 1].x, dw[c][i + 1].y);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = dw[c][i];
+      for (int i = 0; i < 8; ++i)
+        if (i < n[c]) p[i] = i & 1 ? dw[c][i >> 1].y : dw[c][i >> 1].x;
     }
   }
 }
@@ -264,6 +393,14 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int 
   }
 }
 
+// Threads and 8-column chunks per thread of the backward pass: at most 1024.
+void backward_shape(int64_t H, int* threads, int* nc) {
+  const int64_t chunks = (H + 7) / 8;
+  *nc = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
+  const int64_t t = (chunks + *nc - 1) / *nc;
+  *threads = static_cast<int>((t + 31) / 32 * 32);
+}
+
 // Threads and 16-column chunks per thread for H columns: at most 512 threads.
 void norm_shape(int64_t H, int* threads, int* nc) {
   const int64_t chunks = (H + 15) / 16;
@@ -280,7 +417,7 @@ cudaError_t launch_norm_t(const NormArgs& a, int threads, int vec, cudaStream_t 
 
 // Shared memory that a CTA's ring of rows may take: two CTAs per SM, else one.
 constexpr size_t kRingTwo = 112 * 1024, kRingOne = 226 * 1024;
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 1024;
 
 // The ring's depth for a stage of this size (0: no ring) and its bytes.
 int ring_depth(size_t stage, bool vec) { return !vec ? 0 : 4 * stage <= kRingTwo ? 4 : 2 * stage <= kRingOne ? 2 : 0; }
@@ -293,11 +430,11 @@ auto with_backward_kernel(int depth, F&& f) {
 }
 
 template <typename T, int NC, bool H>
-cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, int vec, int grid, cudaStream_t st) {
+cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, bool vec, int grid, cudaStream_t st) {
   const size_t stage = BackwardStage<T, NC, H>::bytes(threads);
-  const int depth = ring_depth(stage, vec != kVecNone);
+  const int depth = ring_depth(stage, vec);
   return with_backward_kernel<T, NC, H>(depth, [&](auto k) {
-    return launch_dependent(k, dim3(grid), threads, depth * stage, st, a, vec == kVec32);
+    return launch_dependent(k, dim3(grid), threads, depth * stage, st, a);
   });
 }
 
@@ -348,8 +485,8 @@ cudaError_t prepare_norm() {
 // their threads), no more than rows, and no more than rows of partial sums.
 int norm_backward_ctas(int64_t M, int64_t H, int sms) {
   int threads, nc;
-  norm_shape(H, &threads, &nc);
-  const int per_sm = threads <= 128 ? 3 : threads <= 256 ? 2 : 1;
+  backward_shape(H, &threads, &nc);
+  const int per_sm = threads <= 256 ? 3 : threads <= 512 ? 2 : 1;
   int64_t most = static_cast<int64_t>(per_sm) * sms;
   if (most > kNormMaxPartials) most = kNormMaxPartials;
   return static_cast<int>(M < most ? M : most);
@@ -357,13 +494,13 @@ int norm_backward_ctas(int64_t M, int64_t H, int sms) {
 
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, int grid, cudaStream_t st) {
   int threads, nc;
-  norm_shape(a.H, &threads, &nc);
+  backward_shape(a.H, &threads, &nc);
   const auto launch = [&](auto t, auto held) {
     using T = decltype(t);
     constexpr bool H = decltype(held)::value;
-    return nc == 1   ? launch_norm_backward_t<T, 1, H>(a, threads, vec, grid, st)
-           : nc == 2 ? launch_norm_backward_t<T, 2, H>(a, threads, vec, grid, st)
-                     : launch_norm_backward_t<T, 4, H>(a, threads, vec, grid, st);
+    return nc == 1   ? launch_norm_backward_t<T, 1, H>(a, threads, vec != kVecNone, grid, st)
+           : nc == 2 ? launch_norm_backward_t<T, 2, H>(a, threads, vec != kVecNone, grid, st)
+                     : launch_norm_backward_t<T, 4, H>(a, threads, vec != kVecNone, grid, st);
   };
   if (grid > 0) {
     const cudaError_t e = with_dtype(dtype, [&](auto t) {
