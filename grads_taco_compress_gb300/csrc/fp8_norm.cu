@@ -371,26 +371,26 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
 }
 
 // dw = the sum of the G rows of partial sums, in a fixed order: a CTA takes 32
-// columns, warp w adds rows w, w + 8, ..., and the 8 sums meet in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* partial, int G, int64_t H, float* dw) {
-  __shared__ float part[8][32];
+// columns, warp w adds rows w, w + 32, ..., and the 32 sums meet in order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* partial, int G, int64_t H, float* dw) {
+  __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   grid_launch_dependents();
   grid_dependency_wait();
   float s = 0.0f;
   if (col < H) {
-#pragma unroll 8
-    for (int g = warp; g < G; g += 8) s += partial[g * H + col];
+#pragma unroll 16
+    for (int g = warp; g < G; g += 32) s += partial[g * H + col];
   }
   part[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < H) {
-    s = part[0][lane];
+  // warp w: column w, one sum per lane
+  s = part[lane][warp];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) s += part[w][lane];
-    dw[col] = s;
-  }
+  for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(kFullMask, s, m);
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && c < H) dw[c] = s;
 }
 
 // Threads and 8-column chunks per thread of the backward pass: at most 1024.
@@ -508,7 +508,7 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, 
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32)), 256, 0, st,
+  return launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32)), 1024, 0, st,
                           static_cast<const float*>(a.partial), grid, a.H, a.dw);
 }
 
