@@ -86,22 +86,26 @@ taco_status check_apart(const Region* in, int nin, const Region* out, int nout, 
 }
 
 std::once_flag g_once[kMaxDevices];
-int g_sms[kMaxDevices];
+struct DeviceFacts {
+  int sms;
+  int clusters[9];   // [s]: clusters of s CTAs of the matrix product that run at once
+};
+DeviceFacts g_device[kMaxDevices];
 cudaError_t g_err[kMaxDevices];
 
-// SMs of the current device; sets the kernels' attributes on the first call.
-cudaError_t device_sms(int* sms) {
+// The current device's facts; sets the kernels' attributes on the first call.
+cudaError_t device_facts(const DeviceFacts** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(g_once[dev], [dev]() {
-    cudaError_t err = cudaDeviceGetAttribute(&g_sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t err = cudaDeviceGetAttribute(&g_device[dev].sms, cudaDevAttrMultiProcessorCount, dev);
     if (err == cudaSuccess) err = prepare_norm();
-    if (err == cudaSuccess) err = prepare_matmul();
+    if (err == cudaSuccess) err = prepare_matmul(g_device[dev].clusters);
     g_err[dev] = err;
   });
-  *sms = g_sms[dev];
+  *out = &g_device[dev];
   return g_err[dev];
 }
 
@@ -138,8 +142,8 @@ taco_status quantize_common(QuantizeArgs& a, int dtype, int vec, const Region* i
   TACO_TRY(check_apart(in, nin, out, 4));
   if (((a.M + 127) / 128) * ((a.K + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
   if (a.M == 0) return TACO_OK;
-  int sms = 0;
-  if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
+  const DeviceFacts* dev = nullptr;
+  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
   return done(launch_quantize(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
@@ -226,9 +230,9 @@ taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
     a.ck_ld = checkpoint->ld_codes;
     a.ck_lds = checkpoint->ld_scales;
   }
-  int sms = 0;
-  if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_norm(a, dtype, vec, sms, static_cast<cudaStream_t>(stream)));
+  const DeviceFacts* dev = nullptr;
+  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
+  return done(launch_norm(a, dtype, vec, dev->sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t taco_rms_norm_workspace_bytes(int64_t M, int64_t H) {
@@ -283,9 +287,9 @@ taco_status taco_rms_norm_fp8_backward(const void* dy, int64_t lddy, const taco_
   a.H = H;
   a.partial = static_cast<float*>(workspace);
   a.dw = dw;
-  int sms = 0;
-  if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_norm_backward(a, dtype, vec, norm_backward_ctas(M, H, sms), static_cast<cudaStream_t>(stream)));
+  const DeviceFacts* dev = nullptr;
+  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
+  return done(launch_norm_backward(a, dtype, vec, norm_backward_ctas(M, H, dev->sms), static_cast<cudaStream_t>(stream)));
 }
 
 taco_status taco_swiglu_fp8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int dtype, int64_t M,
@@ -406,9 +410,9 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   m.tma_add = vec_add != kVecNone && (ldadd * elem(dtype)) % 16 == 0;
   // a tensor map wants a row stride of 16 bytes even where there is one row
   m.tma_out = vec_out != kVecNone && (ldo * elem(dtype)) % 16 == 0;
-  int sms = 0;
-  if (device_sms(&sms) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_matmul(m, dtype, sms, static_cast<cudaStream_t>(stream)));
+  const DeviceFacts* dev = nullptr;
+  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
+  return done(launch_matmul(m, dtype, dev->sms, dev->clusters, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -96,15 +96,19 @@ __device__ __forceinline__ T load_staged(uint32_t addr) {
     return v;
   }
 }
-// v += the `left` (or COLS) elements of a row of `add`; vec: 16-byte aligned.
+// v += the `left` (or COLS) elements of a row of `add`; vec: rows of it start on
+// 16 bytes (and p on as many as COLS elements take, at most 16).
 template <typename T, int COLS>
 __device__ __forceinline__ void add_row(float* v, const T* p, int64_t left, bool vec) {
-  constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+  constexpr int kPer = COLS * static_cast<int>(sizeof(T)) < 16 ? COLS : 16 / static_cast<int>(sizeof(T));
   if (vec && left >= COLS) {
 #pragma unroll
     for (int i = 0; i < COLS; i += kPer) {
       alignas(16) T q[kPer];
-      *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(p + i);
+      if constexpr (kPer * sizeof(T) == 16)
+        *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(p + i);
+      else
+        *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(p + i);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) v[i + e] += to_f32(q[e]);
     }
@@ -112,6 +116,24 @@ __device__ __forceinline__ void add_row(float* v, const T* p, int64_t left, bool
 #pragma unroll
     for (int i = 0; i < COLS; ++i)
       if (i < left) v[i] += to_f32(p[i]);
+  }
+}
+
+// 4 consecutive outputs, of which `left` exist.
+template <typename T>
+__device__ __forceinline__ void store_row4(T* p, const float* v, int64_t left, bool vec) {
+  if (vec && left >= 4) {
+    alignas(16) T q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = from_f32<T>(v[i]);
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(q);
+    else
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(q);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = from_f32<T>(v[i]);
   }
 }
 
@@ -179,6 +201,10 @@ __device__ __forceinline__ void tma_load_2d_plain(uint32_t dst, const CUtensorMa
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+               :: "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1) : "memory");
 }
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -645,6 +671,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 // of a cluster, each of which reads its own part of the weights once. The
 // partial sums meet through distributed shared memory: every CTA adds the
 // parts of its tokens in the order of the splits and writes them.
+constexpr int kMaxSplits = 8;   // the portable cluster size
+
 template <int TT>
 struct Few {
   static constexpr uint32_t kW = 128 * kFp8Block, kX = TT * kFp8Block, kStage = kW + kX;
@@ -707,6 +735,9 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
   tc_fence_after();
   const uint32_t tmem = uniform(lds_u32(base + S::slot));
   grid_launch_dependents();
+  if (warp == 0 && lane == 0)   // while the preceding kernel drains: prefetches into L2 return nothing
+    for (int k = k0; k < k1 && k < k0 + S::kStages; ++k) tma_prefetch_2d(&maps.b, k * kFp8Block, static_cast<int>(n0));
+  __syncwarp();
   grid_dependency_wait();
 
   bool failed = false;
@@ -850,21 +881,32 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
   }
   __syncwarp();
   cluster_sync();   // every split's sums are written
-  if (warp >= 4 && !failed) {
-    const int64_t n = n0 + (warp - 4) * 32 + lane;
+  if (*abort_flag == 0u) {
+    // a warp takes a token at a time, 4 columns a lane, all splits' parts in flight
+    const int64_t n = n0 + 4 * lane, left = a.N - n;
     const int rows = static_cast<int>(a.M - m0 < TT ? a.M - m0 : TT);
-    for (int c = rank; c < rows; c += splits) {
-      float s = 0.0f;
-      for (int r = 0; r < splits; ++r) {
-        float v;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(v) : "r"(in_cta(base + S::stages + 4 * (c * 128 + (warp - 4) * 32 + lane), r)));
-        s = r == 0 ? v : s + v;
-      }
-      if (n < a.N) {
-        if (a.add) s += to_f32(static_cast<const T*>(a.add)[(m0 + c) * a.ldadd + n]);
-        static_cast<T*>(a.out)[(m0 + c) * a.ldo + n] = from_f32<T>(s);
-      }
+    uint32_t from[kMaxSplits];
+#pragma unroll
+    for (int r = 0; r < kMaxSplits; ++r) from[r] = in_cta(base + S::stages + 16 * lane, r < splits ? r : 0);
+#pragma unroll 2
+    for (int c = rank + splits * warp; c < rows; c += splits * (kThreads / 32)) {
+      float4 v[kMaxSplits];
+#pragma unroll
+      for (int r = 0; r < kMaxSplits; ++r)
+        if (r < splits)
+          asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w) : "r"(from[r] + 512 * c));
+      float s[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int r = 1; r < kMaxSplits; ++r)
+        if (r < splits) {
+          s[0] += v[r].x;
+          s[1] += v[r].y;
+          s[2] += v[r].z;
+          s[3] += v[r].w;
+        }
+      if (a.add) add_row<T, 4>(s, static_cast<const T*>(a.add) + (m0 + c) * a.ldadd + n, left, a.vec_add);
+      store_row4<T>(static_cast<T*>(a.out) + (m0 + c) * a.ldo + n, s, left, a.tma_out);
     }
   }
   tc_fence_before();
@@ -903,7 +945,26 @@ bool encode_out(EncodeTiled encode, CUtensorMap* map, const MatmulArgs& a, const
 
 }  // namespace
 
-cudaError_t prepare_matmul() {
+// Launch of `gx` x `gy` CTAs in clusters of `splits`.
+cudaLaunchConfig_t few_config(int splits, unsigned gx, unsigned gy, size_t smem, cudaStream_t st,
+                              cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(gx, gy);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+cudaError_t prepare_matmul(int* clusters) {
   cudaError_t e = cudaSuccess;
   const auto set = [&](auto k, uint32_t bytes) {
     if (e == cudaSuccess)
@@ -912,6 +973,8 @@ cudaError_t prepare_matmul() {
   };
   set(matmul_pair_kernel<__nv_bfloat16, 256>, Pair<256>::bytes);
   set(matmul_pair_kernel<__half, 256>, Pair<256>::bytes);
+  set(matmul_pair_kernel<__nv_bfloat16, 128>, Pair<128>::bytes);
+  set(matmul_pair_kernel<__half, 128>, Pair<128>::bytes);
   set(matmul_pair_kernel<float, 128>, Pair<128>::bytes);
   const auto few = [&](auto t) {
     using T = decltype(t);
@@ -923,6 +986,12 @@ cudaError_t prepare_matmul() {
   few(__nv_bfloat16{});
   few(__half{});
   few(float{});
+  // one CTA per SM in every form: the count is the same for all of them
+  for (int splits = 1; splits <= kMaxSplits && e == cudaSuccess; ++splits) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = few_config(splits, splits, 1, Few<128>::bytes, nullptr, attr);
+    e = cudaOccupancyMaxActiveClusters(&clusters[splits], matmul_few_kernel<__nv_bfloat16, 128>, &cfg);
+  }
   return e;
 }
 
@@ -948,36 +1017,37 @@ cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cuda
   if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, TT) ||
       !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, 128))
     return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128 * splits), static_cast<unsigned>((a.M + TT - 1) / TT));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Few<TT>::bytes;
-  cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  const cudaLaunchConfig_t cfg = few_config(splits, static_cast<unsigned>((a.N + 127) / 128 * splits),
+                                            static_cast<unsigned>((a.M + TT - 1) / TT), Few<TT>::bytes, st, attr);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_few_kernel<T, TT>, maps, a, splits);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, cudaStream_t st) {
+// Which kernel. Few rows (at most 128: one tile of tokens), or more whose 128 x
+// 128 tiles leave room for two CTAs a tile: K split over clusters, as many
+// splits as let all clusters run at once (clusters[s]: how many of s CTAs do).
+// Measured at N = K = 4096, bf16, against the pairs: 128 rows 8.0 and 13.5 us,
+// 256 rows 10.4 and 13.6, 384 rows (one CTA a tile) 15.7 and 14.1. Else pairs,
+// whose tiles are 128 columns wide where that still is one wave (fewer than
+// half of the pairs would have a tile of 256).
+cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st) {
   EncodeTiled encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   return with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    if (a.M > 128) return launch_pair<T, std::is_same<T, float>::value ? 128 : 256>(encode, a, sms, st);
-    const int64_t tiles_n = (a.N + 127) / 128, kb = (a.K + kFp8Block - 1) / kFp8Block;
-    int64_t splits = sms / tiles_n;
-    if (splits > kb) splits = kb;
-    if (splits > 8) splits = 8;
-    if (splits < 1) splits = 1;
-    const int s = static_cast<int>(splits);
+    const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
+    const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 127) / 128);
+    if (a.M > 128 && 2 * tiles > sms) {
+      if constexpr (std::is_same<T, float>::value) {
+        return launch_pair<T, 128>(encode, a, sms, st);
+      } else {
+        const int64_t narrow = ((a.M + 255) / 256) * ((a.N + 127) / 128);
+        return narrow <= sms / 2 ? launch_pair<T, 128>(encode, a, sms, st) : launch_pair<T, 256>(encode, a, sms, st);
+      }
+    }
+    int s = 1;
+    while (s < kMaxSplits && s < kb && tiles <= clusters[s + 1]) ++s;
     return a.M <= 16   ? launch_few<T, 16>(encode, a, s, st)
            : a.M <= 32 ? launch_few<T, 32>(encode, a, s, st)
            : a.M <= 64 ? launch_few<T, 64>(encode, a, s, st)

@@ -252,8 +252,9 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, 
 cudaError_t launch_swiglu(const SwigluArgs& a, int dtype, int vec, cudaStream_t st);
 cudaError_t launch_swiglu_backward(const SwigluBackwardArgs& a, int dtype, int vec, cudaStream_t st);
 cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, int vec, cudaStream_t st);
-cudaError_t prepare_matmul();
-cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, cudaStream_t st);
+// Fills clusters[1 .. 8]: how many clusters of that many CTAs run at once.
+cudaError_t prepare_matmul(int* clusters);
+cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
 cudaError_t matmul_fault(unsigned int* bits, bool clear);
 
 }  // namespace taco
