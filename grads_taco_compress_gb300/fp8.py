@@ -96,9 +96,15 @@ def _describe(t: Fp8Tensor, what: str, one_row_tile: int = 1) -> _Fp8Struct:
     """Checks an FP8 block tensor and describes it to the library. The scales
     of a single row have the same shape in both tilings: one_row_tile then."""
     codes, scales = t
-    shape, strides, sshape, sstrides = codes.shape, codes.stride(), scales.shape, scales.stride()
-    if len(shape) != 2 or len(sshape) != 2 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    shape, sshape = codes.shape, scales.shape
+    if len(shape) != 2 or len(sshape) != 2:
         raise ValueError(f"{what} must be 2-D uint8 codes and scales")
+    return _described(codes, scales, shape, sshape, codes.stride(), scales.stride(), what, one_row_tile)
+
+
+def _described(codes, scales, shape, sshape, strides, sstrides, what, one_row_tile=1) -> _Fp8Struct:
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{what} must be uint8 codes and scales")
     if not (codes.is_cuda and scales.is_cuda):
         raise ValueError(f"{what} must be CUDA tensors")
     rows, cols = shape
@@ -277,11 +283,12 @@ def taco_swiglu_fp8(gate_up: torch.Tensor, checkpoint: bool | Fp8Tensor = False,
 def _planes(ck: Fp8Tensor) -> tuple[_Fp8Struct, _Fp8Struct]:
     """Checks a gated activation's checkpoint and describes its two planes."""
     codes, scales = ck
-    if codes.dim() != 3 or scales.dim() != 3 or codes.shape[0] != 2 or scales.shape[0] != 2:
+    shape, sshape, strides, sstrides = codes.shape, scales.shape, codes.stride(), scales.stride()
+    if len(shape) != 3 or len(sshape) != 3 or shape[0] != 2 or sshape[0] != 2:
         raise ValueError("the checkpoint of a gated activation is [2, M, F]: gate, up")
-    g = _describe(Fp8Tensor(codes[0], scales[0]), "checkpoint")
-    return g, _Fp8Struct(codes.data_ptr() + codes.stride(0), scales.data_ptr() + scales.stride(0), g.ld_codes,
-                         g.ld_scales, g.rows, g.cols, g.tile_rows)
+    g = _described(codes, scales, shape[1:], sshape[1:], strides[1:], sstrides[1:], "checkpoint")
+    return g, _Fp8Struct(codes.data_ptr() + strides[0], scales.data_ptr() + sstrides[0], g.ld_codes, g.ld_scales,
+                         g.rows, g.cols, g.tile_rows)
 
 
 def taco_swiglu_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor, out: torch.Tensor | None = None,
