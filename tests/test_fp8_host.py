@@ -30,11 +30,19 @@ def lib():
     return tb.library()
 
 
+class Struct(ctypes.Structure):
+    """taco_fp8_tensor of taco.h."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
+                ("ld_scales", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("tile_rows", ctypes.c_int32)]
+
+
 def fp8(i, rows, cols, tile=1, **kw):
     d = dict(codes=i * A, scales=i * A + (A >> 1), ld_codes=-(-cols // 16) * 16,
              ld_scales=-(-(-(-cols // 128)) // 4) * 4, rows=rows, cols=cols, tile_rows=tile)
     d.update(kw)
-    return ctypes.byref(F._Fp8Struct(*(d[k] for k, _ in F._Fp8Struct._fields_)))
+    return ctypes.byref(Struct(*(d[k] for k, _ in Struct._fields_)))
 
 
 @no_gpu_only
@@ -176,6 +184,13 @@ def test_binding_refuses_what_is_not_on_the_gpu():
                  lambda: taco.taco_fp8_quantize(x, tile=64)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_fails_loudly_without_its_module(monkeypatch, tmp_path, lib):
+    monkeypatch.setattr(F, "BINDING_PATH", tmp_path / "missing.so")
+    monkeypatch.setattr(F, "_BINDING", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        taco.taco_fp8_quantize(torch.zeros(4, 256))
 
 
 def test_padding_of_a_new_tensor():
