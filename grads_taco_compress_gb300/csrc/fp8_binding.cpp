@@ -20,6 +20,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -135,17 +136,27 @@ Pair new_fp8_planes(int64_t planes, int64_t rows, int64_t cols, const at::Device
           empty_strided({planes, rows, kb}, {rows * lds, lds, 1}, at::kByte, device)};
 }
 
-void* stream_of(PyObject* handle, const at::Tensor& t) {
-  if (given(handle)) {
+// The device of `t` and the stream of the call (the current one, or the one
+// whose handle is given) made current for its length: what the call allocates
+// belongs to that stream, so that memory freed after the call (a workspace
+// above all) is not handed out on another one while the kernels still use it.
+class OnStream {
+ public:
+  OnStream(PyObject* handle, const at::Tensor& t) : device_(t.device()) {
+    if (!given(handle)) return;
     void* p = PyLong_AsVoidPtr(handle);
     if (!p && PyErr_Occurred()) {
       PyErr_Clear();
       refuse("stream must be a CUDA stream");
     }
-    return p;
+    stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), t.device().index()));
   }
-  return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
-}
+  void* handle() const { return c10::cuda::getCurrentCUDAStream().stream(); }
+
+ private:
+  c10::cuda::OptionalCUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard stream_;
+};
 
 struct Result {
   PyObject* tuple;
@@ -218,13 +229,14 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
       M = m.rows;
       K = m.cols;
     }
+    const OnStream on(v[6], x);
     std::optional<Pair> out, out_t;
     if (rows) out = given(v[4]) ? pair_of(v[4], "out") : new_fp8(M, K, tile, x.device());
     if (cols) out_t = given(v[5]) ? pair_of(v[5], "out_t") : new_fp8(K, M, tile, x.device());
     taco_fp8_tensor a{}, b{};
     if (out) a = describe(out->codes, out->scales, "out", tile);
     if (out_t) b = describe(out_t->codes, out_t->scales, "out_t", tile);
-    void* stream = stream_of(v[6], x);
+    void* stream = on.handle();
     const taco_status st = call([&] {
       return source ? taco_fp8_requantize(&from, out ? &a : nullptr, out_t ? &b : nullptr, stream)
                     : taco_fp8_quantize(m.p, m.dtype, M, K, m.ld, out ? &a : nullptr, out_t ? &b : nullptr, stream);
@@ -240,6 +252,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
     const at::Tensor& x = tensor(v[0], "x");
     const Matrix m = matrix(x, "x");
+    const OnStream on(v[8], x);
     const at::Tensor& weight = tensor(v[1], "weight");
     void* w = vector(weight, "weight", m.cols, false);
     const double eps = PyFloat_AsDouble(v[3]);
@@ -267,7 +280,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       ck = new_fp8(m.rows, m.cols, 1, x.device());
     taco_fp8_tensor cd{};
     if (ck) cd = describe(ck->codes, ck->scales, "checkpoint");
-    void* stream = stream_of(v[8], x);
+    void* stream = on.handle();
     const taco_status st = call([&] {
       return taco_rms_norm_fp8(m.p, m.ld, r.p, r.ld, w, dtype_of(weight.scalar_type()), m.dtype, m.rows, m.cols,
                                static_cast<float>(eps), ho.p, ho.ld, static_cast<float*>(rs), &yd, ck ? &cd : nullptr,
@@ -283,6 +296,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
     const at::Tensor& dy = tensor(v[0], "dy");
     const Matrix m = matrix(dy, "dy");
+    const OnStream on(v[8], dy);
     std::optional<Pair> ck;
     taco_fp8_tensor cd{};
     Matrix h, dh;
@@ -307,7 +321,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     } else {
       ws = empty_vector(static_cast<int64_t>(taco_rms_norm_workspace_bytes(m.rows, m.cols)), at::kByte, dy.device());
     }
-    void* stream = stream_of(v[8], dy);
+    void* stream = on.handle();
     const taco_status st = call([&] {
       return taco_rms_norm_fp8_backward(m.p, m.ld, ck ? &cd : nullptr, h.p, h.ld, w, dtype_of(weight.scalar_type()),
                                         static_cast<const float*>(rstd), dh.p, dh.ld, m.dtype, m.rows, m.cols, out.p,
@@ -325,6 +339,7 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Matrix m = matrix(x, "gate_up");
     if (m.cols < 2 || m.cols % 2) refuse("gate_up must have an even number of columns");
     const int64_t F = m.cols / 2;
+    const OnStream on(v[3], x);
     const Pair y = given(v[2]) ? pair_of(v[2], "out") : new_fp8(m.rows, F, 1, x.device());
     const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
     std::optional<Pair> ck;
@@ -340,7 +355,7 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
       u = describe(ck->codes, ck->scales, "checkpoint", 1, 3, 1);
     }
     const char* p = static_cast<const char*>(m.p);
-    void* stream = stream_of(v[3], x);
+    void* stream = on.handle();
     const taco_status st = call([&] {
       return taco_swiglu_fp8(p, m.ld, p ? p + F * x.element_size() : p, m.ld, m.dtype, m.rows, F, &yd, ck ? &g : nullptr,
                              ck ? &u : nullptr, stream);
@@ -355,6 +370,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 4, [&]() -> PyObject* {
     const at::Tensor& dy = tensor(v[0], "dy");
     const Matrix m = matrix(dy, "dy");
+    const OnStream on(v[3], dy);
     const Pair ck = pair_of(v[1], "checkpoint");
     if (ck.codes.dim() != 3 || ck.codes.size(0) != 2 || ck.scales.dim() != 3 || ck.scales.size(0) != 2)
       refuse("the checkpoint of a gated activation is [2, M, F]: gate, up");
@@ -363,7 +379,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const at::Tensor out = given(v[2]) ? tensor(v[2], "out") : empty_matrix(m.rows, 2 * m.cols, dy.scalar_type(), dy.device());
     const Matrix o = like(out, "out", m.rows, 2 * m.cols, m.dtype);
     char* p = static_cast<char*>(o.p);
-    void* stream = stream_of(v[3], dy);
+    void* stream = on.handle();
     const taco_status st = call([&] {
       return taco_swiglu_fp8_backward(m.p, m.ld, &g, &u, m.dtype, m.rows, m.cols, p, o.ld,
                                       p ? p + m.cols * dy.element_size() : p, o.ld, stream);
@@ -378,6 +394,7 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 6, [&]() -> PyObject* {
     const Pair a = pair_of(v[0], "a"), b = pair_of(v[1], "b");
     const taco_fp8_tensor ad = describe(a.codes, a.scales, "a"), bd = describe(b.codes, b.scales, "b");
+    const OnStream on(v[5], a.codes);
     at::Tensor out;
     Matrix add;
     if (given(v[2])) {
@@ -389,7 +406,7 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Matrix o = matrix(out, "out");
     if (o.rows != ad.rows || o.cols != bd.rows) refuse("out must have the rows of a and of b");
     if (given(v[4])) add = like(tensor(v[4], "add"), "add", o.rows, o.cols, o.dtype);
-    void* stream = stream_of(v[5], out);
+    void* stream = on.handle();
     const taco_status st = call([&] { return taco_matmul_fp8(&ad, &bd, add.p, add.ld, o.p, o.ld, o.dtype, stream); });
     if (st != TACO_OK) return PyLong_FromLong(st);
     return Result(1).add(out).tuple;
