@@ -1024,13 +1024,17 @@ cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cuda
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Which kernel. Few rows (at most 128: one tile of tokens), or more whose 128 x
-// 128 tiles leave room for two CTAs a tile: K split over clusters, as many
-// splits as let all clusters run at once (clusters[s]: how many of s CTAs do).
-// Measured at N = K = 4096, bf16, against the pairs: 128 rows 8.0 and 13.5 us,
-// 256 rows 10.4 and 13.6, 384 rows (one CTA a tile) 15.7 and 14.1. Else pairs,
-// whose tiles are 128 columns wide where that still is one wave (fewer than
-// half of the pairs would have a tile of 256).
+// Which kernel. Up to 64 rows: K split over clusters, as many splits as let all
+// clusters run at once (clusters[s]: how many clusters of s CTAs do). Above, a
+// block of 128 columns of K takes either kernel about 0.25 us, and the cluster's
+// barriers and sums cost it about 4 us more than a pair's epilogue: the split
+// pays where it takes kFewSaves blocks off each CTA. N = K = 4096, bf16: 128
+// rows (24 blocks less) 7.9 us split, 8.5 in pairs; 256 rows (16 less) 10.4 and
+// 9.0; 256 rows at K = 16384 (64 less) 24.0 and 33.2. Pairs take tiles 128
+// columns wide where that is one wave (256 rows: 9.0 us, 13.5 at 256 wide),
+// else 256 wide (1024 rows: 15.6 us, 18.5 at 128 wide); f32 always 128, whose
+// sum its epilogue can hold.
+constexpr int kFewSaves = 24;
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st) {
   EncodeTiled encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
@@ -1038,20 +1042,18 @@ cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* cl
     using T = decltype(t);
     const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
     const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 127) / 128);
-    if (a.M > 128 && 2 * tiles > sms) {
-      if constexpr (std::is_same<T, float>::value) {
-        return launch_pair<T, 128>(encode, a, sms, st);
-      } else {
-        const int64_t narrow = ((a.M + 255) / 256) * ((a.N + 127) / 128);
-        return narrow <= sms / 2 ? launch_pair<T, 128>(encode, a, sms, st) : launch_pair<T, 256>(encode, a, sms, st);
-      }
-    }
     int s = 1;
     while (s < kMaxSplits && s < kb && tiles <= clusters[s + 1]) ++s;
-    return a.M <= 16   ? launch_few<T, 16>(encode, a, s, st)
-           : a.M <= 32 ? launch_few<T, 32>(encode, a, s, st)
-           : a.M <= 64 ? launch_few<T, 64>(encode, a, s, st)
-                       : launch_few<T, 128>(encode, a, s, st);
+    if (a.M <= 16) return launch_few<T, 16>(encode, a, s, st);
+    if (a.M <= 32) return launch_few<T, 32>(encode, a, s, st);
+    if (a.M <= 64) return launch_few<T, 64>(encode, a, s, st);
+    if (kb - (kb + s - 1) / s >= kFewSaves) return launch_few<T, 128>(encode, a, s, st);
+    if constexpr (std::is_same<T, float>::value) {
+      return launch_pair<T, 128>(encode, a, sms, st);
+    } else {
+      const int64_t narrow = ((a.M + 255) / 256) * ((a.N + 127) / 128);
+      return narrow <= sms / 2 ? launch_pair<T, 128>(encode, a, sms, st) : launch_pair<T, 256>(encode, a, sms, st);
+    }
   });
 }
 
