@@ -237,7 +237,7 @@ taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
 
 size_t taco_rms_norm_workspace_bytes(int64_t M, int64_t H) {
   if (M < 0 || H < 1 || H > kMaxNormColumns) return 0;
-  const int64_t rows = M < kNormMaxPartials ? (M < 1 ? 1 : M) : kNormMaxPartials;
+  const int64_t most = norm_max_partials(H), rows = M < 1 ? 1 : M < most ? M : most;
   return static_cast<size_t>(rows) * static_cast<size_t>(H) * sizeof(float);
 }
 

@@ -275,14 +275,19 @@ struct Divider {
   __device__ __forceinline__ uint64_t quotient(uint64_t n) const { return d == 1 ? n : __umul64hi(n, magic); }
 };
 
+// Sum over a warp, the same in every lane.
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
+  return v;
+}
 // Sum over the CTA's warps, added in the same order in every thread. `red`
 // holds 32 floats, zero beyond the warps, and must not be the buffer of the
 // call before (a thread may still be reading that one). WIDE: more than 16
 // warps may take part.
 template <bool WIDE>
 __device__ __forceinline__ float cta_sum(float v, float* red) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
+  v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = red[threadIdx.x & (WIDE ? 31 : 15)];

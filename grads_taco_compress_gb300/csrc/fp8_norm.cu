@@ -20,30 +20,38 @@ namespace taco {
 
 namespace {
 
-template <typename T, int NC, bool VEC>
+//
+// WARP: rows of at most 512 columns, one to a warp, kWarpRows to a CTA (65536
+// rows of 512: 67 us with a CTA of one warp a row, 42 us so).
+constexpr int kWarpRows = 8;
+
+template <typename T, int NC, bool VEC, bool WARP>
 __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
   __shared__ float red[32];
   const int lane8 = threadIdx.x & 7;
-  if (threadIdx.x < 32 && threadIdx.x >= blockDim.x >> 5) red[threadIdx.x] = 0.0f;
+  const uint32_t slot = WARP ? threadIdx.x & 31 : threadIdx.x;   // place in the row
+  const uint32_t threads = WARP ? 32 : blockDim.x;
+  if (!WARP && threadIdx.x < 32 && threadIdx.x >= blockDim.x >> 5) red[threadIdx.x] = 0.0f;
   grid_launch_dependents();
   grid_dependency_wait();
-  const int64_t row = blockIdx.x;
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= a.M) return;   // whole warps
   Row16<T> h[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+    const int64_t col = 16 * (static_cast<int64_t>(slot) + c * threads);
     h[c] = load16<T, VEC>(static_cast<const T*>(a.x) + row * a.ldx + col, clamp16(a.H - col), wide);
   }
   if (a.residual) {
     Row16<T> r[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      const int64_t col = 16 * (static_cast<int64_t>(slot) + c * threads);
       r[c] = load16<T, VEC>(static_cast<const T*>(a.residual) + row * a.ldr + col, clamp16(a.H - col), wide);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+      const int64_t col = 16 * (static_cast<int64_t>(slot) + c * threads);
       float x[16], y[16];
       unpack<T>(h[c], x);
       unpack<T>(r[c], y);
@@ -61,12 +69,12 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a, bool wide) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
   }
-  sum = cta_sum<false>(sum, red);
+  sum = WARP ? warp_sum(sum) : cta_sum<false>(sum, red);
   const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.eps);
-  if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+  if (a.rstd && slot == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int64_t col = 16 * (static_cast<int64_t>(threadIdx.x) + c * blockDim.x);
+    const int64_t col = 16 * (static_cast<int64_t>(slot) + c * threads);
     const int n = clamp16(a.H - col);
     float v[16], w[16];
     unpack<T>(h[c], v);
@@ -411,20 +419,30 @@ void norm_shape(int64_t H, int* threads, int* nc) {
 
 template <typename T, int NC>
 cudaError_t launch_norm_t(const NormArgs& a, int threads, int vec, cudaStream_t st) {
-  return launch_dependent(vec ? norm_kernel<T, NC, true> : norm_kernel<T, NC, false>,
+  if (NC == 1 && threads == 32)
+    return launch_dependent(vec ? norm_kernel<T, 1, true, true> : norm_kernel<T, 1, false, true>,
+                            dim3(static_cast<unsigned>((a.M + kWarpRows - 1) / kWarpRows)), 32 * kWarpRows, 0, st, a,
+                            vec == kVec32);
+  return launch_dependent(vec ? norm_kernel<T, NC, true, false> : norm_kernel<T, NC, false, false>,
                           dim3(static_cast<unsigned>(a.M)), threads, 0, st, a, vec == kVec32);
 }
 
-// Shared memory that a CTA's ring of rows may take: two CTAs per SM, else one.
-constexpr size_t kRingTwo = 112 * 1024, kRingOne = 226 * 1024;
-constexpr int kMaxThreads = 1024;
+// CTAs of the backward pass that an SM holds at 64 registers a thread.
+int backward_ctas_per_sm(int threads) { return 1024 / threads < 16 ? 1024 / threads : 16; }
 
-// The ring's depth for a stage of this size (0: no ring) and its bytes.
-int ring_depth(size_t stage, bool vec) { return !vec ? 0 : 4 * stage <= kRingTwo ? 4 : 2 * stage <= kRingOne ? 2 : 0; }
+// Shared memory that the rings of an SM's CTAs may take together, and the
+// ring's depth for a stage of this size (0: no ring).
+constexpr size_t kRingRoom = 222 * 1024;
+constexpr int kMaxDepth = 4;
+int ring_depth(size_t stage, int per_sm, bool vec) {
+  const size_t depth = kRingRoom / per_sm / stage;
+  return !vec || depth < 2 ? 0 : depth < kMaxDepth ? static_cast<int>(depth) : kMaxDepth;
+}
 
 template <typename T, int NC, bool H, typename F>
 auto with_backward_kernel(int depth, F&& f) {
   return depth == 4   ? f(norm_backward_kernel<T, NC, 4, H>)
+         : depth == 3 ? f(norm_backward_kernel<T, NC, 3, H>)
          : depth == 2 ? f(norm_backward_kernel<T, NC, 2, H>)
                       : f(norm_backward_kernel<T, NC, 0, H>);
 }
@@ -432,7 +450,7 @@ auto with_backward_kernel(int depth, F&& f) {
 template <typename T, int NC, bool H>
 cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, bool vec, int grid, cudaStream_t st) {
   const size_t stage = BackwardStage<T, NC, H>::bytes(threads);
-  const int depth = ring_depth(stage, vec);
+  const int depth = ring_depth(stage, backward_ctas_per_sm(threads), vec);
   return with_backward_kernel<T, NC, H>(depth, [&](auto k) {
     return launch_dependent(k, dim3(grid), threads, depth * stage, st, a);
   });
@@ -441,13 +459,12 @@ cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, bool 
 template <typename T, int NC, bool H>
 cudaError_t prepare_backward_t() {
   cudaError_t e = cudaSuccess;
-  for (int depth : {2, 4})
+  for (int depth = 2; depth <= kMaxDepth; ++depth)
     if (e == cudaSuccess)
       e = with_backward_kernel<T, NC, H>(depth, [&](auto k) {
-        const size_t most = depth * BackwardStage<T, NC, H>::bytes(kMaxThreads);
-        const size_t room = depth == 4 ? kRingTwo : kRingOne;
+        const size_t most = depth * BackwardStage<T, NC, H>::bytes(1024);
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(most < room ? most : room));
+                                    static_cast<int>(most < kRingRoom ? most : kRingRoom));
       });
   return e;
 }
@@ -481,14 +498,16 @@ cudaError_t prepare_norm() {
   return e;
 }
 
-// CTAs of the backward pass: as many as stay resident (3, 2 or 1 per SM by
-// their threads), no more than rows, and no more than rows of partial sums.
+int64_t norm_max_partials(int64_t H) { return H >= 2048 ? 512 : H >= 512 ? 512 * 2048 / H : 2048; }
+
+// CTAs of the backward pass: as many as stay resident, no more than rows, and
+// no more than rows of partial sums.
 int norm_backward_ctas(int64_t M, int64_t H, int sms) {
   int threads, nc;
   backward_shape(H, &threads, &nc);
-  const int per_sm = threads <= 256 ? 3 : threads <= 512 ? 2 : 1;
-  int64_t most = static_cast<int64_t>(per_sm) * sms;
-  if (most > kNormMaxPartials) most = kNormMaxPartials;
+  int64_t most = static_cast<int64_t>(backward_ctas_per_sm(threads)) * sms;
+  const int64_t partials = norm_max_partials(H);
+  if (most > partials) most = partials;
   return static_cast<int>(M < most ? M : most);
 }
 

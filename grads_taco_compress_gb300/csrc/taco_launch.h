@@ -244,8 +244,9 @@ struct MatmulArgs {
 };
 
 cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st);
-// Most CTAs, and so rows of partial sums, of the norm's backward pass.
-constexpr int64_t kNormMaxPartials = 512;
+// Most CTAs, and so rows of partial sums, of the norm's backward pass on rows of
+// H (512 at 2048 columns and more, up to 2048 of shorter rows).
+int64_t norm_max_partials(int64_t H);
 cudaError_t prepare_norm();
 int norm_backward_ctas(int64_t M, int64_t H, int sms);
 cudaError_t launch_norm_backward(const NormBackwardArgs& a, int dtype, int vec, int grid, cudaStream_t st);
