@@ -172,19 +172,137 @@ __device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t*
           make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   }
 }
+// ------------------------------------------- rows that start anywhere ----
+// The W words of a lane's consecutive elements at p, of which n exist (the
+// others read as zero), through aligned 16-byte loads and a shift. Every load
+// holds at least one byte of an element that exists.
+template <typename T, int W>
+__device__ __forceinline__ void load_shifted(const T* p, int n, uint32_t (&w)[W]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint32_t s = static_cast<uint32_t>(at & 15);
+  const uint4* from = reinterpret_cast<const uint4*>(at - s);
+  const int bytes = n ? static_cast<int>(s) + n * static_cast<int>(sizeof(T)) : 0;
+  uint32_t v[W + 4];
+#pragma unroll
+  for (int j = 0; j <= W / 4; ++j) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (16 * j < bytes) q = from[j];
+    v[4 * j] = q.x;
+    v[4 * j + 1] = q.y;
+    v[4 * j + 2] = q.z;
+    v[4 * j + 3] = q.w;
+  }
+  if (s & 8) {
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) v[i] = v[i + 2];
+  }
+  if (s & 4) {
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) v[i] = v[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    w[i] = sizeof(T) == 4 ? v[i] : __funnelshift_r(v[i], v[i + 1], 8 * (s & 2));
+    // elements beyond the row are zero
+    if (sizeof(T) == 4) {
+      if (i >= n) w[i] = 0u;
+    } else {
+      if (2 * i >= n) w[i] = 0u;
+      else if (2 * i + 1 >= n) w[i] &= 0xffffu;
+    }
+  }
+}
+
+// Writes the W words of each lane of a converged warp, whose lanes hold
+// consecutive elements (n of a lane's exist; a lane after a partial one has
+// none): whole aligned 16-byte pieces, each by the lane in whose place it
+// starts, with the end of the lane before; what a piece at either end of the
+// warp or of the row lacks goes element by element.
+template <typename T, int W>
+__device__ __forceinline__ void store_shifted(T* p, int n, const uint32_t (&w)[W]) {
+  constexpr int kEs = sizeof(T), kPer = 16 / kEs, kElems = 4 * W / kEs;
+  const int lane = threadIdx.x & 31;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint32_t s = static_cast<uint32_t>(at & 15);   // the same in every lane
+  const int before = static_cast<int>(s) / kEs;        // elements of the first piece that are the last lane's
+  uint32_t v[W + 8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_up_sync(kFullMask, w[W - 4 + i], 1);
+  const int n_before = __shfl_up_sync(kFullMask, n, 1);
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[4 + i] = w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[4 + W + i] = 0u;
+  // shift by the 16 - s bytes in front of the first piece
+  const uint32_t d = 16u - s;
+  if (d & 16) {
+#pragma unroll
+    for (int i = 0; i < W + 4; ++i) v[i] = v[i + 4];
+  }
+  if (d & 8) {
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) v[i] = v[i + 2];
+  }
+  if (d & 4) {
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) v[i] = v[i + 1];
+  }
+  if (kEs == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 8 * (d & 2));
+  }
+  T* first = reinterpret_cast<T*>(at - s);
+#pragma unroll
+  for (int j = 0; j < W / 4; ++j) {
+    const auto exists = [&](int e) {   // e: element of the pieces, counted from the first one's start
+      const int own = e - before;
+      return own >= 0 ? own < n : lane > 0 && kElems + own < n_before;
+    };
+    if (exists(j * kPer) && exists(j * kPer + kPer - 1)) {
+      *reinterpret_cast<uint4*>(first + j * kPer) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (exists(j * kPer + k)) {
+          const uint32_t word = v[4 * j + k * kEs / 4];
+          if (kEs == 4)
+            reinterpret_cast<uint32_t*>(first)[j * kPer + k] = word;
+          else
+            reinterpret_cast<uint16_t*>(first)[j * kPer + k] = static_cast<uint16_t>(word >> (16 * (k & 1)));
+        }
+    }
+  }
+  if (lane == 31) {   // the end of the last lane starts no piece of the warp
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int e = kElems - kPer + k;
+      if (e >= kElems - before && e < n) {
+        const uint32_t word = w[e * kEs / 4];
+        if (kEs == 4)
+          reinterpret_cast<uint32_t*>(p)[e] = word;
+        else
+          reinterpret_cast<uint16_t*>(p)[e] = static_cast<uint16_t>(word >> (16 * (e & 1)));
+      }
+    }
+  }
+}
+
 // The elements of 16 consecutive columns, of which n (0 .. 16) exist; the
-// others read as zero. VEC: p is 16-byte aligned, and 32-byte aligned if wide.
+// others read as zero. VEC: p is 16-byte aligned, and 32-byte aligned if wide;
+// without it a store takes whole warps on consecutive columns.
 template <typename T, bool VEC>
 __device__ __forceinline__ Row16<T> load16(const T* p, int n, bool wide) {
   Row16<T> r;
   if (VEC && n == 16) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) load_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
-  } else {
+  } else if constexpr (VEC) {   // the end of a row
     float v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
     r = pack<T>(v);
+  } else {
+    load_shifted(p, n, r.w);
   }
   return r;
 }
@@ -193,12 +311,14 @@ __device__ __forceinline__ void store16(T* p, int n, bool wide, const Row16<T>& 
   if (VEC && n == 16) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) store_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
-  } else {
+  } else if constexpr (VEC) {
     float v[16];
     unpack<T>(r, v);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (i < n) p[i] = from_f32<T>(v[i]);
+  } else {
+    store_shifted(p, n, r.w);
   }
 }
 // Codes of 16 consecutive columns: rows of codes start at multiples of 16
@@ -237,9 +357,13 @@ __device__ __forceinline__ void load_vector16(const T* p, int n, float (&v)[16])
     for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
       *reinterpret_cast<uint4*>(r.w + 4 * i) = *reinterpret_cast<const uint4*>(p + 4 * i * (4 / sizeof(T)));
     unpack<T>(r, v);
-  } else {
+  } else if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+  } else {
+    Row16<T> r;
+    load_shifted(p, n, r.w);
+    unpack<T>(r, v);
   }
 }
 template <bool VEC>

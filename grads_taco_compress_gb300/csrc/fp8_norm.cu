@@ -132,15 +132,17 @@ __device__ __forceinline__ void store8(T* p, int n, const Row8<T>& r) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
       *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
-  } else {
+  } else if constexpr (VEC) {
     f2 v[4];
     unpack8<T>(r, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = from_f32<T>(i & 1 ? v[i >> 1].y : v[i >> 1].x);
+  } else {
+    store_shifted(p, n, r.w);
   }
 }
-// 8 entries of a vector or row, one by one where it is not aligned.
+// 8 entries of a vector or row.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, int n, f2 (&v)[4]) {
   Row8<T> r;
@@ -148,12 +150,10 @@ __device__ __forceinline__ void load8(const T* p, int n, f2 (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
       *reinterpret_cast<uint4*>(r.w + 4 * i) = *reinterpret_cast<const uint4*>(p + 4 * i);
-    unpack8<T>(r, v);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] = f2{2 * i < n ? to_f32(p[2 * i]) : 0.0f, 2 * i + 1 < n ? to_f32(p[2 * i + 1]) : 0.0f};
+    load_shifted(p, n, r.w);
   }
+  unpack8<T>(r, v);
 }
 template <bool VEC>
 __device__ __forceinline__ void load_weight8(const void* w, int dtype, int64_t col, int n, f2 (&v)[4]) {
@@ -172,6 +172,7 @@ __device__ __forceinline__ void decode8(uint2 c, float s, f2 (&v)[4]) {
   v[3] = mul2(e4m3x2_to_f2(c.y >> 16), ss);
 }
 __device__ __forceinline__ uint2 load_codes8(const uint8_t* p, int n) {
+  if (n == 8) return *reinterpret_cast<const uint2*>(p);
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
   const uint32_t threads = blockDim.x, step = gridDim.x;
 
   // Everything that does not change from row to row: this thread's columns and
-  // how many exist (columns beyond the row read from its start, zero bytes),
-  // its byte offsets in a row, and its place in a stage of the ring.
+  // how many exist (copies of none read zero bytes at the row's start), and its
+  // place in a stage of the ring.
   int64_t col[NC];
   int n[NC];
 #pragma unroll
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
     col[c] = 8 * (static_cast<int64_t>(threadIdx.x) + c * threads);
     const int64_t left = a.H - col[c];
     n[c] = left < 0 ? 0 : left > 8 ? 8 : static_cast<int>(left);
-    if (n[c] == 0) col[c] = 0;
+    if (VEC && n[c] == 0) col[c] = 0;
   }
   const uint32_t stage_bytes = NC * S::kThread * threads;
   const uint32_t slot16 = smem_u32(ring) + 16 * threadIdx.x;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
     rstds += step;
     if (!H) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) next_scale[c] = scales[static_cast<uint32_t>(col[c]) / kFp8Block];
+      for (int c = 0; c < NC; ++c) next_scale[c] = scales[n[c] ? static_cast<uint32_t>(col[c]) / kFp8Block : 0u];
       scales += scales_step;
     }
   };

@@ -73,11 +73,13 @@ __global__ void __launch_bounds__(kThreads, backward_ctas<T>()) swiglu_backward_
   grid_launch_dependents();
   grid_dependency_wait();
   const int n = clamp16(a.F - col);
-  if (row >= a.M || n == 0) return;
+  if (row >= a.M || (VEC && n == 0)) return;   // unaligned rows are stored by whole warps
   const Row16<T> dr = load16<T, VEC>(static_cast<const T*>(a.dy) + row * a.lddy + col, n, wide);
   const uint4 gc = load_codes16(a.g_codes + row * a.g_ld + col, n);
   const uint4 uc = load_codes16(a.u_codes + row * a.u_ld + col, n);
-  const float gs = fp8_scale(a.g_scales[row * a.g_lds + k]), us = fp8_scale(a.u_scales[row * a.u_lds + k]);
+  const bool any = VEC || n > 0;
+  const float gs = any ? fp8_scale(a.g_scales[row * a.g_lds + k]) : 1.0f;
+  const float us = any ? fp8_scale(a.u_scales[row * a.u_lds + k]) : 1.0f;
   float d[16], g[16], u[16];
   unpack<T>(dr, d);
   decode16(gc, gs, g);
