@@ -22,6 +22,16 @@
 //              tcgen05.cp 32x128b spreads over the tensor memory;
 //   warps 4-7  epilogue: lane = row, tensor memory to registers to C.
 // Every wait is bounded in time with a CTA-wide abort flag.
+//
+// Measured (twice the measured bf16 rate of a library product is 3.94 PFLOP/s):
+// 16384 x 4096 x 3584 to bf16 135 us, 3.56 PFLOP/s, tensor pipe 79% active, and
+// 160 us (3.0 PFLOP/s) in a second-long loop under the power limit; the MMAs
+// without copies 120 us, the copies without MMAs 89 us: both go through shared
+// memory, 32 KB in and 32 KB or more out a block of 128 columns. 1600 x 4096 x
+// 8190 to f32 with add 54 us, 2.0 PFLOP/s, pipe 48%: a tile 128 columns wide
+// moves a third more bytes a product, and 224 tiles are 2.95 waves of pairs.
+// Few rows: 8 x 4096 x 4096 5.5 us, from launch to the last store of which the
+// weights' 16.8 MB would take 2.5; 1 x 16384 x 4096 13.5 us, 5.0 TB/s.
 
 #include "fp8_block.cuh"
 #include "tcgen05.cuh"

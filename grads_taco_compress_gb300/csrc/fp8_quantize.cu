@@ -10,6 +10,12 @@
 // magnitudes of the columns meet in shared memory; the transposed codes go
 // through it too, 4 rows of a column to a word, so that they leave as whole
 // 128-byte rows.
+//
+// Measured (a plain copy: 6.7 TB/s): rows of 8192 x 4096 bf16 15.4 us, 6.5 TB/s;
+// rows and transpose from one read 26.4 us, 5.1 TB/s, 59% of the issue slots;
+// the transpose of 8192 x 1600 codes 13.7 us, 63% of the issue slots at 1.8
+// waves of CTAs: every code is decoded twice, for the maximum and for its new
+// block.
 
 #include "fp8_block.cuh"
 
