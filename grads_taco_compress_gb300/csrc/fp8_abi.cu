@@ -142,8 +142,6 @@ taco_status quantize_common(QuantizeArgs& a, int dtype, int vec, const Region* i
   TACO_TRY(check_apart(in, nin, out, 4));
   if (((a.M + 127) / 128) * ((a.K + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
   if (a.M == 0) return TACO_OK;
-  const DeviceFacts* dev = nullptr;
-  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
   return done(launch_quantize(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
@@ -230,9 +228,7 @@ taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
     a.ck_ld = checkpoint->ld_codes;
     a.ck_lds = checkpoint->ld_scales;
   }
-  const DeviceFacts* dev = nullptr;
-  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_norm(a, dtype, vec, dev->sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_norm(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
 size_t taco_rms_norm_workspace_bytes(int64_t M, int64_t H) {
@@ -289,7 +285,8 @@ taco_status taco_rms_norm_fp8_backward(const void* dy, int64_t lddy, const taco_
   a.dw = dw;
   const DeviceFacts* dev = nullptr;
   if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
-  return done(launch_norm_backward(a, dtype, vec, norm_backward_ctas(M, H, dev->sms), static_cast<cudaStream_t>(stream)));
+  const int grid = norm_backward_ctas(M, H, dev->sms);
+  return done(launch_norm_backward(a, dtype, vec, grid, static_cast<cudaStream_t>(stream)));
 }
 
 taco_status taco_swiglu_fp8(const void* gate, int64_t ldg, const void* up, int64_t ldu, int dtype, int64_t M,

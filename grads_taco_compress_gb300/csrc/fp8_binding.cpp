@@ -56,7 +56,8 @@ struct Matrix {
 Matrix matrix(const at::Tensor& t, const char* what) {
   Matrix m;
   m.dtype = dtype_of(t.scalar_type());
-  if (!t.is_cuda() || m.dtype < 0 || t.dim() != 2) refuse(std::string(what) + " must be a 2-D bf16, f16 or f32 CUDA tensor");
+  if (!t.is_cuda() || m.dtype < 0 || t.dim() != 2)
+    refuse(std::string(what) + " must be a 2-D bf16, f16 or f32 CUDA tensor");
   m.rows = t.size(0);
   m.cols = t.size(1);
   if (m.cols > 1 && t.stride(1) != 1) refuse(std::string(what) + " must have contiguous columns");
@@ -77,7 +78,8 @@ Matrix like(const at::Tensor& t, const char* what, int64_t rows, int64_t cols, i
 void* vector(const at::Tensor& t, const char* what, int64_t n, bool f32) {
   if (!t.is_cuda() || dtype_of(t.scalar_type()) < 0 || t.dim() != 1 || t.size(0) != n || !t.is_contiguous() ||
       (f32 && t.scalar_type() != at::kFloat))
-    refuse(std::string(what) + " must be a contiguous " + (f32 ? "f32 " : "") + "CUDA tensor [" + std::to_string(n) + "]");
+    refuse(std::string(what) + " must be a contiguous " + (f32 ? "f32 " : "") + "CUDA tensor [" + std::to_string(n) +
+           "]");
   return t.data_ptr();
 }
 
@@ -86,7 +88,8 @@ void* vector(const at::Tensor& t, const char* what, int64_t n, bool f32) {
 // one_row_tile then.
 taco_fp8_tensor describe(const at::Tensor& codes, const at::Tensor& scales, const char* what, int one_row_tile = 1,
                          int dims = 2, int64_t plane = 0) {
-  if (codes.dim() != dims || scales.dim() != dims || codes.scalar_type() != at::kByte || scales.scalar_type() != at::kByte)
+  if (codes.dim() != dims || scales.dim() != dims || codes.scalar_type() != at::kByte ||
+      scales.scalar_type() != at::kByte)
     refuse(std::string(what) + " must be " + std::to_string(dims) + "-D uint8 codes and scales");
   if (!codes.is_cuda() || !scales.is_cuda()) refuse(std::string(what) + " must be CUDA tensors");
   const int r = dims - 2, c = dims - 1;
@@ -115,7 +118,8 @@ Pair pair_of(PyObject* o, const char* what) {
   return {tensor(PyTuple_GET_ITEM(o, 0), what), tensor(PyTuple_GET_ITEM(o, 1), what)};
 }
 
-at::Tensor empty_strided(at::IntArrayRef shape, at::IntArrayRef strides, at::ScalarType type, const at::Device& device) {
+at::Tensor empty_strided(at::IntArrayRef shape, at::IntArrayRef strides, at::ScalarType type,
+                         const at::Device& device) {
   return at::empty_strided(shape, strides, at::TensorOptions().dtype(type).device(device));
 }
 at::Tensor empty_matrix(int64_t rows, int64_t cols, at::ScalarType type, const at::Device& device) {
@@ -310,7 +314,8 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     void* w = vector(weight, "weight", m.cols, false);
     void* rstd = vector(tensor(v[3], "rstd"), "rstd", m.rows, true);
     if (given(v[4])) dh = like(tensor(v[4], "dh"), "dh", m.rows, m.cols, m.dtype);
-    const at::Tensor dx = given(v[5]) ? tensor(v[5], "dx") : empty_matrix(m.rows, m.cols, dy.scalar_type(), dy.device());
+    const at::Tensor dx =
+        given(v[5]) ? tensor(v[5], "dx") : empty_matrix(m.rows, m.cols, dy.scalar_type(), dy.device());
     const Matrix out = like(dx, "dx", m.rows, m.cols, m.dtype);
     const at::Tensor dw = given(v[6]) ? tensor(v[6], "dw") : empty_vector(m.cols, at::kFloat, dy.device());
     void* dwp = vector(dw, "dw", m.cols, true);
@@ -357,8 +362,8 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const char* p = static_cast<const char*>(m.p);
     void* stream = on.handle();
     const taco_status st = call([&] {
-      return taco_swiglu_fp8(p, m.ld, p ? p + F * x.element_size() : p, m.ld, m.dtype, m.rows, F, &yd, ck ? &g : nullptr,
-                             ck ? &u : nullptr, stream);
+      return taco_swiglu_fp8(p, m.ld, p ? p + F * x.element_size() : p, m.ld, m.dtype, m.rows, F, &yd,
+                             ck ? &g : nullptr, ck ? &u : nullptr, stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
     return Result(4).add(std::optional<Pair>(y)).add(ck).tuple;
@@ -376,7 +381,8 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
       refuse("the checkpoint of a gated activation is [2, M, F]: gate, up");
     const taco_fp8_tensor g = describe(ck.codes, ck.scales, "checkpoint", 1, 3, 0);
     const taco_fp8_tensor u = describe(ck.codes, ck.scales, "checkpoint", 1, 3, 1);
-    const at::Tensor out = given(v[2]) ? tensor(v[2], "out") : empty_matrix(m.rows, 2 * m.cols, dy.scalar_type(), dy.device());
+    const at::Tensor out =
+        given(v[2]) ? tensor(v[2], "out") : empty_matrix(m.rows, 2 * m.cols, dy.scalar_type(), dy.device());
     const Matrix o = like(out, "out", m.rows, 2 * m.cols, m.dtype);
     char* p = static_cast<char*>(o.p);
     void* stream = on.handle();
@@ -413,7 +419,8 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
-#define TACO_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+#define TACO_METHOD(name) \
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {TACO_METHOD(quantize), TACO_METHOD(rms_norm), TACO_METHOD(rms_norm_backward),
                           TACO_METHOD(swiglu), TACO_METHOD(swiglu_backward), TACO_METHOD(matmul),
                           {nullptr, nullptr, 0, nullptr}};

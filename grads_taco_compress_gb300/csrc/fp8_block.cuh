@@ -295,7 +295,8 @@ __device__ __forceinline__ Row16<T> load16(const T* p, int n, bool wide) {
   Row16<T> r;
   if (VEC && n == 16) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) load_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      load_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
   } else if constexpr (VEC) {   // the end of a row
     float v[16];
 #pragma unroll
@@ -310,7 +311,8 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void store16(T* p, int n, bool wide, const Row16<T>& r) {
   if (VEC && n == 16) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) store_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      store_words8(p + 8 * i * (4 / sizeof(T)), wide, r.w + 8 * i);
   } else if constexpr (VEC) {
     float v[16];
     unpack<T>(r, v);

@@ -17,9 +17,10 @@
 //              the 128-byte swizzle;
 //   warp 1     owns the tensor memory; one lane copies the scales to tensor
 //              memory, issues the MMAs and commits each stage;
-//   warp 2     (and 3, in pairs) scales: every chunk of 4 blocks (512 columns) one 32-bit word per
-//              row of A and B, byte j the scale of block j, in the order that
-//              tcgen05.cp 32x128b spreads over the tensor memory;
+//   warp 2     (and 3, in pairs) scales: every chunk of 4 blocks (512 columns)
+//              one 32-bit word per row of A and B, byte j the scale of block j,
+//              in the order that tcgen05.cp 32x128b spreads over the tensor
+//              memory;
 //   warps 4-7  epilogue: lane = row, tensor memory to registers to C.
 // Every wait is bounded in time with a CTA-wide abort flag.
 //
@@ -65,13 +66,7 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
   const uint64_t desc = umma_desc(saddr, 0, 128);   // no swizzle, 8 rows of 16 bytes per group
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
 }
-// wait_or_abort, with the first tries free of the timer: reading it between
-// two tries cost more than most waits last.
-constexpr int kFreeTries = 256;
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-#pragma unroll 1
-  for (int i = 0; i < kFreeTries; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
   return wait_or_abort(bar, parity, abort_flag, &g_fp8_matmul_fault, kFaultFp8MatmulWait);
 }
 
@@ -291,9 +286,11 @@ struct Pair {
   static constexpr uint32_t scales = staging + 4 * kBoxes * 4096;
   static constexpr uint32_t full = scales + kScaleBufs * kScale;
   static constexpr uint32_t empty = full + 8 * kStages;
-  static constexpr uint32_t sfull = empty + 8 * kStages;      // scale words of a chunk are in shared memory
-  static constexpr uint32_t sempty = sfull + 8 * kScaleBufs;  // and were copied to tensor memory
-  static constexpr uint32_t sdone = sempty + 8 * kScaleBufs;  // the chunk's MMAs are done: its set of scale columns is free
+  // scale words of a chunk: in shared memory; copied to tensor memory; read by
+  // the last MMA of the chunk, whose set of scale columns is free
+  static constexpr uint32_t sfull = empty + 8 * kStages;
+  static constexpr uint32_t sempty = sfull + 8 * kScaleBufs;
+  static constexpr uint32_t sdone = sempty + 8 * kScaleBufs;
   static constexpr uint32_t tfull = sdone + 16;
   static constexpr uint32_t tempty = tfull + 16;
   static constexpr uint32_t added = tempty + 16;              // `add` has landed in a warp's staging
@@ -359,7 +356,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     fence_mbar_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(base + S::slot) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                 :: "r"(base + S::slot) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
@@ -460,7 +458,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
               const uint32_t next = idesc + ((1u << 29) | (1u << 4));   // the scale words' next byte
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_mx_pair(d, adesc + (S::kBlock >> 4) + 2 * kk, bdesc + (S::kBlock >> 4) + 2 * kk, next, sfa, sfb, 1u);
+                mma_mx_pair(d, adesc + (S::kBlock >> 4) + 2 * kk, bdesc + (S::kBlock >> 4) + 2 * kk, next, sfa, sfb,
+                            1u);
             }
             commit_pair(base + S::empty + 8 * s);
             if (end) commit_here(base + S::sdone + 8 * (q & 1u));
@@ -484,7 +483,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     // ---------------------------------------------------------- scales ----
     // The words of 4 chunks (a group) are read together; the two warps take
     // the pair's groups in turn and read their next one ahead of its use.
-    const ScaleRows ra{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa}, rb{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb};
+    const ScaleRows ra{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa};
+    const ScaleRows rb{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb};
     const int groups = (chunks + 3) / 4;
     uint4 na[4], nb[TN / 32];
     int64_t t = pair;      // group g of tile t, whose first chunk is number q of the pair
@@ -560,7 +560,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           const uint32_t bar = base + S::added + 8 * quad;
           mbar_arrive_expect_tx(bar, boxes * 4096);
           for (int c = 0; c < boxes; ++c)
-            tma_load_2d_plain(staging + c * 4096, &add_map, static_cast<int>(n0) + c * kCols, static_cast<int>(m0), bar);
+            tma_load_2d_plain(staging + c * 4096, &add_map, static_cast<int>(n0) + c * kCols, static_cast<int>(m0),
+                              bar);
         }
       }
       __syncwarp();
@@ -818,7 +819,8 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
     __syncwarp();
   } else if (warp == 2) {
     const int chunks = (kb + kChunk - 1) / kChunk;
-    const ScaleRows rw{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb}, rx{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa};
+    const ScaleRows rw{a.sb, a.ldb_s, a.N, a.tile_b, chunks, a.vec_sb};
+    const ScaleRows rx{a.sa, a.lda_s, a.M, a.tile_a, chunks, a.vec_sa};
     const uint4 one = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
     uint4 nw[4], nx[4];
     const auto fetch = [&](int g) {

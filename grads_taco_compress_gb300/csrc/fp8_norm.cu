@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
         else
           load8<T, false>(h + col[c], n[c], xh[c]);
       } else {
-        decode8(VEC ? lds64(slot8 + get + c * (S::kThread * threads)) : load_codes8(codes + col[c], n[c]), scale[c], xh[c]);
+        const uint2 q = VEC ? lds64(slot8 + get + c * (S::kThread * threads)) : load_codes8(codes + col[c], n[c]);
+        decode8(q, scale[c], xh[c]);
       }
       if (NC > 1) load_weight8<VEC>(a.weight, a.weight_dtype, col[c], n[c], w);
 #pragma unroll
@@ -477,8 +478,7 @@ cudaError_t prepare_backward_t() {
 
 }  // namespace
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st) {
-  (void)sms;
+cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, cudaStream_t st) {
   int threads, nc;
   norm_shape(a.H, &threads, &nc);
   return with_dtype(dtype, [&](auto t) {

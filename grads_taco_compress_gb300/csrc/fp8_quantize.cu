@@ -161,7 +161,8 @@ constexpr int tile_ctas() {
 }
 
 template <typename T, bool VEC, bool TILE, bool TRANSPOSE>
-__global__ void __launch_bounds__(kThreads, (tile_ctas<T, TILE>())) quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
+__global__ void __launch_bounds__(kThreads, (tile_ctas<T, TILE>()))
+quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
   __shared__ __align__(16) uint32_t words[TRANSPOSE ? kFp8Block * 32 : 4];
   __shared__ uint32_t col_max[kFp8Block];   // TILE: entry 0 is the tile's
   __shared__ __align__(16) float col_inv[kFp8Block];

@@ -68,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, forward_ctas<T>()) swiglu_kernel(Swi
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, backward_ctas<T>()) swiglu_backward_kernel(SwigluBackwardArgs a, Divider per_row, bool wide) {
+__global__ void __launch_bounds__(kThreads, backward_ctas<T>())
+swiglu_backward_kernel(SwigluBackwardArgs a, Divider per_row, bool wide) {
   const int lane8 = threadIdx.x & 7;
   const uint64_t w = static_cast<uint64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   const int64_t row = per_row.quotient(w);

@@ -240,10 +240,10 @@ struct MatmulArgs {
   int64_t ldo;
   bool vec_sa, vec_sb;      // the scales' rows all start on 16 bytes
   bool vec_add;             // add's rows all start on 16 bytes
-  bool tma_add, tma_out;    // and its row stride is one a tensor copy takes; the same of out
+  bool tma_add, tma_out;    // add's, out's do, and the stride is one that a tensor copy takes
 };
 
-cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, int sms, cudaStream_t st);
+cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, cudaStream_t st);
 // Most CTAs, and so rows of partial sums, of the norm's backward pass on rows of
 // H (512 at 2048 columns and more, up to 2048 of shorter rows).
 int64_t norm_max_partials(int64_t H);

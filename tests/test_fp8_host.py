@@ -48,7 +48,8 @@ def fp8(i, rows, cols, tile=1, **kw):
 @no_gpu_only
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=3), ARG), (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(ld=255), SHAPE), (dict(x=None), NULL),
-    (dict(x=A + 1), ALIGN), (dict(out=None), NULL), (dict(out=fp8(2, 4, 128)), SHAPE), (dict(out=fp8(2, 5, 256)), SHAPE),
+    (dict(x=A + 1), ALIGN), (dict(out=None), NULL), (dict(out=fp8(2, 4, 128)), SHAPE),
+    (dict(out=fp8(2, 5, 256)), SHAPE),
     (dict(out=fp8(2, 4, 256, tile=64)), BLOCK), (dict(out=fp8(2, 4, 256, ld_codes=264)), SHAPE),
     (dict(out=fp8(2, 4, 256, ld_scales=1)), SHAPE), (dict(out=fp8(2, 4, 256, ld_codes=240)), SHAPE),
     (dict(out=fp8(2, 4, 256, codes=2 * A + 8)), ALIGN), (dict(out=fp8(2, 4, 256, scales=2 * A + 2)), ALIGN),
@@ -85,7 +86,8 @@ def _norm(lib, **kw):
     (dict(dtype=-1), ARG), (dict(wd=7), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG),
     (dict(eps=float("inf")), ARG), (dict(M=-1), SHAPE), (dict(H=0), SHAPE), (dict(H=32769), SHAPE),
     (dict(ldx=200), SHAPE), (dict(ldr=255), SHAPE), (dict(ldh=0), SHAPE), (dict(x=None), NULL), (dict(w=None), NULL),
-    (dict(y=None), NULL), (dict(res=None), NULL), (dict(h=None), NULL), (dict(x=A + 1), ALIGN), (dict(w=3 * A + 2), ALIGN),
+    (dict(y=None), NULL), (dict(res=None), NULL), (dict(h=None), NULL), (dict(x=A + 1), ALIGN),
+    (dict(w=3 * A + 2), ALIGN),
     (dict(rstd=5 * A + 2), ALIGN), (dict(y=fp8(6, 4, 256, tile=128)), BLOCK), (dict(y=fp8(6, 4, 384)), SHAPE),
     (dict(ck=fp8(6, 4, 256)), ARG), (dict(h=A + 64), ARG), (dict(h=A, ldh=512), ARG), (dict(rstd=4 * A), ARG),
     (dict(rstd=A), ARG), (dict(y=fp8(1, 4, 256)), ARG), (dict(ck=fp8(3, 4, 256)), ARG),
@@ -105,7 +107,8 @@ def _norm_backward(lib, **kw):
 
 @no_gpu_only
 @pytest.mark.parametrize("kw,status", [
-    (dict(dtype=9), ARG), (dict(M=-2), SHAPE), (dict(H=40000), SHAPE), (dict(ck=None), NULL), (dict(h=9 * A, ldh=256), NULL),
+    (dict(dtype=9), ARG), (dict(M=-2), SHAPE), (dict(H=40000), SHAPE), (dict(ck=None), NULL),
+    (dict(h=9 * A, ldh=256), NULL),
     (dict(w=None), NULL), (dict(rstd=None), NULL), (dict(dw=None), NULL), (dict(dx=None), NULL), (dict(dy=None), NULL),
     (dict(ws=None), WS), (dict(wsb=4 * 256 * 4 - 1), WS), (dict(ws=8 * A + 4), ALIGN), (dict(dx=6 * A + 1), ALIGN),
     (dict(dw=7 * A + 2), ALIGN), (dict(lddx=100), SHAPE), (dict(dx=A, lddx=512), ARG), (dict(dx=A + 32), ARG),
