@@ -128,16 +128,27 @@ at::Tensor empty_matrix(int64_t rows, int64_t cols, at::ScalarType type, const a
 at::Tensor empty_vector(int64_t n, at::ScalarType type, const at::Device& device) {
   return empty_strided({n}, {1}, type, device);
 }
-// Rows of codes on 16 bytes, rows of scales on 16 (which a product reads fastest).
-Pair new_fp8(int64_t rows, int64_t cols, int64_t tile, const at::Device& device) {
-  const int64_t kb = (cols + kBlock - 1) / kBlock;
-  return {empty_strided({rows, cols}, {up(cols, 16), 1}, at::kByte, device),
-          empty_strided({(rows + tile - 1) / tile, kb}, {up(kb, 16), 1}, at::kByte, device)};
-}
-Pair new_fp8_planes(int64_t planes, int64_t rows, int64_t cols, const at::Device& device) {
-  const int64_t kb = (cols + kBlock - 1) / kBlock, ld = up(cols, 16), lds = up(kb, 16);
-  return {empty_strided({planes, rows, cols}, {rows * ld, ld, 1}, at::kByte, device),
-          empty_strided({planes, rows, kb}, {rows * lds, lds, 1}, at::kByte, device)};
+// Codes and scales of a new FP8 block tensor, rows of either on 16 bytes (which a
+// product reads fastest), in one allocation: they live and die together, and an
+// allocation costs more than the rest of such a call's arguments.
+Pair new_fp8(at::IntArrayRef shape, int64_t tile, const at::Device& device) {
+  const int64_t cols = shape.back(), rows = shape[shape.size() - 2], planes = shape.size() == 3 ? shape[0] : 1;
+  const int64_t kb = (cols + kBlock - 1) / kBlock, srows = (rows + tile - 1) / tile;
+  const int64_t ld = up(cols, 16), lds = up(kb, 16), at = up(planes * rows * ld, 256);
+  at::Tensor codes = empty_vector(at + planes * srows * lds, at::kByte, device);
+  at::Tensor scales = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(codes.storage()),
+                                                               codes.key_set(), codes.dtype());
+  const auto lay_out = [](at::Tensor& t, at::IntArrayRef sizes, at::IntArrayRef strides, int64_t offset) {
+    t.unsafeGetTensorImpl()->set_sizes_and_strides(sizes, strides, offset);
+  };
+  if (shape.size() == 3) {
+    lay_out(codes, {planes, rows, cols}, {rows * ld, ld, 1}, 0);
+    lay_out(scales, {planes, srows, kb}, {srows * lds, lds, 1}, at);
+  } else {
+    lay_out(codes, {rows, cols}, {ld, 1}, 0);
+    lay_out(scales, {srows, kb}, {lds, 1}, at);
+  }
+  return {codes, scales};
 }
 
 // The device of `t` and the stream of the call (the current one, or the one
@@ -235,8 +246,8 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
     }
     const OnStream on(v[6], x);
     std::optional<Pair> out, out_t;
-    if (rows) out = given(v[4]) ? pair_of(v[4], "out") : new_fp8(M, K, tile, x.device());
-    if (cols) out_t = given(v[5]) ? pair_of(v[5], "out_t") : new_fp8(K, M, tile, x.device());
+    if (rows) out = given(v[4]) ? pair_of(v[4], "out") : new_fp8({M, K}, tile, x.device());
+    if (cols) out_t = given(v[5]) ? pair_of(v[5], "out_t") : new_fp8({K, M}, tile, x.device());
     taco_fp8_tensor a{}, b{};
     if (out) a = describe(out->codes, out->scales, "out", tile);
     if (out_t) b = describe(out_t->codes, out_t->scales, "out_t", tile);
@@ -273,7 +284,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     } else if (given(v[6])) {
       refuse("h is an output of the residual's addition: pass residual too");
     }
-    const Pair y = given(v[5]) ? pair_of(v[5], "out") : new_fp8(m.rows, m.cols, 1, x.device());
+    const Pair y = given(v[5]) ? pair_of(v[5], "out") : new_fp8({m.rows, m.cols}, 1, x.device());
     const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
     const at::Tensor rstd = given(v[7]) ? tensor(v[7], "rstd") : empty_vector(m.rows, at::kFloat, x.device());
     void* rs = vector(rstd, "rstd", m.rows, true);
@@ -281,7 +292,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (PyTuple_Check(v[4]))
       ck = pair_of(v[4], "checkpoint");
     else if (PyObject_IsTrue(v[4]))
-      ck = new_fp8(m.rows, m.cols, 1, x.device());
+      ck = new_fp8({m.rows, m.cols}, 1, x.device());
     taco_fp8_tensor cd{};
     if (ck) cd = describe(ck->codes, ck->scales, "checkpoint");
     void* stream = on.handle();
@@ -345,13 +356,13 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (m.cols < 2 || m.cols % 2) refuse("gate_up must have an even number of columns");
     const int64_t F = m.cols / 2;
     const OnStream on(v[3], x);
-    const Pair y = given(v[2]) ? pair_of(v[2], "out") : new_fp8(m.rows, F, 1, x.device());
+    const Pair y = given(v[2]) ? pair_of(v[2], "out") : new_fp8({m.rows, F}, 1, x.device());
     const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
     std::optional<Pair> ck;
     if (PyTuple_Check(v[1]))
       ck = pair_of(v[1], "checkpoint");
     else if (PyObject_IsTrue(v[1]))
-      ck = new_fp8_planes(2, m.rows, F, x.device());
+      ck = new_fp8({2, m.rows, F}, 1, x.device());
     taco_fp8_tensor g{}, u{};
     if (ck) {
       if (ck->codes.dim() != 3 || ck->codes.size(0) != 2 || ck->scales.dim() != 3 || ck->scales.size(0) != 2)
