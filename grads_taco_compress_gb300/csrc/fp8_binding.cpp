@@ -7,19 +7,23 @@
 // described, outputs allocated through torch, and the library of taco.h is
 // called on the current stream.
 //
-// Every function returns a tuple of tensors (None where there is none), or the
-// int status of a library call that failed; wrong arguments raise ValueError.
+// Every function returns what its Python entry point does (None for what there
+// is not), or the int status of a library call that failed; wrong arguments
+// raise ValueError.
 
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <exception>
+#include <initializer_list>
 #include <optional>
 #include <stdexcept>
 #include <string>
 
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -118,24 +122,24 @@ Pair pair_of(PyObject* o, const char* what) {
   return {tensor(PyTuple_GET_ITEM(o, 0), what), tensor(PyTuple_GET_ITEM(o, 1), what)};
 }
 
-at::Tensor empty_strided(at::IntArrayRef shape, at::IntArrayRef strides, at::ScalarType type,
-                         const at::Device& device) {
-  return at::empty_strided(shape, strides, at::TensorOptions().dtype(type).device(device));
+// A new tensor on the current device (the call's: see OnStream), straight from
+// torch's caching allocator: the dispatcher on the way to it costs as much again.
+at::Tensor empty_strided(at::IntArrayRef shape, at::IntArrayRef strides, at::ScalarType type) {
+  return at::detail::empty_strided_generic(shape, strides, c10::cuda::CUDACachingAllocator::get(),
+                                           c10::DispatchKeySet(c10::DispatchKey::CUDA), type);
 }
-at::Tensor empty_matrix(int64_t rows, int64_t cols, at::ScalarType type, const at::Device& device) {
-  return empty_strided({rows, cols}, {cols > 1 ? cols : 1, 1}, type, device);
+at::Tensor empty_matrix(int64_t rows, int64_t cols, at::ScalarType type) {
+  return empty_strided({rows, cols}, {cols > 1 ? cols : 1, 1}, type);
 }
-at::Tensor empty_vector(int64_t n, at::ScalarType type, const at::Device& device) {
-  return empty_strided({n}, {1}, type, device);
-}
+at::Tensor empty_vector(int64_t n, at::ScalarType type) { return empty_strided({n}, {1}, type); }
 // Codes and scales of a new FP8 block tensor, rows of either on 16 bytes (which a
 // product reads fastest), in one allocation: they live and die together, and an
 // allocation costs more than the rest of such a call's arguments.
-Pair new_fp8(at::IntArrayRef shape, int64_t tile, const at::Device& device) {
+Pair new_fp8(at::IntArrayRef shape, int64_t tile) {
   const int64_t cols = shape.back(), rows = shape[shape.size() - 2], planes = shape.size() == 3 ? shape[0] : 1;
   const int64_t kb = (cols + kBlock - 1) / kBlock, srows = (rows + tile - 1) / tile;
   const int64_t ld = up(cols, 16), lds = up(kb, 16), at = up(planes * rows * ld, 256);
-  at::Tensor codes = empty_vector(at + planes * srows * lds, at::kByte, device);
+  at::Tensor codes = empty_vector(at + planes * srows * lds, at::kByte);
   at::Tensor scales = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(codes.storage()),
                                                                codes.key_set(), codes.dtype());
   const auto lay_out = [](at::Tensor& t, at::IntArrayRef sizes, at::IntArrayRef strides, int64_t offset) {
@@ -173,25 +177,34 @@ class OnStream {
   c10::cuda::OptionalCUDAStreamGuard stream_;
 };
 
-struct Result {
-  PyObject* tuple;
+// fp8.py's Fp8Tensor and RmsNormOutput (named tuples), given by it once.
+PyTypeObject *fp8_type = nullptr, *norm_type = nullptr;
+
+PyObject* none() {
+  Py_INCREF(Py_None);
+  return Py_None;
+}
+PyObject* object(const at::Tensor& t) { return THPVariable_Wrap(t); }
+
+// A tuple, or one of the types above, of `items`, whose references it takes.
+PyObject* tuple(PyTypeObject* type, std::initializer_list<PyObject*> items) {
+  PyObject* t = type->tp_alloc(type, static_cast<Py_ssize_t>(items.size()));
   Py_ssize_t n = 0;
-  explicit Result(Py_ssize_t size) : tuple(PyTuple_New(size)) {}
-  Result& add(const std::optional<at::Tensor>& t) {
-    PyObject* o = Py_None;
-    if (t) {
-      o = THPVariable_Wrap(*t);
-    } else {
-      Py_INCREF(o);
-    }
-    PyTuple_SET_ITEM(tuple, n++, o);
-    return *this;
+  bool whole = t != nullptr;
+  for (PyObject* o : items) {
+    whole = whole && o;
+    if (t)
+      PyTuple_SET_ITEM(t, n++, o);
+    else
+      Py_XDECREF(o);
   }
-  Result& add(const std::optional<Pair>& p) {
-    add(p ? std::optional<at::Tensor>(p->codes) : std::nullopt);
-    return add(p ? std::optional<at::Tensor>(p->scales) : std::nullopt);
-  }
-};
+  if (whole) return t;
+  Py_XDECREF(t);
+  return nullptr;
+}
+PyObject* object(const std::optional<Pair>& p) {
+  return p ? tuple(fp8_type, {object(p->codes), object(p->scales)}) : none();
+}
 
 template <typename F>
 taco_status call(F&& f) {
@@ -220,7 +233,7 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t count, F&& body) {
   return nullptr;
 }
 
-// quantize(x, rows, cols, tile, out, out_t, stream) -> codes, scales, codes_t, scales_t
+// quantize(x, rows, cols, tile, out, out_t, stream) -> rows, transpose
 PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> PyObject* {
     const bool rows = PyObject_IsTrue(v[1]), cols = PyObject_IsTrue(v[2]);
@@ -246,8 +259,8 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
     }
     const OnStream on(v[6], x);
     std::optional<Pair> out, out_t;
-    if (rows) out = given(v[4]) ? pair_of(v[4], "out") : new_fp8({M, K}, tile, x.device());
-    if (cols) out_t = given(v[5]) ? pair_of(v[5], "out_t") : new_fp8({K, M}, tile, x.device());
+    if (rows) out = given(v[4]) ? pair_of(v[4], "out") : new_fp8({M, K}, tile);
+    if (cols) out_t = given(v[5]) ? pair_of(v[5], "out_t") : new_fp8({K, M}, tile);
     taco_fp8_tensor a{}, b{};
     if (out) a = describe(out->codes, out->scales, "out", tile);
     if (out_t) b = describe(out_t->codes, out_t->scales, "out_t", tile);
@@ -257,12 +270,12 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
                     : taco_fp8_quantize(m.p, m.dtype, M, K, m.ld, out ? &a : nullptr, out_t ? &b : nullptr, stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
-    return Result(4).add(out).add(out_t).tuple;
+    return tuple(&PyTuple_Type, {object(out), object(out_t)});
   });
 }
 
 // rms_norm(x, weight, residual, eps, checkpoint, out, h, rstd, stream)
-//   -> codes, scales, h, rstd, checkpoint codes, checkpoint scales
+//   -> y, h, rstd, checkpoint
 PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
     const at::Tensor& x = tensor(v[0], "x");
@@ -279,20 +292,20 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     at::Tensor h = x;
     if (given(v[2])) {
       r = like(tensor(v[2], "residual"), "residual", m.rows, m.cols, m.dtype);
-      h = given(v[6]) ? tensor(v[6], "h") : empty_matrix(m.rows, m.cols, x.scalar_type(), x.device());
+      h = given(v[6]) ? tensor(v[6], "h") : empty_matrix(m.rows, m.cols, x.scalar_type());
       ho = like(h, "h", m.rows, m.cols, m.dtype);
     } else if (given(v[6])) {
       refuse("h is an output of the residual's addition: pass residual too");
     }
-    const Pair y = given(v[5]) ? pair_of(v[5], "out") : new_fp8({m.rows, m.cols}, 1, x.device());
+    const Pair y = given(v[5]) ? pair_of(v[5], "out") : new_fp8({m.rows, m.cols}, 1);
     const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
-    const at::Tensor rstd = given(v[7]) ? tensor(v[7], "rstd") : empty_vector(m.rows, at::kFloat, x.device());
+    const at::Tensor rstd = given(v[7]) ? tensor(v[7], "rstd") : empty_vector(m.rows, at::kFloat);
     void* rs = vector(rstd, "rstd", m.rows, true);
     std::optional<Pair> ck;
     if (PyTuple_Check(v[4]))
       ck = pair_of(v[4], "checkpoint");
     else if (PyObject_IsTrue(v[4]))
-      ck = new_fp8({m.rows, m.cols}, 1, x.device());
+      ck = new_fp8({m.rows, m.cols}, 1);
     taco_fp8_tensor cd{};
     if (ck) cd = describe(ck->codes, ck->scales, "checkpoint");
     void* stream = on.handle();
@@ -302,7 +315,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
-    return Result(6).add(std::optional<Pair>(y)).add(h).add(rstd).add(ck).tuple;
+    return tuple(norm_type, {object(std::optional<Pair>(y)), object(h), object(rstd), object(ck)});
   });
 }
 
@@ -326,16 +339,16 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     void* rstd = vector(tensor(v[3], "rstd"), "rstd", m.rows, true);
     if (given(v[4])) dh = like(tensor(v[4], "dh"), "dh", m.rows, m.cols, m.dtype);
     const at::Tensor dx =
-        given(v[5]) ? tensor(v[5], "dx") : empty_matrix(m.rows, m.cols, dy.scalar_type(), dy.device());
+        given(v[5]) ? tensor(v[5], "dx") : empty_matrix(m.rows, m.cols, dy.scalar_type());
     const Matrix out = like(dx, "dx", m.rows, m.cols, m.dtype);
-    const at::Tensor dw = given(v[6]) ? tensor(v[6], "dw") : empty_vector(m.cols, at::kFloat, dy.device());
+    const at::Tensor dw = given(v[6]) ? tensor(v[6], "dw") : empty_vector(m.cols, at::kFloat);
     void* dwp = vector(dw, "dw", m.cols, true);
     at::Tensor ws;
     if (given(v[7])) {
       ws = tensor(v[7], "workspace");
       if (!ws.is_cuda() || !ws.is_contiguous()) refuse("workspace must be a contiguous CUDA tensor");
     } else {
-      ws = empty_vector(static_cast<int64_t>(taco_rms_norm_workspace_bytes(m.rows, m.cols)), at::kByte, dy.device());
+      ws = empty_vector(static_cast<int64_t>(taco_rms_norm_workspace_bytes(m.rows, m.cols)), at::kByte);
     }
     void* stream = on.handle();
     const taco_status st = call([&] {
@@ -344,11 +357,11 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                         out.ld, static_cast<float*>(dwp), ws.data_ptr(), ws.nbytes(), stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
-    return Result(2).add(dx).add(dw).tuple;
+    return tuple(&PyTuple_Type, {object(dx), object(dw)});
   });
 }
 
-// swiglu(gate_up, checkpoint, out, stream) -> codes, scales, checkpoint codes, checkpoint scales
+// swiglu(gate_up, checkpoint, out, stream) -> y, checkpoint
 PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(n, 4, [&]() -> PyObject* {
     const at::Tensor& x = tensor(v[0], "gate_up");
@@ -356,13 +369,13 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (m.cols < 2 || m.cols % 2) refuse("gate_up must have an even number of columns");
     const int64_t F = m.cols / 2;
     const OnStream on(v[3], x);
-    const Pair y = given(v[2]) ? pair_of(v[2], "out") : new_fp8({m.rows, F}, 1, x.device());
+    const Pair y = given(v[2]) ? pair_of(v[2], "out") : new_fp8({m.rows, F}, 1);
     const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
     std::optional<Pair> ck;
     if (PyTuple_Check(v[1]))
       ck = pair_of(v[1], "checkpoint");
     else if (PyObject_IsTrue(v[1]))
-      ck = new_fp8({2, m.rows, F}, 1, x.device());
+      ck = new_fp8({2, m.rows, F}, 1);
     taco_fp8_tensor g{}, u{};
     if (ck) {
       if (ck->codes.dim() != 3 || ck->codes.size(0) != 2 || ck->scales.dim() != 3 || ck->scales.size(0) != 2)
@@ -377,7 +390,7 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
                              ck ? &g : nullptr, ck ? &u : nullptr, stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
-    return Result(4).add(std::optional<Pair>(y)).add(ck).tuple;
+    return tuple(&PyTuple_Type, {object(std::optional<Pair>(y)), object(ck)});
   });
 }
 
@@ -393,7 +406,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const taco_fp8_tensor g = describe(ck.codes, ck.scales, "checkpoint", 1, 3, 0);
     const taco_fp8_tensor u = describe(ck.codes, ck.scales, "checkpoint", 1, 3, 1);
     const at::Tensor out =
-        given(v[2]) ? tensor(v[2], "out") : empty_matrix(m.rows, 2 * m.cols, dy.scalar_type(), dy.device());
+        given(v[2]) ? tensor(v[2], "out") : empty_matrix(m.rows, 2 * m.cols, dy.scalar_type());
     const Matrix o = like(out, "out", m.rows, 2 * m.cols, m.dtype);
     char* p = static_cast<char*>(o.p);
     void* stream = on.handle();
@@ -402,7 +415,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
                                       p ? p + m.cols * dy.element_size() : p, o.ld, stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
-    return Result(1).add(out).tuple;
+    return object(out);
   });
 }
 
@@ -418,7 +431,7 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
       out = tensor(v[2], "out");
     } else {
       if (!THPDtype_Check(v[3])) refuse("out_dtype must be a torch.dtype");
-      out = empty_matrix(ad.rows, bd.rows, reinterpret_cast<THPDtype*>(v[3])->scalar_type, a.codes.device());
+      out = empty_matrix(ad.rows, bd.rows, reinterpret_cast<THPDtype*>(v[3])->scalar_type);
     }
     const Matrix o = matrix(out, "out");
     if (o.rows != ad.rows || o.cols != bd.rows) refuse("out must have the rows of a and of b");
@@ -426,13 +439,28 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
     void* stream = on.handle();
     const taco_status st = call([&] { return taco_matmul_fp8(&ad, &bd, add.p, add.ld, o.p, o.ld, o.dtype, stream); });
     if (st != TACO_OK) return PyLong_FromLong(st);
-    return Result(1).add(out).tuple;
+    return object(out);
   });
+}
+
+// types(Fp8Tensor, RmsNormOutput)
+PyObject* types(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (!PyType_Check(v[i]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(v[i]), &PyTuple_Type)) n = -1;
+  if (n != 2) {
+    PyErr_SetString(PyExc_TypeError, "types(Fp8Tensor, RmsNormOutput): two subclasses of tuple");
+    return nullptr;
+  }
+  Py_INCREF(v[0]);
+  Py_INCREF(v[1]);
+  fp8_type = reinterpret_cast<PyTypeObject*>(v[0]);
+  norm_type = reinterpret_cast<PyTypeObject*>(v[1]);
+  return none();
 }
 
 #define TACO_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {TACO_METHOD(quantize), TACO_METHOD(rms_norm), TACO_METHOD(rms_norm_backward),
+PyMethodDef kMethods[] = {TACO_METHOD(types), TACO_METHOD(quantize), TACO_METHOD(rms_norm), TACO_METHOD(rms_norm_backward),
                           TACO_METHOD(swiglu), TACO_METHOD(swiglu_backward), TACO_METHOD(matmul),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8_binding", "Argument marshalling of the FP8 entry points.", -1,

@@ -74,6 +74,7 @@ def _binding():
         loader = importlib.machinery.ExtensionFileLoader("_fp8_binding", str(BINDING_PATH))
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fp8_binding", loader))
         loader.exec_module(module)
+        module.types(Fp8Tensor, RmsNormOutput)
         _BINDING = module
     return _BINDING
 
@@ -105,7 +106,7 @@ def taco_fp8_quantize(x, rows: bool = True, cols: bool = False, tile: int = 1, o
     r = _binding().quantize(x, rows, cols, tile, out, out_t, _handle(stream))
     if type(r) is int:
         _check(r, "taco_fp8_quantize")
-    return Fp8Tensor(r[0], r[1]) if rows else None, Fp8Tensor(r[2], r[3]) if cols else None
+    return r
 
 
 def taco_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
@@ -120,7 +121,7 @@ def taco_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Ten
     r = _binding().rms_norm(x, weight, residual, eps, checkpoint, out, h, rstd, _handle(stream))
     if type(r) is int:
         _check(r, "taco_rms_norm_fp8")
-    return RmsNormOutput(Fp8Tensor(r[0], r[1]), r[2], r[3], None if r[4] is None else Fp8Tensor(r[4], r[5]))
+    return r
 
 
 def taco_rms_norm_fp8_backward(dy: torch.Tensor, saved, weight: torch.Tensor, rstd: torch.Tensor,
@@ -144,7 +145,7 @@ def taco_swiglu_fp8(gate_up: torch.Tensor, checkpoint: bool | Fp8Tensor = False,
     r = _binding().swiglu(gate_up, checkpoint, out, _handle(stream))
     if type(r) is int:
         _check(r, "taco_swiglu_fp8")
-    return Fp8Tensor(r[0], r[1]), None if r[2] is None else Fp8Tensor(r[2], r[3])
+    return r
 
 
 def taco_swiglu_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor, out: torch.Tensor | None = None,
@@ -153,7 +154,7 @@ def taco_swiglu_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor, out: torch
     r = _binding().swiglu_backward(dy, checkpoint, out, _handle(stream))
     if type(r) is int:
         _check(r, "taco_swiglu_fp8_backward")
-    return r[0]
+    return r
 
 
 def taco_matmul_fp8(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
@@ -164,4 +165,4 @@ def taco_matmul_fp8(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     r = _binding().matmul(a, b, out, out_dtype, add, _handle(stream))
     if type(r) is int:
         _check(r, "taco_matmul_fp8")
-    return r[0]
+    return r
