@@ -132,27 +132,35 @@ at::Tensor empty_matrix(int64_t rows, int64_t cols, at::ScalarType type) {
   return empty_strided({rows, cols}, {cols > 1 ? cols : 1, 1}, type);
 }
 at::Tensor empty_vector(int64_t n, at::ScalarType type) { return empty_strided({n}, {1}, type); }
+void lay_out(const at::Tensor& t, at::IntArrayRef shape, at::IntArrayRef strides, int64_t offset) {
+  t.unsafeGetTensorImpl()->set_sizes_and_strides(shape, strides, offset);
+}
+// A tensor in the allocation of another, from the byte `at` (a multiple of its element) on.
+at::Tensor part(const at::Tensor& whole, int64_t at, at::IntArrayRef shape, at::IntArrayRef strides,
+                at::ScalarType type) {
+  const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
+                                                          whole.key_set(), meta);
+  lay_out(t, shape, strides, at / static_cast<int64_t>(meta.itemsize()));
+  return t;
+}
 // Codes and scales of a new FP8 block tensor, rows of either on 16 bytes (which a
 // product reads fastest), in one allocation: they live and die together, and an
-// allocation costs more than the rest of such a call's arguments.
-Pair new_fp8(at::IntArrayRef shape, int64_t tile) {
+// allocation costs more than the rest of such a call's arguments. A norm's
+// checkpoint has its rstd there too, which the backward pass reads with it.
+Pair new_fp8(at::IntArrayRef shape, int64_t tile, at::Tensor* rstd = nullptr) {
   const int64_t cols = shape.back(), rows = shape[shape.size() - 2], planes = shape.size() == 3 ? shape[0] : 1;
   const int64_t kb = (cols + kBlock - 1) / kBlock, srows = (rows + tile - 1) / tile;
   const int64_t ld = up(cols, 16), lds = up(kb, 16), at = up(planes * rows * ld, 256);
-  at::Tensor codes = empty_vector(at + planes * srows * lds, at::kByte);
-  at::Tensor scales = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(codes.storage()),
-                                                               codes.key_set(), codes.dtype());
-  const auto lay_out = [](at::Tensor& t, at::IntArrayRef sizes, at::IntArrayRef strides, int64_t offset) {
-    t.unsafeGetTensorImpl()->set_sizes_and_strides(sizes, strides, offset);
-  };
+  const int64_t end = at + planes * srows * lds;  // a multiple of 16
+  const at::Tensor codes = empty_vector(end + (rstd ? 4 * rows : 0), at::kByte);
+  if (rstd) *rstd = part(codes, end, {rows}, {1}, at::kFloat);
   if (shape.size() == 3) {
     lay_out(codes, {planes, rows, cols}, {rows * ld, ld, 1}, 0);
-    lay_out(scales, {planes, srows, kb}, {srows * lds, lds, 1}, at);
-  } else {
-    lay_out(codes, {rows, cols}, {ld, 1}, 0);
-    lay_out(scales, {srows, kb}, {lds, 1}, at);
+    return {codes, part(codes, at, {planes, srows, kb}, {srows * lds, lds, 1}, at::kByte)};
   }
-  return {codes, scales};
+  lay_out(codes, {rows, cols}, {ld, 1}, 0);
+  return {codes, part(codes, at, {srows, kb}, {lds, 1}, at::kByte)};
 }
 
 // The device of `t` and the stream of the call (the current one, or the one
@@ -288,24 +296,33 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
       PyErr_Clear();
       refuse("eps must be a number");
     }
-    Matrix r, ho;
-    at::Tensor h = x;
-    if (given(v[2])) {
-      r = like(tensor(v[2], "residual"), "residual", m.rows, m.cols, m.dtype);
-      h = given(v[6]) ? tensor(v[6], "h") : empty_matrix(m.rows, m.cols, x.scalar_type());
-      ho = like(h, "h", m.rows, m.cols, m.dtype);
-    } else if (given(v[6])) {
-      refuse("h is an output of the residual's addition: pass residual too");
-    }
-    const Pair y = given(v[5]) ? pair_of(v[5], "out") : new_fp8({m.rows, m.cols}, 1);
-    const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
-    const at::Tensor rstd = given(v[7]) ? tensor(v[7], "rstd") : empty_vector(m.rows, at::kFloat);
-    void* rs = vector(rstd, "rstd", m.rows, true);
+    // A new rstd lies with the new tensor that lives as long: the checkpoint, else h.
+    at::Tensor h = x, rstd;
+    if (given(v[7])) rstd = tensor(v[7], "rstd");
     std::optional<Pair> ck;
     if (PyTuple_Check(v[4]))
       ck = pair_of(v[4], "checkpoint");
     else if (PyObject_IsTrue(v[4]))
-      ck = new_fp8({m.rows, m.cols}, 1);
+      ck = new_fp8({m.rows, m.cols}, 1, rstd.defined() ? nullptr : &rstd);
+    Matrix r, ho;
+    if (given(v[2])) {
+      r = like(tensor(v[2], "residual"), "residual", m.rows, m.cols, m.dtype);
+      if (given(v[6])) {
+        h = tensor(v[6], "h");
+      } else {
+        const int64_t end = up(m.rows * m.cols * x.element_size(), 16);
+        const at::Tensor whole = empty_vector(end + (rstd.defined() ? 0 : 4 * m.rows), at::kByte);
+        h = part(whole, 0, {m.rows, m.cols}, {m.cols > 1 ? m.cols : 1, 1}, x.scalar_type());
+        if (!rstd.defined()) rstd = part(whole, end, {m.rows}, {1}, at::kFloat);
+      }
+      ho = like(h, "h", m.rows, m.cols, m.dtype);
+    } else if (given(v[6])) {
+      refuse("h is an output of the residual's addition: pass residual too");
+    }
+    if (!rstd.defined()) rstd = empty_vector(m.rows, at::kFloat);
+    void* rs = vector(rstd, "rstd", m.rows, true);
+    const Pair y = given(v[5]) ? pair_of(v[5], "out") : new_fp8({m.rows, m.cols}, 1);
+    const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
     taco_fp8_tensor cd{};
     if (ck) cd = describe(ck->codes, ck->scales, "checkpoint");
     void* stream = on.handle();
