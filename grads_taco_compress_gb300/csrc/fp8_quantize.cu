@@ -11,11 +11,12 @@
 // through it too, 4 rows of a column to a word, so that they leave as whole
 // 128-byte rows.
 //
+// The transpose of codes alone works on pairs of fp16 (below).
+//
 // Measured (a plain copy: 6.7 TB/s): rows of 8192 x 4096 bf16 15.4 us, 6.5 TB/s;
 // rows and transpose from one read 26.4 us, 5.1 TB/s, 59% of the issue slots;
-// the transpose of 8192 x 1600 codes 13.7 us, 63% of the issue slots at 1.8
-// waves of CTAs: every code is decoded twice, for the maximum and for its new
-// block.
+// the transpose of 8192 x 1600 codes 8.6 us (13.7 in fp32, 1500 instructions a
+// thread, 63% of the issue slots).
 
 #include "fp8_block.cuh"
 
@@ -152,6 +153,211 @@ __device__ __forceinline__ void fold_columns(const typename RowOf<T>::type (&r)[
   }
 }
 
+// 8 lanes write the 128 codes of one column of the transposed tile, 16 each.
+__device__ __forceinline__ void store_transposed(const QuantizeArgs& a, const uint32_t* words, int64_t r0, int64_t c0,
+                                                 int lane8, int r4) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = 32 * i + r4;
+    const int n = c0 + c < a.K ? clamp16(a.M - r0 - 16 * lane8) : 0;
+    const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(c, 4 * lane8)]);
+    store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, n, w);
+  }
+}
+
+// ------------------------------------------ re-blocking in half precision ----
+// A code times 2^d is exact in fp16 down to 2^-23 and so takes half the
+// instructions of fp32: the codes of a tile are decoded to w = code *
+// 2^(scale - top), top the largest scale byte of its rows that hold anything
+// but zeros, and the transposed codes are w * 2^(top - new scale), both
+// products exact where the code does not round to zero (it does below 2^-10,
+// fp16 loses bits only below 2^-24). Tiles whose rows' scales are further
+// apart than kSpread, or that hold a NaN or scales near the end of the range,
+// and columns that need a factor above 2^15, leave the tile to fp32.
+constexpr int kSpread = 14;
+constexpr uint32_t kTopLimit = 240;
+constexpr uint32_t kAbs2 = 0x7fff7fffu;
+
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two_codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(two_codes)));
+  return h;
+}
+__device__ __forceinline__ uint32_t e4m3x2_from_h2(uint32_t h) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+  return c;
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// fp16 bits of 2^d, -14 <= d <= 15.
+__device__ __forceinline__ uint32_t h_pow2(int d) { return static_cast<uint32_t>(d + 15) << 10; }
+
+// Largest and smallest scale byte of a warp's rows that hold anything but
+// zeros, as top << 16 | 255 - low: a maximum over 16-bit halves joins them.
+__device__ __forceinline__ uint32_t scale_range(const Fp8Row16 (&r)[4]) {
+  uint32_t top = 0, low = 255;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4& c = r[i].codes;
+    if (((c.x | c.y | c.z | c.w) & 0x7f7f7f7fu) != 0u || r[i].scale == kScaleNan) {
+      top = max(top, r[i].scale);
+      low = min(low, r[i].scale);
+    }
+  }
+  return __reduce_max_sync(kFullMask, top) << 16 | (255u - __reduce_min_sync(kFullMask, low));
+}
+
+// The factor of a row, 2^(scale - top), in both halves.
+__device__ __forceinline__ uint32_t row_factor(uint32_t scale, uint32_t top) {
+  const int d = static_cast<int>(scale) - static_cast<int>(top);   // rows of zeros may lie anywhere
+  return h_pow2(min(max(d, -kSpread), 0)) * 0x10001u;
+}
+// Columns 2 p and 2 p + 1 of a row as w (above).
+__device__ __forceinline__ uint32_t packed_pair(const Fp8Row16& r, int p, uint32_t factor) {
+  const uint32_t c = p < 2 ? r.codes.x : p < 4 ? r.codes.y : p < 6 ? r.codes.z : r.codes.w;
+  return mul_h2(e4m3x2_to_h2(p & 1 ? c >> 16 : c & 0xffffu), factor);
+}
+
+// The new scale byte of a column whose largest |w| is m, and its factor as
+// fp16 bits; false where fp16 cannot carry it.
+__device__ __forceinline__ bool column_scale(float m, uint32_t top, uint32_t& byte, uint32_t& factor) {
+  const uint32_t bits = __float_as_uint(m);
+  byte = kScaleOne;
+  factor = h_pow2(0);
+  if (bits == 0u) return true;
+  if (bits >= 0x7f800000u) return false;
+  const int e = static_cast<int>((bits >> 23) + top) - 127;   // of m * 2^(top - 127); subnormal below 1
+  byte = fp8_scale_byte(e < 1 ? 1u : static_cast<uint32_t>(e) << 23 | (bits & 0x7fffffu));
+  const int d = static_cast<int>(top) - static_cast<int>(byte);
+  if (d > 15) return false;
+  factor = h_pow2(d);
+  return true;
+}
+
+// The transpose of codes alone: quantize_tile_kernel's tile and threads.
+__global__ void __launch_bounds__(kThreads, 4)
+transpose_codes_kernel(QuantizeArgs a, Divider per_row) {
+  static_assert(kThreads == 256, "eight warps");
+  __shared__ __align__(16) uint32_t words[kFp8Block * 32];
+  __shared__ uint32_t col_max[kFp8Block];
+  __shared__ __align__(16) uint32_t factors[kFp8Block];   // pairs of fp16, or fp32
+  __shared__ __align__(16) uint32_t ranges[8];
+  __shared__ bool wide_range;   // fp16 cannot carry the tile
+  const int64_t rb = per_row.quotient(blockIdx.x);
+  const int64_t cb = blockIdx.x - rb * static_cast<int64_t>(per_row.d);
+  const int lane8 = threadIdx.x & 7, r4 = threadIdx.x >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
+  const int64_t row = r0 + 4 * r4, col = c0 + 16 * lane8;
+  if (threadIdx.x < kFp8Block) col_max[threadIdx.x] = 0;
+  if (threadIdx.x == 0) wide_range = false;
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  Fp8Row16 r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = read16<Fp8Source, true>(a, row + i, col, row + i < a.M ? clamp16(a.K - col) : 0, false);
+  const uint32_t mine = scale_range(r);
+  if (lane == 0) ranges[warp] = mine;
+  __syncthreads();
+
+  const uint4 x = reinterpret_cast<const uint4*>(ranges)[0], y = reinterpret_cast<const uint4*>(ranges)[1];
+  const uint32_t range = __vmaxu2(__vimax3_u16x2(x.x, x.y, x.z),
+                                  __vmaxu2(__vimax3_u16x2(x.w, y.x, y.y), __vmaxu2(y.z, y.w)));
+  const uint32_t top = range >> 16, low = 255u - (range & 0xffffu);
+  bool packed = top <= kTopLimit && static_cast<int>(top) - static_cast<int>(low) <= kSpread;
+  uint32_t rf[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rf[i] = row_factor(r[i].scale, top);
+  if (packed) {
+    uint32_t m[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = packed_pair(r[i], p, rf[i]) & kAbs2;
+      m[p] = __vmaxu2(__vimax3_u16x2(w[0], w[1], w[2]), w[3]);
+      m[p] = __vmaxu2(m[p], __shfl_xor_sync(kFullMask, m[p], 8));
+      m[p] = __vmaxu2(m[p], __shfl_xor_sync(kFullMask, m[p], 16));
+    }
+    if (lane < 8) {
+      uint4* to = reinterpret_cast<uint4*>(&words[warp * (kFp8Block / 2) + 8 * lane8]);
+      to[0] = make_uint4(m[0], m[1], m[2], m[3]);
+      to[1] = make_uint4(m[4], m[5], m[6], m[7]);
+    }
+    __syncthreads();
+    uint32_t b0 = 0, b1 = 0;
+    if (threadIdx.x < kFp8Block / 2) {
+      uint32_t all = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) all = __vmaxu2(all, words[i * (kFp8Block / 2) + threadIdx.x]);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&all));
+      uint32_t f0, f1;
+      const bool fits0 = column_scale(f.x, top, b0, f0), fits1 = column_scale(f.y, top, b1, f1);
+      if (!fits0 || !fits1) wide_range = true;
+      factors[threadIdx.x] = f0 | f1 << 16;
+    }
+    __syncthreads();
+    packed = !wide_range;
+    if (packed && threadIdx.x < kFp8Block / 2) {
+      const int64_t c = c0 + 2 * threadIdx.x;
+      if (c < a.K) a.t_scales[c * a.t_lds + rb] = static_cast<uint8_t>(b0);
+      if (c + 1 < a.K) a.t_scales[(c + 1) * a.t_lds + rb] = static_cast<uint8_t>(b1);
+    }
+  }
+  if (packed) {
+    const uint4 g = *reinterpret_cast<const uint4*>(&factors[8 * lane8]);
+    const uint4 h = *reinterpret_cast<const uint4*>(&factors[8 * lane8 + 4]);
+    const uint32_t f[8] = {g.x, g.y, g.z, g.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = e4m3x2_from_h2(mul_h2(packed_pair(r[i], p, rf[i]), f[p]));
+      const uint32_t q01 = __byte_perm(q[0], q[1], 0x5410), q23 = __byte_perm(q[2], q[3], 0x5410);
+      const int c = 16 * lane8 + 2 * p;
+      words[tile_word(c, r4)] = __byte_perm(q01, q23, 0x6420);
+      words[tile_word(c + 1, r4)] = __byte_perm(q01, q23, 0x7531);
+    }
+  } else {   // in fp32, four columns at a time
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      float v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) values4<Fp8Source>(r[i], q, v[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        atomicMax(&col_max[16 * lane8 + 4 * q + e],
+                  __float_as_uint(amax3(amax3(0.0f, v[0][e], v[1][e]), v[2][e], v[3][e])));
+    }
+    __syncthreads();
+    if (threadIdx.x < kFp8Block) {
+      const uint32_t b = fp8_scale_byte(col_max[threadIdx.x]);
+      factors[threadIdx.x] = __float_as_uint(fp8_inverse_scale(b));
+      if (c0 + threadIdx.x < a.K) a.t_scales[(c0 + threadIdx.x) * a.t_lds + rb] = static_cast<uint8_t>(b);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      float v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) values4<Fp8Source>(r[i], q, v[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = 16 * lane8 + 4 * q + e;
+        const float inv = __uint_as_float(factors[c]);
+        words[tile_word(c, r4)] = e4m3x4_from_f32(v[0][e] * inv, v[1][e] * inv, v[2][e] * inv, v[3][e] * inv);
+      }
+    }
+  }
+  __syncthreads();
+  store_transposed(a, words, r0, c0, lane8, r4);
+}
+
 // CTAs per SM that the tile kernel's registers are held to (bf16, rows and
 // transpose of 8192 x 4096: 2: 54 us, 4: 33 us; more, and more for the wider
 // sources and the tiles, spill).
@@ -246,14 +452,7 @@ quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
       }
     }
     __syncthreads();
-    // 8 lanes write the 128 codes of one column, 16 each
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = 32 * i + r4;
-      const int n = c0 + c < a.K ? clamp16(a.M - r0 - 16 * lane8) : 0;
-      const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(c, 4 * lane8)]);
-      store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, n, w);
-    }
+    store_transposed(a, words, r0, c0, lane8, r4);
   }
 }
 
@@ -268,6 +467,8 @@ cudaError_t launch_t(const QuantizeArgs& a, bool wide, cudaStream_t st) {
   }
   const Divider per_row((a.K + kFp8Block - 1) / kFp8Block);
   const dim3 grid(static_cast<unsigned>(per_row.d * ((a.M + kFp8Block - 1) / kFp8Block)));
+  if constexpr (std::is_same<T, Fp8Source>::value)
+    if (a.tile == 1 && !a.codes) return launch_dependent(transpose_codes_kernel, grid, kThreads, 0, st, a, per_row);
   auto k = a.tile == 1    ? quantize_tile_kernel<T, VEC, false, true>
            : a.t_codes ? quantize_tile_kernel<T, VEC, true, true>
                        : quantize_tile_kernel<T, VEC, true, false>;
