@@ -14,9 +14,9 @@
 // The transpose of codes alone works on pairs of fp16 (below).
 //
 // Measured (a plain copy: 6.7 TB/s): rows of 8192 x 4096 bf16 15.4 us, 6.5 TB/s;
-// rows and transpose from one read 26.4 us, 5.1 TB/s, 59% of the issue slots;
-// the transpose of 8192 x 1600 codes 8.6 us (13.7 in fp32, 1500 instructions a
-// thread, 63% of the issue slots).
+// rows and transpose from one read 25.0 us, 5.4 TB/s;
+// the transpose of 8192 x 1600 codes 8.1 us at 780 instructions a thread, 53% of
+// the issue slots and 1.4 waves of CTAs (13.7 us and 1500 in fp32).
 
 #include "fp8_block.cuh"
 
@@ -106,62 +106,106 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a,
   quantize16(v, n, a.codes + row * a.ldc + col, a.scales + row * a.lds + k, lane8);
 }
 
+// Four rows of 16 columns of a tile that begins at (rb, cb) blocks, the first at
+// (row, col); n: the columns that exist, rows: the rows.
+template <typename T, bool VEC>
+__device__ __forceinline__ void read_tile(const QuantizeArgs& a, int64_t rb, int64_t cb, int64_t row, int64_t col, int n,
+                                          int rows, bool wide, typename RowOf<T>::type (&r)[4]) {
+  if constexpr (std::is_same<T, Fp8Source>::value) {
+    const uint8_t* p = static_cast<const uint8_t*>(a.x) + row * a.ldx + col;
+    const uint8_t* s = a.x_scales + (a.x_tile == 1 ? row : rb) * a.x_lds + cb;
+    const int64_t step = a.x_tile == 1 ? a.x_lds : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool any = i < rows && n > 0;
+      r[i] = Fp8Row16{make_uint4(0, 0, 0, 0), kScaleOne, static_cast<uint32_t>(any ? n : 0)};
+      if (any) {
+        r[i].codes = load_codes16(p + i * a.ldx, n);
+        r[i].scale = s[i * step];
+      }
+    }
+  } else {
+    const T* p = static_cast<const T*>(a.x) + row * a.ldx + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = load16<T, VEC>(p + i * a.ldx, i < rows ? n : 0, wide);
+  }
+}
+__device__ __forceinline__ int clamp4(int64_t left) { return left < 0 ? 0 : (left > 4 ? 4 : static_cast<int>(left)); }
+
 // Word of the transposed tile that holds rows 4 r4 .. 4 r4 + 3 of column c: 32
 // words a column, in the order r4 ^ 4 (c / 16 % 8). A warp writes one column
 // of each of its 8 lane groups at a time, 4 words apiece: 32 banks.
 __device__ __forceinline__ int tile_word(int c, int r4) { return c * 32 + (r4 ^ (4 * ((c >> 4) & 7))); }
 
-// Folds the largest magnitudes of a thread's 16 columns over its 4 rows, and
-// over the 4 lanes of the warp that hold other rows of the same columns, into
-// col_max (fp32 bits). 16-bit types stay packed: with the sign cleared their
-// order is that of unsigned integers, NaN above infinity.
+// The largest magnitudes of a tile's columns. 16-bit types (and re-blocked
+// codes, below) stay packed, pairs of columns to a word: with the sign cleared
+// their order is that of unsigned integers, NaN above infinity. Every warp
+// writes the 64 words of its 16 rows to `words`; after a barrier the first 64
+// threads join them.
+constexpr uint32_t kAbs2 = 0x7fff7fffu;
+constexpr int kPairs = kFp8Block / 2;
+
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  uint32_t m = __vmaxu2(__vimax3_u16x2(a & kAbs2, b & kAbs2, c & kAbs2), d & kAbs2);
+  m = __vmaxu2(m, __shfl_xor_sync(kFullMask, m, 8));
+  return __vmaxu2(m, __shfl_xor_sync(kFullMask, m, 16));
+}
+__device__ __forceinline__ void put_pairs(const uint32_t (&m)[8], uint32_t* words) {
+  const int lane = threadIdx.x & 31;
+  if (lane < 8) {
+    uint4* to = reinterpret_cast<uint4*>(&words[(threadIdx.x >> 5) * kPairs + 8 * lane]);
+    to[0] = make_uint4(m[0], m[1], m[2], m[3]);
+    to[1] = make_uint4(m[4], m[5], m[6], m[7]);
+  }
+}
+__device__ __forceinline__ uint32_t join_pairs(const uint32_t* words, int pair) {
+  uint32_t all = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) all = __vmaxu2(all, words[i * kPairs + pair]);
+  return all;
+}
+// 32-bit types: over the thread's 4 rows and the 4 lanes of the warp that hold
+// other rows of the same columns, into col_max (fp32 bits).
 template <typename T>
 __device__ __forceinline__ void fold_columns(const typename RowOf<T>::type (&r)[4], uint32_t* col_max, int lane8) {
   const bool writes = (threadIdx.x & 31) < 8;
-  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      constexpr uint32_t kAbs = 0x7fff7fffu;
-      uint32_t w = __vmaxu2(__vimax3_u16x2(r[0].w[i] & kAbs, r[1].w[i] & kAbs, r[2].w[i] & kAbs), r[3].w[i] & kAbs);
-      w = __vmaxu2(w, __shfl_xor_sync(kFullMask, w, 8));
-      w = __vmaxu2(w, __shfl_xor_sync(kFullMask, w, 16));
-      uint32_t lo = w << 16, hi = w & 0xffff0000u;
-      if constexpr (std::is_same<T, __half>::value) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        lo = __float_as_uint(f.x);
-        hi = __float_as_uint(f.y);
-      }
-      if (writes) {
-        atomicMax(&col_max[16 * lane8 + 2 * i], lo);
-        atomicMax(&col_max[16 * lane8 + 2 * i + 1], hi);
-      }
+  for (int q = 0; q < 4; ++q) {
+    float v[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) values4<T>(r[i], q, v[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t w = __float_as_uint(amax3(amax3(0.0f, v[0][e], v[1][e]), v[2][e], v[3][e]));
+      w = max(w, __shfl_xor_sync(kFullMask, w, 8));
+      w = max(w, __shfl_xor_sync(kFullMask, w, 16));
+      if (writes) atomicMax(&col_max[16 * lane8 + 4 * q + e], w);
     }
+  }
+}
+// The two halves of a word as fp32 bits.
+template <typename T>
+__device__ __forceinline__ void pair_bits(uint32_t w, uint32_t (&b)[2]) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    b[0] = __float_as_uint(f.x);
+    b[1] = __float_as_uint(f.y);
   } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) values4<T>(r[i], q, v[i]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t w = __float_as_uint(amax3(amax3(0.0f, v[0][e], v[1][e]), v[2][e], v[3][e]));
-        w = max(w, __shfl_xor_sync(kFullMask, w, 8));
-        w = max(w, __shfl_xor_sync(kFullMask, w, 16));
-        if (writes) atomicMax(&col_max[16 * lane8 + 4 * q + e], w);
-      }
-    }
+    b[0] = w << 16;
+    b[1] = w & 0xffff0000u;
   }
 }
 
 // 8 lanes write the 128 codes of one column of the transposed tile, 16 each.
 __device__ __forceinline__ void store_transposed(const QuantizeArgs& a, const uint32_t* words, int64_t r0, int64_t c0,
                                                  int lane8, int r4) {
+  const int n = clamp16(a.M - r0 - 16 * lane8);
+  const int64_t left = a.K - c0 - r4;
+  uint8_t* const p = a.t_codes + (c0 + r4) * a.t_ldc + r0 + 16 * lane8;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = 32 * i + r4;
-    const int n = c0 + c < a.K ? clamp16(a.M - r0 - 16 * lane8) : 0;
-    const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(c, 4 * lane8)]);
-    store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, n, w);
+    const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(32 * i + r4, 4 * lane8)]);
+    store_codes16(p + 32 * i * a.t_ldc, 32 * i < left ? n : 0, w);
   }
 }
 
@@ -176,7 +220,6 @@ __device__ __forceinline__ void store_transposed(const QuantizeArgs& a, const ui
 // and columns that need a factor above 2^15, leave the tile to fp32.
 constexpr int kSpread = 14;
 constexpr uint32_t kTopLimit = 240;
-constexpr uint32_t kAbs2 = 0x7fff7fffu;
 
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two_codes) {
   uint32_t h;
@@ -258,9 +301,7 @@ transpose_codes_kernel(QuantizeArgs a, Divider per_row) {
   grid_dependency_wait();
 
   Fp8Row16 r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = read16<Fp8Source, true>(a, row + i, col, row + i < a.M ? clamp16(a.K - col) : 0, false);
+  read_tile<Fp8Source, true>(a, rb, cb, row, col, clamp16(a.K - col), clamp4(a.M - row), false, r);
   const uint32_t mine = scale_range(r);
   if (lane == 0) ranges[warp] = mine;
   __syncthreads();
@@ -279,22 +320,14 @@ transpose_codes_kernel(QuantizeArgs a, Divider per_row) {
     for (int p = 0; p < 8; ++p) {
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = packed_pair(r[i], p, rf[i]) & kAbs2;
-      m[p] = __vmaxu2(__vimax3_u16x2(w[0], w[1], w[2]), w[3]);
-      m[p] = __vmaxu2(m[p], __shfl_xor_sync(kFullMask, m[p], 8));
-      m[p] = __vmaxu2(m[p], __shfl_xor_sync(kFullMask, m[p], 16));
+      for (int i = 0; i < 4; ++i) w[i] = packed_pair(r[i], p, rf[i]);
+      m[p] = max_abs2(w[0], w[1], w[2], w[3]);
     }
-    if (lane < 8) {
-      uint4* to = reinterpret_cast<uint4*>(&words[warp * (kFp8Block / 2) + 8 * lane8]);
-      to[0] = make_uint4(m[0], m[1], m[2], m[3]);
-      to[1] = make_uint4(m[4], m[5], m[6], m[7]);
-    }
+    put_pairs(m, words);
     __syncthreads();
     uint32_t b0 = 0, b1 = 0;
-    if (threadIdx.x < kFp8Block / 2) {
-      uint32_t all = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) all = __vmaxu2(all, words[i * (kFp8Block / 2) + threadIdx.x]);
+    if (threadIdx.x < kPairs) {
+      const uint32_t all = join_pairs(words, threadIdx.x);
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&all));
       uint32_t f0, f1;
       const bool fits0 = column_scale(f.x, top, b0, f0), fits1 = column_scale(f.y, top, b1, f1);
@@ -303,7 +336,7 @@ transpose_codes_kernel(QuantizeArgs a, Divider per_row) {
     }
     __syncthreads();
     packed = !wide_range;
-    if (packed && threadIdx.x < kFp8Block / 2) {
+    if (packed && threadIdx.x < kPairs) {
       const int64_t c = c0 + 2 * threadIdx.x;
       if (c < a.K) a.t_scales[c * a.t_lds + rb] = static_cast<uint8_t>(b0);
       if (c + 1 < a.K) a.t_scales[(c + 1) * a.t_lds + rb] = static_cast<uint8_t>(b1);
@@ -382,8 +415,8 @@ quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
   grid_dependency_wait();
 
   typename RowOf<T>::type r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = read16<T, VEC>(a, row + i, col, row + i < a.M ? clamp16(a.K - col) : 0, wide);
+  const int n = clamp16(a.K - col), rows = clamp4(a.M - row);
+  read_tile<T, VEC>(a, rb, cb, row, col, n, rows, wide, r);
   __syncthreads();
 
   if (TILE) {
@@ -398,15 +431,23 @@ quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
     if ((threadIdx.x & 31) == 0) atomicMax(&col_max[0], top);
   } else {
     if (a.codes) {
+      uint8_t* const codes = a.codes + row * a.ldc + col;
+      uint8_t* const scales = a.scales + row * a.lds + cb;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float v[16];
         values16<T>(r[i], v);
-        quantize16(v, row + i < a.M ? clamp16(a.K - col) : 0, a.codes + (row + i) * a.ldc + col,
-                   a.scales + (row + i) * a.lds + cb, lane8);
+        quantize16(v, i < rows ? n : 0, codes + i * a.ldc, scales + i * a.lds, lane8);
       }
     }
-    fold_columns<T>(r, col_max, lane8);
+    if constexpr (sizeof(T) == 2) {
+      uint32_t m[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) m[p] = max_abs2(r[0].w[p], r[1].w[p], r[2].w[p], r[3].w[p]);
+      put_pairs(m, words);
+    } else {
+      fold_columns<T>(r, col_max, lane8);
+    }
   }
   __syncthreads();
   if (TILE) {
@@ -421,7 +462,7 @@ quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
       for (int i = 0; i < 4; ++i) {
         float v[16];
         values16<T>(r[i], v);
-        store_codes16(a.codes + (row + i) * a.ldc + col, row + i < a.M ? clamp16(a.K - col) : 0, codes16(v, inv));
+        store_codes16(a.codes + (row + i) * a.ldc + col, i < rows ? n : 0, codes16(v, inv));
       }
     }
   }
@@ -430,10 +471,20 @@ quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
     if (TILE) {
       tile_inv = fp8_inverse_scale(fp8_scale_byte(col_max[0]));
     } else {
-      if (threadIdx.x < kFp8Block) {
-        const uint32_t b = fp8_scale_byte(col_max[threadIdx.x]);
-        col_inv[threadIdx.x] = fp8_inverse_scale(b);
-        if (c0 + threadIdx.x < a.K) a.t_scales[(c0 + threadIdx.x) * a.t_lds + rb] = static_cast<uint8_t>(b);
+      const auto set = [&](int c, uint32_t amax) {
+        const uint32_t b = fp8_scale_byte(amax);
+        col_inv[c] = fp8_inverse_scale(b);
+        if (c0 + c < a.K) a.t_scales[(c0 + c) * a.t_lds + rb] = static_cast<uint8_t>(b);
+      };
+      if constexpr (sizeof(T) == 2) {
+        if (threadIdx.x < kPairs) {
+          uint32_t b[2];
+          pair_bits<T>(join_pairs(words, threadIdx.x), b);
+          set(2 * threadIdx.x, b[0]);
+          set(2 * threadIdx.x + 1, b[1]);
+        }
+      } else if (threadIdx.x < kFp8Block) {
+        set(threadIdx.x, col_max[threadIdx.x]);
       }
       __syncthreads();
     }
