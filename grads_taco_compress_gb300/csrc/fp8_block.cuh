@@ -173,25 +173,10 @@ __device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t*
   }
 }
 // ------------------------------------------- rows that start anywhere ----
-// The W words of a lane's consecutive elements at p, of which n exist (the
-// others read as zero), through aligned 16-byte loads and a shift. Every load
-// holds at least one byte of an element that exists.
+// The W words of n consecutive elements (the others become zero) that start s
+// bytes, a multiple of their size below 16, into the words v.
 template <typename T, int W>
-__device__ __forceinline__ void load_shifted(const T* p, int n, uint32_t (&w)[W]) {
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-  const uint32_t s = static_cast<uint32_t>(at & 15);
-  const uint4* from = reinterpret_cast<const uint4*>(at - s);
-  const int bytes = n ? static_cast<int>(s) + n * static_cast<int>(sizeof(T)) : 0;
-  uint32_t v[W + 4];
-#pragma unroll
-  for (int j = 0; j <= W / 4; ++j) {
-    uint4 q = make_uint4(0, 0, 0, 0);
-    if (16 * j < bytes) q = from[j];
-    v[4 * j] = q.x;
-    v[4 * j + 1] = q.y;
-    v[4 * j + 2] = q.z;
-    v[4 * j + 3] = q.w;
-  }
+__device__ __forceinline__ void shift_words(uint32_t (&v)[W + 4], uint32_t s, int n, uint32_t (&w)[W]) {
   if (s & 8) {
 #pragma unroll
     for (int i = 0; i < W + 2; ++i) v[i] = v[i + 2];
@@ -211,6 +196,27 @@ __device__ __forceinline__ void load_shifted(const T* p, int n, uint32_t (&w)[W]
       else if (2 * i + 1 >= n) w[i] &= 0xffffu;
     }
   }
+}
+// The W words of a lane's consecutive elements at p, of which n exist (the
+// others read as zero), through aligned 16-byte loads and a shift. Every load
+// holds at least one byte of an element that exists.
+template <typename T, int W>
+__device__ __forceinline__ void load_shifted(const T* p, int n, uint32_t (&w)[W]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint32_t s = static_cast<uint32_t>(at & 15);
+  const uint4* from = reinterpret_cast<const uint4*>(at - s);
+  const int bytes = n ? static_cast<int>(s) + n * static_cast<int>(sizeof(T)) : 0;
+  uint32_t v[W + 4];
+#pragma unroll
+  for (int j = 0; j <= W / 4; ++j) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (16 * j < bytes) q = from[j];
+    v[4 * j] = q.x;
+    v[4 * j + 1] = q.y;
+    v[4 * j + 2] = q.z;
+    v[4 * j + 3] = q.w;
+  }
+  shift_words<T>(v, s, n, w);
 }
 
 // Writes the W words of each lane of a converged warp, whose lanes hold

@@ -188,21 +188,24 @@ __device__ __forceinline__ uint2 load_codes8(const uint8_t* p, int n) {
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ... of the backward pass; the CTA's
 // column sums of dy xh go to its row of `partial`. Each thread copies its own
 // columns of the next DEPTH - 1 rows to shared memory while it works on one
-// (rows that do not start on 16 bytes are loaded as they come: DEPTH 0), so the
-// copies need no barrier and what is in flight costs no registers.
-template <typename T, int NC, bool H>
+// (DEPTH 0, where no two stages fit: rows are loaded as they come), so the
+// copies need no barrier and what is in flight costs no registers. SHIFT: rows
+// start anywhere; a thread copies the aligned 16-byte pieces that hold its
+// columns, one more than they fill, and shifts as it reads them (9240 x 2804
+// bf16: 87 us with rows loaded as they come, 68 so).
+template <typename T, int NC, bool H, bool SHIFT>
 struct BackwardStage {
-  // bytes of 8 columns: dy, dh, and h or codes
-  static constexpr int kRow = 8 * sizeof(T), kSaved = H ? kRow : 8;
+  // 8 columns: 16-byte pieces of dy, dh and h, and bytes of h or codes
+  static constexpr int kPieces = sizeof(T) / 2 + (SHIFT ? 1 : 0), kRow = 16 * kPieces, kSaved = H ? kRow : 8;
   static constexpr int kThread = 2 * kRow + kSaved;
   static constexpr size_t bytes(int threads) { return static_cast<size_t>(NC) * kThread * threads; }
 };
 
-template <typename T, int NC, int DEPTH, bool H>
+template <typename T, int NC, int DEPTH, bool H, bool SHIFT>
 __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a) {
-  using S = BackwardStage<T, NC, H>;
-  constexpr bool VEC = DEPTH > 0;
-  constexpr int kPieces = S::kRow / 16;
+  using S = BackwardStage<T, NC, H, SHIFT>;
+  constexpr bool RING = DEPTH > 0, VEC = RING && !SHIFT;
+  constexpr int kPieces = S::kPieces;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float red[2][32];
   if (threadIdx.x < 32 && threadIdx.x >= blockDim.x >> 5) red[0][threadIdx.x] = red[1][threadIdx.x] = 0.0f;
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
                 scales_step = step * a.ck_lds, dx_step = step * a.lddx;
 
   // dy, dh, h and codes run ahead of the row that is worked on by the ring's
-  // depth (VEC), scales and rstd by one row
+  // depth (RING), scales and rstd by one row
   int64_t ahead = blockIdx.x;
   uint32_t put = 0, get = 0;   // byte offsets of the stages written and read next
   const auto begin_copy = [&]() {
@@ -253,6 +256,14 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
         const auto copy = [&](const T* from, int first) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
+            if (SHIFT) {
+              const uintptr_t at = reinterpret_cast<uintptr_t>(from);
+              const int s = static_cast<int>(at & 15);
+              const bool any = n[c] && 16 * i < s + n[c] * static_cast<int>(sizeof(T));
+              copy_async16(slot16 + to + (first + i) * 16 * threads,
+                           reinterpret_cast<const T*>(at - s + (any ? col[c] * sizeof(T) + 16 * i : 0)), any ? 16 : 0);
+              continue;
+            }
             constexpr int kPer = 16 / static_cast<int>(sizeof(T));
             const int left = n[c] - kPer * i;   // elements of this piece that exist
             const int bytes = (left < 0 ? 0 : left > kPer ? kPer : left) * static_cast<int>(sizeof(T));
@@ -264,7 +275,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
         if (H)
           copy(h, 2 * kPieces);
         else
-          copy_async8(slot8 + to, codes + col[c], n[c]);
+          copy_async8(slot8 + to, codes + (SHIFT && n[c] == 0 ? 0 : col[c]), n[c]);
       }
       dy += dy_step;
       if (dh) dh += dh_step;
@@ -275,15 +286,23 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
     copy_async_commit();
     put = put + stage_bytes == DEPTH * stage_bytes ? 0 : put + stage_bytes;
   };
-  const auto staged = [&](int c, int first, f2 (&v)[4]) {
+  const auto staged = [&](int c, int first, const void* base, int64_t ld, int64_t row, f2 (&v)[4]) {
     Row8<T> r;
+    uint32_t q[4 * kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const uint4 q = lds128(slot16 + get + c * (S::kThread * threads) + (first + i) * 16 * threads);
-      r.w[4 * i] = q.x;
-      r.w[4 * i + 1] = q.y;
-      r.w[4 * i + 2] = q.z;
-      r.w[4 * i + 3] = q.w;
+      const uint4 piece = lds128(slot16 + get + c * (S::kThread * threads) + (first + i) * 16 * threads);
+      q[4 * i] = piece.x;
+      q[4 * i + 1] = piece.y;
+      q[4 * i + 2] = piece.z;
+      q[4 * i + 3] = piece.w;
+    }
+    if constexpr (SHIFT) {
+      const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld)) & 15u;
+      shift_words<T>(q, s, n[c], r.w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4 * kPieces; ++i) r.w[i] = q[i];
     }
     unpack8<T>(r, v);
   };
@@ -301,35 +320,35 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
     }
   };
 
-  if (VEC)
+  if (RING)
     for (int s = 0; s < DEPTH - 1; ++s) begin_copy();
   peek(blockIdx.x);
   f2 w[4];   // in registers for the whole call where a thread has one chunk
   if (NC == 1) load_weight8<VEC>(a.weight, a.weight_dtype, col[0], n[0], w);
   uint32_t turn = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += step, turn ^= 1u) {
-    if (VEC) begin_copy();
+    if (RING) begin_copy();
     float scale[NC];
     const float rstd = next_rstd;
     // a code times its scale is exact, so scale and rstd may be multiplied first
 #pragma unroll
     for (int c = 0; c < NC; ++c) scale[c] = H ? rstd : fp8_scale(next_scale[c]) * rstd;
     peek(row + step);
-    if (VEC) copy_async_wait<VEC ? DEPTH - 1 : 0>();
+    if (RING) copy_async_wait<RING ? DEPTH - 1 : 0>();
     f2 g[NC][4], xh[NC][4], part{0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (VEC)
-        staged(c, 0, g[c]);
+      if (RING)
+        staged(c, 0, a.dy, a.lddy, row, g[c]);
       else
         load8<T, false>(dy + col[c], n[c], g[c]);
       if (H) {
-        if (VEC)
-          staged(c, 2 * kPieces, xh[c]);
+        if (RING)
+          staged(c, 2 * kPieces, a.h, a.ldh, row, xh[c]);
         else
           load8<T, false>(h + col[c], n[c], xh[c]);
       } else {
-        const uint2 q = VEC ? lds64(slot8 + get + c * (S::kThread * threads)) : load_codes8(codes + col[c], n[c]);
+        const uint2 q = RING ? lds64(slot8 + get + c * (S::kThread * threads)) : load_codes8(codes + col[c], n[c]);
         decode8(q, scale[c], xh[c]);
       }
       if (NC > 1) load_weight8<VEC>(a.weight, a.weight_dtype, col[c], n[c], w);
@@ -348,8 +367,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
     for (int c = 0; c < NC; ++c) {
       f2 d[4];
       if (a.dh) {
-        if (VEC)
-          staged(c, kPieces, d);
+        if (RING)
+          staged(c, kPieces, a.dh, a.lddh, row, d);
         else
           load8<T, false>(dh + col[c], n[c], d);
       }
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
       store8<T, VEC>(dx + col[c], n[c], pack8<T>(g[c]));
     }
     dx += dx_step;
-    if (!VEC) {
+    if (!RING) {
       dy += dy_step;
       if (dh) dh += dh_step;
       if (H) h += h_step;
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
     }
     get = get + stage_bytes == DEPTH * stage_bytes ? 0 : get + stage_bytes;
   }
-  if (VEC) copy_async_wait<0>();
+  if (RING) copy_async_wait<0>();
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     float* p = a.partial + blockIdx.x * a.H + col[c];
@@ -441,38 +460,62 @@ int backward_ctas_per_sm(int threads) { return 1024 / threads < 16 ? 1024 / thre
 // ring's depth for a stage of this size (0: no ring).
 constexpr size_t kRingRoom = 222 * 1024;
 constexpr int kMaxDepth = 4;
-int ring_depth(size_t stage, int per_sm, bool vec) {
+int ring_depth(size_t stage, int per_sm) {
   const size_t depth = kRingRoom / per_sm / stage;
-  return !vec || depth < 2 ? 0 : depth < kMaxDepth ? static_cast<int>(depth) : kMaxDepth;
+  return depth < 2 ? 0 : depth < kMaxDepth ? static_cast<int>(depth) : kMaxDepth;
 }
 
-template <typename T, int NC, bool H, typename F>
+// Rows that start anywhere: rings of 2 or 4 stages for threads of one chunk of
+// a 16-bit type (fp32 copies half as much again as it uses: 4096 x 8191 takes
+// 158 us so, 124 us with rows loaded as they come).
+template <typename T>
+constexpr bool shifted_ring() { return sizeof(T) == 2; }
+template <typename T, int NC, bool H, bool SHIFT, typename F>
 auto with_backward_kernel(int depth, F&& f) {
-  return depth == 4   ? f(norm_backward_kernel<T, NC, 4, H>)
-         : depth == 3 ? f(norm_backward_kernel<T, NC, 3, H>)
-         : depth == 2 ? f(norm_backward_kernel<T, NC, 2, H>)
-                      : f(norm_backward_kernel<T, NC, 0, H>);
+  if constexpr (SHIFT)
+    return depth == 4 ? f(norm_backward_kernel<T, NC, 4, H, true>) : f(norm_backward_kernel<T, NC, 2, H, true>);
+  else
+    return depth == 4   ? f(norm_backward_kernel<T, NC, 4, H, false>)
+           : depth == 3 ? f(norm_backward_kernel<T, NC, 3, H, false>)
+           : depth == 2 ? f(norm_backward_kernel<T, NC, 2, H, false>)
+                        : f(norm_backward_kernel<T, NC, 0, H, false>);
 }
 
 template <typename T, int NC, bool H>
 cudaError_t launch_norm_backward_t(const NormBackwardArgs& a, int threads, bool vec, int grid, cudaStream_t st) {
-  const size_t stage = BackwardStage<T, NC, H>::bytes(threads);
-  const int depth = ring_depth(stage, backward_ctas_per_sm(threads), vec);
-  return with_backward_kernel<T, NC, H>(depth, [&](auto k) {
+  const int per_sm = backward_ctas_per_sm(threads);
+  if constexpr (NC == 1 && shifted_ring<T>()) {
+    const size_t stage = BackwardStage<T, 1, H, true>::bytes(threads);
+    const int depth = vec ? 0 : ring_depth(stage, per_sm) & ~1;
+    if (depth)
+      return with_backward_kernel<T, 1, H, true>(depth, [&](auto k) {
+        return launch_dependent(k, dim3(grid), threads, depth * stage, st, a);
+      });
+  }
+  const size_t stage = BackwardStage<T, NC, H, false>::bytes(threads);
+  const int depth = vec ? ring_depth(stage, per_sm) : 0;
+  return with_backward_kernel<T, NC, H, false>(depth, [&](auto k) {
     return launch_dependent(k, dim3(grid), threads, depth * stage, st, a);
   });
 }
 
-template <typename T, int NC, bool H>
-cudaError_t prepare_backward_t() {
+template <typename T, int NC, bool H, bool SHIFT>
+cudaError_t prepare_rings() {
   cudaError_t e = cudaSuccess;
-  for (int depth = 2; depth <= kMaxDepth; ++depth)
+  for (int depth = 2; depth <= kMaxDepth; depth += SHIFT ? 2 : 1)
     if (e == cudaSuccess)
-      e = with_backward_kernel<T, NC, H>(depth, [&](auto k) {
-        const size_t most = depth * BackwardStage<T, NC, H>::bytes(1024);
+      e = with_backward_kernel<T, NC, H, SHIFT>(depth, [&](auto k) {
+        const size_t most = depth * BackwardStage<T, NC, H, SHIFT>::bytes(1024);
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(most < kRingRoom ? most : kRingRoom));
       });
+  return e;
+}
+template <typename T, int NC, bool H>
+cudaError_t prepare_backward_t() {
+  const cudaError_t e = prepare_rings<T, NC, H, false>();
+  if constexpr (NC == 1 && shifted_ring<T>())
+    if (e == cudaSuccess) return prepare_rings<T, 1, H, true>();
   return e;
 }
 
