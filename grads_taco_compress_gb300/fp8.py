@@ -4,7 +4,9 @@ The taco_*_fp8 and taco_fp8_* entry points of include/taco.h, which states
 formats, formulas and errors. A block tensor is E4M3 codes plus one E8M0 scale
 byte per row and 128 columns, or per 128 x 128 tile for weights. As in
 ``binding``, torch supplies device memory and streams only, every output can be
-preallocated, and the work goes to ``stream`` or to the current one. The
+preallocated, and the work goes to ``stream`` or to the current one. Codes and
+scales that a call allocates share one allocation, and so does a norm's rstd
+with its checkpoint, or with h where there is none: holding one holds the other. The
 arguments are marshalled by a compiled module (csrc/fp8_binding.cpp): these
 calls take a few microseconds on small inputs, and so do their arguments in
 Python. Wrong arguments raise ValueError, a status of the library TacoError.
