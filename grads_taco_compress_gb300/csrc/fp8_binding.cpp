@@ -477,7 +477,8 @@ PyObject* types(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 #define TACO_METHOD(name) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {TACO_METHOD(types), TACO_METHOD(quantize), TACO_METHOD(rms_norm), TACO_METHOD(rms_norm_backward),
+PyMethodDef kMethods[] = {TACO_METHOD(types), TACO_METHOD(quantize), TACO_METHOD(rms_norm),
+                          TACO_METHOD(rms_norm_backward),
                           TACO_METHOD(swiglu), TACO_METHOD(swiglu_backward), TACO_METHOD(matmul),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8_binding", "Argument marshalling of the FP8 entry points.", -1,

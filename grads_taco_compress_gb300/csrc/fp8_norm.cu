@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(NormBackwardArgs a)
       q[4 * i + 3] = piece.w;
     }
     if constexpr (SHIFT) {
-      const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld)) & 15u;
+      const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld);
+      const uint32_t s = static_cast<uint32_t>(at & 15);
       shift_words<T>(q, s, n[c], r.w);
     } else {
 #pragma unroll
