@@ -73,12 +73,15 @@ taco_status check_fp8(const taco_fp8_tensor* t, int64_t rows, int64_t cols, bool
   return TACO_OK;
 }
 
-// Every output apart from every input and from the other outputs; an output
-// may be one of the inputs `in_place` names, with the same rows.
-taco_status check_apart(const Region* in, int nin, const Region* out, int nout, const Region* in_place = nullptr) {
+// Bit i of a set of inputs.
+constexpr unsigned input(int i) { return 1u << i; }
+
+// Every output apart from every input and from the other outputs; the first
+// output may be one of the inputs in the set `shared`, with the same rows.
+taco_status check_apart(const Region* in, int nin, const Region* out, int nout, unsigned shared = 0) {
   for (int o = 0; o < nout; ++o) {
     for (int i = 0; i < nin; ++i)
-      if (overlap(out[o], in[i]) && !(in_place == &out[o] && out[o].same(in[i]))) return TACO_ERR_ARG;
+      if (overlap(out[o], in[i]) && !(o == 0 && (shared & input(i)) && out[o].same(in[i]))) return TACO_ERR_ARG;
     for (int p = 0; p < o; ++p)
       if (overlap(out[o], out[p])) return TACO_ERR_ARG;
   }
@@ -203,7 +206,8 @@ taco_status taco_rms_norm_fp8(const void* x, int64_t ldx, const void* residual, 
   if (rstd) TACO_TRY(check_matrix(rstd, 1, M, M, TACO_DTYPE_F32, &out[1], nullptr));
   TACO_TRY(check_fp8(y, M, H, false, &out[2], &out[3]));
   if (checkpoint) TACO_TRY(check_fp8(checkpoint, M, H, false, &out[4], &out[5]));
-  TACO_TRY(check_apart(in, 3, out, 6, &out[0]));
+  // h_out may be x or residual
+  TACO_TRY(check_apart(in, 3, out, 6, input(0) | input(2)));
   if (M == 0) return TACO_OK;
   NormArgs a{};
   a.x = x;
@@ -260,7 +264,8 @@ taco_status taco_rms_norm_fp8_backward(const void* dy, int64_t lddy, const taco_
   if (!workspace || workspace_bytes < need) return TACO_ERR_WORKSPACE;
   if (addr(workspace) % 16) return TACO_ERR_ALIGN;
   out[2] = Region{addr(workspace), 1, static_cast<int64_t>(need), static_cast<int64_t>(need)};
-  TACO_TRY(check_apart(in, 7, out, 3, &out[0]));
+  // dx may be dy, h or dh
+  TACO_TRY(check_apart(in, 7, out, 3, input(0) | input(3) | input(6)));
   NormBackwardArgs a{};
   a.dy = dy;
   a.h = h;
@@ -345,8 +350,8 @@ taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy, const taco_fp
   TACO_TRY(check_matrix(dup, M, F, lddu, dtype, &out[1], &vec));
   // one of the two may be dy itself; the outputs stay apart from each other
   if (overlap(out[0], out[1])) return TACO_ERR_ARG;
-  TACO_TRY(check_apart(in, 5, out, 1, &out[0]));
-  TACO_TRY(check_apart(in, 5, out + 1, 1, &out[1]));
+  TACO_TRY(check_apart(in, 5, out, 1, input(0)));
+  TACO_TRY(check_apart(in, 5, out + 1, 1, input(0)));
   if (M == 0) return TACO_OK;
   SwigluBackwardArgs a{};
   a.dy = dy;
@@ -380,7 +385,7 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   int vec_add = kVec32, vec_out = kVec32;
   if (add) TACO_TRY(check_matrix(add, M, N, ldadd, dtype, &in[4], &vec_add));
   if (N > 0) TACO_TRY(check_matrix(out, M, N, ldo, dtype, &o, &vec_out));
-  TACO_TRY(check_apart(in, 5, &o, 1, &o));
+  TACO_TRY(check_apart(in, 5, &o, 1, input(4)));   // out may be add
   if (M == 0 || N == 0) return TACO_OK;
   if (((M + 127) / 128) * ((N + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
   MatmulArgs m{};
