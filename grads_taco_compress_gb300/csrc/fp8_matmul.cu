@@ -69,6 +69,10 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
 __device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   return wait_or_abort(bar, parity, abort_flag, &g_fp8_matmul_fault, kFaultFp8MatmulWait);
 }
+// The same on a barrier that the other CTA of a pair arrives at.
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return wait_or_abort<true>(bar, parity, abort_flag, &g_fp8_matmul_fault, kFaultFp8MatmulWait);
+}
 
 struct MatmulMaps {
   CUtensorMap a, b;
@@ -194,13 +198,16 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// An arrival on the other CTA's barrier at CTA scope: what it announces is read
-// by this SM's own tensor core or memory system (scale words, after the proxy
-// fence) or is tensor memory (after the tcgen05 fence), never by the other
-// CTA's threads. A release at cluster scope waits for the warp's loads in
-// flight (148 -> 140 us at 16384 x 4096 x 3584 without).
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+// An arrival on the barrier `bar` (this CTA's address) of the even CTA of the
+// pair, behind everything that the thread has written or seen written. From the
+// odd CTA it is a release at cluster scope, which the barrier's waiter acquires
+// at that scope (wait_pair); such a release takes about a microsecond, and
+// longer where the thread has loads in flight.
+__device__ __forceinline__ void arrive_even(uint32_t bar, uint32_t even_bar, uint32_t rank) {
+  if (rank == 0)
+    mbar_arrive(bar);
+  else
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(even_bar) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
@@ -264,10 +271,11 @@ struct TileMap {
   }
 };
 
-// Chunks whose scale words may wait in shared memory. The warps that bring them
-// stall for the latency of their loads at every release to the other CTA; eight
-// chunks (32 blocks) cover it (two, released with the MMAs that use them: 155
-// us instead of 127 at 16384 x 4096 x 3584).
+// Chunks whose scale words may wait in shared memory: two groups of 4, one of
+// either warp that brings them. A warp stalls for the latency of its loads and
+// of the release to the other CTA once a group, and the other group (16 blocks)
+// covers it. 16384 x 4096 x 3584: 139 us; 141 with a release a chunk and the
+// next loads in front of it (f32, 8192 x 4096 x 8192: 223 and 231).
 constexpr int kScaleBufs = 8;
 
 template <int TN>
@@ -385,7 +393,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       const int row_a = static_cast<int>(mt * 256 + rank * 128);
       const int row_b = static_cast<int>(nt * TN + rank * (TN / 2));
       for (int k = 0; k < kb; k += 2) {
-        ok = wait_here(base + S::empty + 8 * s, ph ^ 1u, abort_flag);
+        ok = wait_pair(base + S::empty + 8 * s, ph ^ 1u, abort_flag);
         ok = __all_sync(kFullMask, ok);
         if (!ok) break;
         const uint32_t st = base + S::stages + s * S::kStage, bar = full0 + 8 * s;
@@ -428,13 +436,13 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
             // the accumulator is free, and so are the columns it shares
             const uint32_t before = TN == 256 ? 1u : 2u;
             if (u >= before)
-              ok = wait_here(base + S::tempty + 8 * ((u - before) & 1u), ((u - before) >> 1) & 1u, abort_flag);
+              ok = wait_pair(base + S::tempty + 8 * ((u - before) & 1u), ((u - before) >> 1) & 1u, abort_flag);
           }
           if (ok && j == 0) {
-            ok = wait_here(base + S::sfull + 8 * sb, (q / kScaleBufs) & 1u, abort_flag);
+            ok = wait_pair(base + S::sfull + 8 * sb, (q / kScaleBufs) & 1u, abort_flag);
             if (ok && q >= 2) ok = wait_here(base + S::sdone + 8 * (q & 1u), ((q - 2) >> 1) & 1u, abort_flag);
           }
-          if (ok) ok = wait_here(base + S::full + 8 * s, ph, abort_flag);
+          if (ok) ok = wait_pair(base + S::full + 8 * s, ph, abort_flag);
           ok = __all_sync(kFullMask, ok);
           if (!ok) break;
           tc_fence_after();
@@ -505,6 +513,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
       for (int r = 0; r < TN / 32; ++r) nb[r] = rb.at(nt * TN + r * 32 + lane, g);
     };
+    const uint32_t sfull0 = in_cta(base + S::sfull, 0);
     bool ok = true;
     if (warp == 3) advance();
     if (t < tiles) fetch();
@@ -515,27 +524,33 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
       for (int r = 0; r < TN / 32; ++r) wb[r] = nb[r];
       const uint32_t q0 = q;
-      const int here = chunks - 4 * g;
+      const int here = chunks - 4 * g < 4 ? chunks - 4 * g : 4;
       advance();
       if (t < tiles) advance();
-      if (t < tiles) fetch();
+      for (int j = 0; j < here && ok; ++j) {
+        const uint32_t use = q0 + j;
+        ok = wait_pair(base + S::sempty + 8 * (use % kScaleBufs), ((use / kScaleBufs) & 1u) ^ 1u, abort_flag);
+      }
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= here) break;
-        const uint32_t sb = (q0 + j) % kScaleBufs, ph = ((q0 + j) / kScaleBufs) & 1u;
-        ok = wait_here(base + S::sempty + 8 * sb, ph ^ 1u, abort_flag);
-        ok = __all_sync(kFullMask, ok);
-        if (!ok) break;
-        const uint32_t sc = base + S::scales + sb * S::kScale + lane * 16;
+        const uint32_t sc = base + S::scales + ((q0 + j) % kScaleBufs) * S::kScale + lane * 16;
         sts_words(sc, word_of(wa[0], j), word_of(wa[1], j), word_of(wa[2], j), word_of(wa[3], j));
 #pragma unroll
         for (int n = 0; n < TN / 128; ++n)
           sts_words(sc + 512 * (n + 1), word_of(wb[4 * n], j), word_of(wb[4 * n + 1], j), word_of(wb[4 * n + 2], j),
                     word_of(wb[4 * n + 3], j));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(in_cta(base + S::sfull + 8 * sb, 0));
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      // the group's chunks by one release, a lane each, and the next loads behind it
+      if (lane < here) {
+        const uint32_t at = 8 * ((q0 + lane) % kScaleBufs);
+        arrive_even(base + S::sfull + at, sfull0 + at, rank);
+      }
+      if (t < tiles) fetch();
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------- epilogue ----
@@ -543,7 +558,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t staging = base + S::staging + quad * (S::kBoxes * 4096);
     const bool tma_add = kSeg && a.add && a.tma_add;
-    const uint32_t tempty[2] = {in_cta(base + S::tempty, 0), in_cta(base + S::tempty + 8, 0)};
+    const uint32_t tempty0 = in_cta(base + S::tempty, 0);
     constexpr int kCols = 128 / static_cast<int>(sizeof(T));   // columns of one 128-byte staging row
     if (lane == 0 && a.tma_out) prefetch_map(&out_map);
     if (lane == 0 && tma_add) prefetch_map(&add_map);
@@ -571,7 +586,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
 #pragma unroll
         for (int c = 0; c < TN; ++c) sum[c] = 0.0f;
         for (int g = 0; g < segments && ok; ++g, ++u) {
-          ok = wait_here(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+          ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
           ok = __all_sync(kFullMask, ok);
           if (!ok) break;
           tc_fence_after();
@@ -585,10 +600,10 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_cluster(tempty[u & 1u]);
+          if (lane == 0) arrive_even(base + S::tempty + 8 * (u & 1u), tempty0 + 8 * (u & 1u), rank);
         }
       } else {
-        ok = wait_here(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+        ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
         ok = __all_sync(kFullMask, ok);
       }
       if (tma_add && boxes > 0) {
@@ -616,7 +631,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           if (c == (TN == 256 ? 0 : TN / kCols - 1)) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(tempty[u & 1u]);
+            if (lane == 0) arrive_even(base + S::tempty + 8 * (u & 1u), tempty0 + 8 * (u & 1u), rank);
           }
         }
         const int64_t m = m0 + lane, n = n0 + static_cast<int64_t>(chunk) * kCols;

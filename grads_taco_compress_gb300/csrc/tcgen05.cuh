@@ -134,16 +134,28 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 }
 
 // ------------------------------------------------------ waits and votes ----
-// Wait for phase `parity` of `bar`. Gives up when the CTA's abort flag is set
-// or after kWaitLimitNs; the timed-out waiter sets the flag and `bit` in the
-// kernel's fault word.
+// As mbar_try_wait, on a barrier that another CTA of the cluster arrives at.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Wait for phase `parity` of `bar` (CLUSTER: one that another CTA of the
+// cluster arrives at). Gives up when the CTA's abort flag is set or after
+// kWaitLimitNs; the timed-out waiter sets the flag and `bit` in the kernel's
+// fault word.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
                                               volatile uint32_t* abort_flag,
                                               unsigned int* fault_word, unsigned int bit) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const unsigned long long t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1u;

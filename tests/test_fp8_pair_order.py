@@ -1,0 +1,34 @@
+"""How the CTA pairs of the FP8 product order memory across the two CTAs, read
+from the source: what one CTA announces to the other goes through a release at
+cluster scope and an acquire at cluster scope. A missing order need not show
+in a result, so no run can test it."""
+
+from __future__ import annotations
+
+import pathlib
+import re
+
+CSRC = pathlib.Path(__file__).resolve().parent.parent / "grads_taco_compress_gb300" / "csrc"
+
+
+def test_arrivals_at_other_ctas_release_at_cluster_scope():
+    found = 0
+    for path in sorted(CSRC.glob("*.cu*")):
+        for instr in re.findall(r"mbarrier\.arrive[\w.:]*", path.read_text()):
+            if "shared::cluster" in instr:
+                found += 1
+                assert ".release.cluster." in instr, (path.name, instr)
+    assert found
+
+
+def test_waits_of_a_pair_acquire_at_cluster_scope():
+    source = (CSRC / "fp8_matmul.cu").read_text()
+    start = source.index("matmul_pair_kernel(")
+    body = source[start:source.index("\n}\n", start)]
+    # no other CTA touches the barriers of the CTA's own copy of `add` and of its tensor core's set of scale columns
+    assert set(re.findall(r"wait_here\(base \+ S::(\w+)", body)) == {"added", "sdone"}
+    assert set(re.findall(r"wait_pair\(base \+ S::(\w+)", body)) == {"empty", "tempty", "sfull", "full", "sempty",
+                                                                     "tfull"}
+    assert "wait_or_abort<true>" in source
+    helper = (CSRC / "tcgen05.cuh").read_text()
+    assert "mbarrier.try_wait.parity.acquire.cluster." in helper
