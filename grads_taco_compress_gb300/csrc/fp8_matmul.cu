@@ -246,6 +246,9 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
 __device__ __forceinline__ void commit_here(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
+// How long the odd CTA of a pair that gives up waits for copies that it has
+// issued: thousands of times what one takes.
+constexpr unsigned long long kDrainNs = 10ull * 1000ull * 1000ull;
 // 32 consecutive fp32 columns of this thread's lane, without the wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   tmem_ld16(taddr, v);
@@ -417,6 +420,9 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     if (!ok && rank == 0) {   // copies still in flight land before the CTAs exit
       const uint32_t first = issued > static_cast<uint32_t>(S::kStages) ? issued - S::kStages : 0u;
       for (uint32_t j = first; j < issued; ++j) mbar_wait(base + S::full + 8 * (j % S::kStages), (j / S::kStages) & 1u);
+    } else if (!ok) {   // the odd CTA's, of which it may have issued more, count where it cannot wait
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < kDrainNs) __nanosleep(1000);
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -1,7 +1,8 @@
 """How the CTA pairs of the FP8 product order memory across the two CTAs, read
 from the source: what one CTA announces to the other goes through a release at
-cluster scope and an acquire at cluster scope. A missing order need not show
-in a result, so no run can test it."""
+cluster scope and an acquire at cluster scope, and a pair that gives up waits
+for the copies of both. A missing order need not show in a result, so no run
+can test it."""
 
 from __future__ import annotations
 
@@ -21,10 +22,14 @@ def test_arrivals_at_other_ctas_release_at_cluster_scope():
     assert found
 
 
-def test_waits_of_a_pair_acquire_at_cluster_scope():
+def pair_kernel():
     source = (CSRC / "fp8_matmul.cu").read_text()
     start = source.index("matmul_pair_kernel(")
-    body = source[start:source.index("\n}\n", start)]
+    return source, source[start:source.index("\n}\n", start)]
+
+
+def test_waits_of_a_pair_acquire_at_cluster_scope():
+    source, body = pair_kernel()
     # no other CTA touches the barriers of the CTA's own copy of `add` and of its tensor core's set of scale columns
     assert set(re.findall(r"wait_here\(base \+ S::(\w+)", body)) == {"added", "sdone"}
     assert set(re.findall(r"wait_pair\(base \+ S::(\w+)", body)) == {"empty", "tempty", "sfull", "full", "sempty",
@@ -32,3 +37,13 @@ def test_waits_of_a_pair_acquire_at_cluster_scope():
     assert "wait_or_abort<true>" in source
     helper = (CSRC / "tcgen05.cuh").read_text()
     assert "mbarrier.try_wait.parity.acquire.cluster." in helper
+
+
+def test_a_pair_that_gives_up_waits_for_the_copies_of_both_ctas():
+    """The copies of both CTAs count on the even one's barriers, and the odd one
+    may have issued stages that the even one has not."""
+    _, body = pair_kernel()
+    producer = body[:body.index("MMA issuer")]
+    even, odd = producer.index("if (!ok && rank == 0)"), producer.index("else if (!ok)")
+    assert "mbar_wait(base + S::full" in producer[even:odd]
+    assert "kDrainNs" in producer[odd:]
