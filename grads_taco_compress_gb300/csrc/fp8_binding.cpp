@@ -223,15 +223,37 @@ taco_status call(F&& f) {
   return st;
 }
 
+// The CUDA tensors among the arguments, those in an Fp8Tensor included, all on
+// one device: the call's kernels run on the first's and take the others'
+// addresses as they are. (What is no CUDA tensor is refused where it is read.)
+void on_one_device(PyObject* const* v, Py_ssize_t n) {
+  std::optional<c10::Device> device;
+  const auto check = [&](PyObject* o) {
+    if (!THPVariable_Check(o)) return;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) return;
+    if (!device) device = t.device();
+    if (*device != t.device())
+      refuse("the tensors of a call must be on one device, not on " + device->str() + " and " + t.device().str());
+  };
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (PyTuple_Check(v[i]))
+      for (Py_ssize_t j = 0; j < PyTuple_GET_SIZE(v[i]); ++j) check(PyTuple_GET_ITEM(v[i], j));
+    else
+      check(v[i]);
+  }
+}
+
 // Runs `body` on `count` positional arguments; C++ exceptions become Python's.
 template <typename F>
-PyObject* guarded(Py_ssize_t got, Py_ssize_t count, F&& body) {
+PyObject* guarded(PyObject* const* v, Py_ssize_t got, Py_ssize_t count, F&& body) {
   if (got != count) {
     PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", count, got);
     return nullptr;
   }
   try {
     at::AutoDispatchBelowADInplaceOrView guard;
+    on_one_device(v, got);
     return body();
   } catch (const std::invalid_argument& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
@@ -243,7 +265,7 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t count, F&& body) {
 
 // quantize(x, rows, cols, tile, out, out_t, stream) -> rows, transpose
 PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(v, n, 7, [&]() -> PyObject* {
     const bool rows = PyObject_IsTrue(v[1]), cols = PyObject_IsTrue(v[2]);
     const long tile = PyLong_AsLong(v[3]);
     if (PyErr_Occurred()) PyErr_Clear();
@@ -285,7 +307,7 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
 // rms_norm(x, weight, residual, eps, checkpoint, out, h, rstd, stream)
 //   -> y, h, rstd, checkpoint
 PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 9, [&]() -> PyObject* {
+  return guarded(v, n, 9, [&]() -> PyObject* {
     const at::Tensor& x = tensor(v[0], "x");
     const Matrix m = matrix(x, "x");
     const OnStream on(v[8], x);
@@ -338,7 +360,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 // rms_norm_backward(dy, saved, weight, rstd, dh, dx, dw, workspace, stream) -> dx, dw
 PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 9, [&]() -> PyObject* {
+  return guarded(v, n, 9, [&]() -> PyObject* {
     const at::Tensor& dy = tensor(v[0], "dy");
     const Matrix m = matrix(dy, "dy");
     const OnStream on(v[8], dy);
@@ -380,7 +402,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 // swiglu(gate_up, checkpoint, out, stream) -> y, checkpoint
 PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject* {
+  return guarded(v, n, 4, [&]() -> PyObject* {
     const at::Tensor& x = tensor(v[0], "gate_up");
     const Matrix m = matrix(x, "gate_up");
     if (m.cols < 2 || m.cols % 2) refuse("gate_up must have an even number of columns");
@@ -413,7 +435,7 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 // swiglu_backward(dy, checkpoint, out, stream) -> d gate_up
 PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject* {
+  return guarded(v, n, 4, [&]() -> PyObject* {
     const at::Tensor& dy = tensor(v[0], "dy");
     const Matrix m = matrix(dy, "dy");
     const OnStream on(v[3], dy);
@@ -438,7 +460,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 // matmul(a, b, out, out_dtype, add, stream) -> out
 PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
+  return guarded(v, n, 6, [&]() -> PyObject* {
     const Pair a = pair_of(v[0], "a"), b = pair_of(v[1], "b");
     const taco_fp8_tensor ad = describe(a.codes, a.scales, "a"), bd = describe(b.codes, b.scales, "b");
     const OnStream on(v[5], a.codes);
