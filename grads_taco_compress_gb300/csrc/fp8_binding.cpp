@@ -42,6 +42,15 @@ int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 
 bool given(PyObject* o) { return o && o != Py_None; }
 
+bool flag(PyObject* o, const char* what) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(what) + " must be true or false");
+  }
+  return v != 0;
+}
+
 const at::Tensor& tensor(PyObject* o, const char* what) {
   if (!THPVariable_Check(o)) refuse(std::string(what) + " must be a tensor");
   return THPVariable_Unpack(o);
@@ -266,7 +275,7 @@ PyObject* guarded(PyObject* const* v, Py_ssize_t got, Py_ssize_t count, F&& body
 // quantize(x, rows, cols, tile, out, out_t, stream) -> rows, transpose
 PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(v, n, 7, [&]() -> PyObject* {
-    const bool rows = PyObject_IsTrue(v[1]), cols = PyObject_IsTrue(v[2]);
+    const bool rows = flag(v[1], "rows"), cols = flag(v[2], "cols");
     const long tile = PyLong_AsLong(v[3]);
     if (PyErr_Occurred()) PyErr_Clear();
     if (tile != 1 && tile != kBlock) refuse("tile must be 1 or 128");
@@ -310,6 +319,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return guarded(v, n, 9, [&]() -> PyObject* {
     const at::Tensor& x = tensor(v[0], "x");
     const Matrix m = matrix(x, "x");
+    const bool keep = PyTuple_Check(v[4]) || flag(v[4], "checkpoint");
     const OnStream on(v[8], x);
     const at::Tensor& weight = tensor(v[1], "weight");
     void* w = vector(weight, "weight", m.cols, false);
@@ -324,7 +334,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
     std::optional<Pair> ck;
     if (PyTuple_Check(v[4]))
       ck = pair_of(v[4], "checkpoint");
-    else if (PyObject_IsTrue(v[4]))
+    else if (keep)
       ck = new_fp8({m.rows, m.cols}, 1, rstd.defined() ? nullptr : &rstd);
     Matrix r, ho;
     if (given(v[2])) {
@@ -407,13 +417,14 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const Matrix m = matrix(x, "gate_up");
     if (m.cols < 2 || m.cols % 2) refuse("gate_up must have an even number of columns");
     const int64_t F = m.cols / 2;
+    const bool keep = PyTuple_Check(v[1]) || flag(v[1], "checkpoint");
     const OnStream on(v[3], x);
     const Pair y = given(v[2]) ? pair_of(v[2], "out") : new_fp8({m.rows, F}, 1);
     const taco_fp8_tensor yd = describe(y.codes, y.scales, "out");
     std::optional<Pair> ck;
     if (PyTuple_Check(v[1]))
       ck = pair_of(v[1], "checkpoint");
-    else if (PyObject_IsTrue(v[1]))
+    else if (keep)
       ck = new_fp8({2, m.rows, F}, 1);
     taco_fp8_tensor g{}, u{};
     if (ck) {

@@ -9,7 +9,8 @@ scales that a call allocates share one allocation, and so does a norm's rstd
 with its checkpoint, or with h where there is none: holding one holds the other. The
 arguments are marshalled by a compiled module (csrc/fp8_binding.cpp): these
 calls take a few microseconds on small inputs, and so do their arguments in
-Python. Wrong arguments raise ValueError, a status of the library TacoError.
+Python. Wrong arguments (tensors on different devices among them) raise
+ValueError, a status of the library TacoError.
 
 A linear layer y = x W^T in training::
 

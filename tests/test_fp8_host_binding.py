@@ -59,3 +59,13 @@ def test_tensors_on_another_device(i, name, part):
             fake_fp8(*v.codes.shape, device=0, scales_device=1)
     with pytest.raises(ValueError, match="one device"):
         call(**kw)
+
+
+@pytest.mark.parametrize("call,kw,name", [
+    (taco.taco_fp8_quantize, dict(x=(4, 512)), "rows"), (taco.taco_fp8_quantize, dict(x=(4, 512)), "cols"),
+    (taco.taco_rms_norm_fp8, dict(x=(4, 512), weight=(512,)), "checkpoint"),
+    (taco.taco_swiglu_fp8, dict(gate_up=(4, 1024)), "checkpoint")])
+def test_flags_without_a_truth_value(call, kw, name):
+    """Such as a tensor in the place of an Fp8Tensor: refused, with the argument's name."""
+    with pytest.raises(ValueError, match=name):
+        call(**{k: fake(*shape) for k, shape in kw.items()}, **{name: torch.zeros(2)})
