@@ -79,11 +79,16 @@ class EmulatedTwoShotAllReduce:
         """Kernel launches of one AllReduce."""
         return 3 if self.batched else 2 * self.R + 1
 
-    def __call__(self, xs: torch.Tensor, stream=None) -> torch.Tensor:
-        """xs: bf16 [R, M, h], rank r's tensor in xs[r]. Returns the reduced [M, h]."""
+    def __call__(self, xs: torch.Tensor, stream=None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """xs: bf16 [R, M, h], rank r's tensor in xs[r]. Returns the reduced [M, h],
+        in ``out`` or else in the object's own buffer, which the next call overwrites."""
         R, c, h, n = self.R, self.chunk, self.h, self.block
         if xs.shape != (R, self.M, h) or xs.dtype != torch.bfloat16 or not xs.is_contiguous():
             raise ValueError(f"xs must be a contiguous bf16 tensor of shape {(R, self.M, h)}")
+        if out is None:
+            out = self.out
+        elif out.shape != (self.M, h) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous bf16 tensor of shape {(self.M, h)}")
         if self.batched:                                              # 1. compress
             self._compress(xs.view(R * R, c, h), n, self.target_energy, self.variant,
                            bundle=self.bundle_all, headers=self.headers_all,
@@ -106,8 +111,8 @@ class EmulatedTwoShotAllReduce:
                                  shard=self.reduced[dst], header=self.reduced_headers[dst],
                                  workspace=self.workspace, stream=stream)
         self._expand(self.reduced, c, h, n,                           # 4.+5. all-gather
-                     out=self.out.view(R, c, h), stream=stream)
-        return self.out
+                     out=out.view(R, c, h), stream=stream)
+        return out
 
     def capture(self, xs: torch.Tensor) -> torch.cuda.CUDAGraph:
         """Record one AllReduce of `xs` (fixed address) into a CUDA graph.

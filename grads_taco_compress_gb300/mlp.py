@@ -15,10 +15,20 @@ tensors), with the FP8 block-tensor operators between the two exchanges:
 
 Weights are bf16 masters, quantised with one scale per 128 x 128 tile by
 ``refresh`` (after every update); weight gradients are running f32 sums. As in
-``allreduce``, nothing here computes: every step is a libtaco call.
+``allreduce``, every step is a libtaco call, but for the addition of the norm
+weight's gradient to its running sum.
+
+Several forward passes may be open at a time (micro-batches)::
+
+    out1, h1 = block.forward(x1, r1); saved1 = block.saved
+    out2, h2 = block.forward(x2, r2); saved2 = block.saved
+    dx1 = block.backward(dout1, dh1, saved1)
+    dx2 = block.backward(dout2, dh2, saved2)
 """
 
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import torch
 
@@ -27,8 +37,20 @@ from . import fp8 as F
 from .allreduce import EmulatedTwoShotAllReduce
 
 
+class MlpSaved(NamedTuple):
+    """What a forward pass keeps for its backward pass: the norm's output, rstd
+    and checkpoint, and each rank's gated output with the checkpoint of gate and
+    up. All in 8 bits but rstd; h itself is the caller's alone."""
+
+    y: F.Fp8Tensor
+    rstd: torch.Tensor
+    checkpoint: F.Fp8Tensor
+    gated: tuple
+
+
 class TensorParallelMlp:
-    """Weights, gradients and the launch sequence of one block."""
+    """Weights, gradients and the launch sequence of one block. ``saved``: the
+    MlpSaved of the last forward pass, None once its backward pass has run."""
 
     def __init__(self, R: int, M: int, h: int, f: int, block: int = 128, eps: float = 1e-6, device="cuda"):
         """R ranks, M tokens, hidden size h, f gated channels in all (f / R a
@@ -50,6 +72,8 @@ class TensorParallelMlp:
         self.part = torch.empty((R, M, h), dtype=torch.bfloat16, device=dev)
         self.reduce_forward = EmulatedTwoShotAllReduce(R, M, h, block, device=dev)
         self.reduce_backward = EmulatedTwoShotAllReduce(R, M, h, block, device=dev)
+        self.saved = None
+        self._replaced = False      # a forward pass took the place of a saved state
         self.refresh()
 
     def refresh(self) -> None:
@@ -57,24 +81,36 @@ class TensorParallelMlp:
         self._in = [F.taco_fp8_quantize(w, cols=True, tile=F.BLOCK) for w in self.w_in]
         self._out = [F.taco_fp8_quantize(w, cols=True, tile=F.BLOCK) for w in self.w_out]
 
-    def forward(self, x: torch.Tensor, residual: torch.Tensor):
-        """bf16 x, residual [M, h] -> (the block's output [M, h], the residual
-        stream x + residual [M, h])."""
-        self.norm = n = F.taco_rms_norm_fp8(x, self.w_norm, residual, self.eps, checkpoint=True)
-        self.gated = []
+    def forward(self, x: torch.Tensor, residual: torch.Tensor, out: torch.Tensor | None = None):
+        """bf16 x, residual [M, h] -> (the block's output [M, h], in ``out`` or a
+        new tensor, and the residual stream x + residual [M, h])."""
+        if out is None:
+            out = torch.empty((self.M, self.h), dtype=torch.bfloat16, device=self.part.device)
+        n = F.taco_rms_norm_fp8(x, self.w_norm, residual, self.eps, checkpoint=True)
+        gated = []
         for r in range(self.R):
             y, kept = F.taco_swiglu_fp8(F.taco_matmul_fp8(n.y, self._in[r][0]), checkpoint=True)
             F.taco_matmul_fp8(y, self._out[r][0], out=self.part[r])
-            self.gated.append((y, kept))
-        return self.reduce_forward(self.part), n.h
+            gated.append((y, kept))
+        self.reduce_forward(self.part, out=out)
+        self._replaced = self.saved is not None
+        self.saved = MlpSaved(n.y, n.rstd, n.checkpoint, tuple(gated))
+        return out, n.h
 
-    def backward(self, dout: torch.Tensor, dh: torch.Tensor | None = None) -> torch.Tensor:
-        """dout: gradient of the output, dh: of the residual stream. Returns the
-        gradient of x and of residual; the weights' are added to dw_*."""
-        n = self.norm
+    def backward(self, dout: torch.Tensor, dh: torch.Tensor | None = None,
+                 saved: MlpSaved | None = None) -> torch.Tensor:
+        """dout: gradient of the output, dh: of the residual stream, of the forward
+        pass that left ``saved`` (None: the last one, the only one open). Returns
+        the gradient of x and of residual; the weights' are added to dw_*."""
+        if saved is None:
+            if self.saved is None:
+                raise ValueError("no forward pass to go back through")
+            if self._replaced:
+                raise ValueError("more than one forward pass since the last backward: pass the saved state of one")
+            saved = self.saved
         dq, dt = F.taco_fp8_quantize(dout, cols=True)
-        _, nt = F.taco_fp8_quantize(n.y, rows=False, cols=True)
-        for r, (y, kept) in enumerate(self.gated):
+        _, nt = F.taco_fp8_quantize(saved.y, rows=False, cols=True)
+        for r, (y, kept) in enumerate(saved.gated):
             _, yt = F.taco_fp8_quantize(y, rows=False, cols=True)
             F.taco_matmul_fp8(dt, yt, out=self.dw_out[r], add=self.dw_out[r])
             dgu = F.taco_swiglu_fp8_backward(F.taco_matmul_fp8(dq, self._out[r][1]), kept)
@@ -82,6 +118,8 @@ class TensorParallelMlp:
             F.taco_matmul_fp8(gt, nt, out=self.dw_in[r], add=self.dw_in[r])
             F.taco_matmul_fp8(gq, self._in[r][1], out=self.part[r])
         dn = self.reduce_backward(self.part)
-        dx, dw = F.taco_rms_norm_fp8_backward(dn, n.checkpoint, self.w_norm, n.rstd, dh=dh)
+        dx, dw = F.taco_rms_norm_fp8_backward(dn, saved.checkpoint, self.w_norm, saved.rstd, dh=dh)
         self.dw_norm += dw
+        if saved is self.saved:
+            self.saved, self._replaced = None, False
         return dx
