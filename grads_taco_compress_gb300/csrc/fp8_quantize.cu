@@ -392,9 +392,14 @@ transpose_codes_kernel(QuantizeArgs a, Divider per_row) {
   store_transposed(a, words, r0, c0, lane8, r4);
 }
 
-// CTAs per SM that the tile kernel's registers are held to (bf16, rows and
-// transpose of 8192 x 4096: 2: 54 us, 4: 33 us; more, and more for the wider
-// sources and the tiles, spill).
+// CTAs per SM that the tile kernel's registers are held to, with 2, 3 and 4 (and
+// the bytes that the aligned form with the transpose then spills):
+//   16-bit rows and transpose, 8192 x 4096     27.4 (0), 27.7 (0), 25.5 us (8)
+//   16-bit 128 x 128 tiles, 16384 x 4096       53.2 (0), 46.3 (108), 55.8 us (240)
+//   codes, rows and transpose, 8192 x 4096     49.8 (0), 43.9 (92), 49.4 us (232)
+//   codes, 128 x 128 tiles, 8192 x 4096        43.2 (0), 38.5 (84), 43.5 us (220)
+//   f32 rows and transpose, 8192 x 4096        41.4 (0), 41.8 (156), 76.0 us (760)
+//   f32 128 x 128 tiles, 16384 x 4096          62.3 (0), 61.1 (100), 125 us (864)
 template <typename T, bool TILE>
 constexpr int tile_ctas() {
   return std::is_same<T, float>::value ? 2 : std::is_same<T, Fp8Source>::value || TILE ? 3 : 4;
