@@ -209,6 +209,14 @@ __device__ __forceinline__ void arrive_even(uint32_t bar, uint32_t even_bar, uin
   else
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(even_bar) : "memory");
 }
+// The same for accumulators that this warp has read. No memory is announced, and
+// the fence of the tensor-memory loads (tc_fence_before) orders them before any
+// execution-ordering operation, so the arrival needs no release, whose latency
+// would lie between the tiles (16384 x 4096 x 3584: 136 us, 142 with a release;
+// f32, 8192 x 4096 x 8192: 213 and 224).
+__device__ __forceinline__ void arrive_even_read(uint32_t even_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(even_bar) : "memory");
+}
 __device__ __forceinline__ void tma_load_2d_plain(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -277,8 +285,8 @@ struct TileMap {
 // Chunks whose scale words may wait in shared memory: two groups of 4, one of
 // either warp that brings them. A warp stalls for the latency of its loads and
 // of the release to the other CTA once a group, and the other group (16 blocks)
-// covers it. 16384 x 4096 x 3584: 139 us; 141 with a release a chunk and the
-// next loads in front of it (f32, 8192 x 4096 x 8192: 223 and 231).
+// covers it (a release a chunk, the next loads in front of it, took 1% more for
+// 16384 x 4096 x 3584 and 4% for f32, 8192 x 4096 x 8192).
 constexpr int kScaleBufs = 8;
 
 template <int TN>
@@ -606,7 +614,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_even(base + S::tempty + 8 * (u & 1u), tempty0 + 8 * (u & 1u), rank);
+          if (lane == 0) arrive_even_read(tempty0 + 8 * (u & 1u));
         }
       } else {
         ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
@@ -637,7 +645,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
           if (c == (TN == 256 ? 0 : TN / kCols - 1)) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_even(base + S::tempty + 8 * (u & 1u), tempty0 + 8 * (u & 1u), rank);
+            if (lane == 0) arrive_even_read(tempty0 + 8 * (u & 1u));
           }
         }
         const int64_t m = m0 + lane, n = n0 + static_cast<int64_t>(chunk) * kCols;
