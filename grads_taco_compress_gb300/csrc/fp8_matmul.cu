@@ -670,7 +670,9 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
         }
 #pragma unroll
         for (int p = 0; p < 8; ++p) sts128(row + 16 * (p ^ (lane & 7)), pack16<T>(v + p * (kCols / 8)));
-        if (a.tma_out) {
+        // a tensor copy to memory ends on 16 bytes and takes what lies behind the row
+        // with it, so rows that end elsewhere are finished by plain stores
+        if (a.tma_out && (n + kCols <= a.N || ((a.N - n) * static_cast<int>(sizeof(T))) % 16 == 0)) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && m0 < a.M && n < a.N) {
