@@ -27,7 +27,9 @@ struct Region {
   int64_t rows = 0, width = 0, pitch = 0;
   uintptr_t end() const { return p + static_cast<uintptr_t>((rows - 1) * pitch + width); }
   bool empty() const { return rows <= 0 || p == 0; }
-  bool same(const Region& o) const { return p == o.p && pitch == o.pitch && width == o.width && rows == o.rows; }
+  bool same(const Region& o) const {
+    return p == o.p && width == o.width && rows == o.rows && (rows == 1 || pitch == o.pitch);
+  }
 };
 // Whether two regions may share a byte. Rows that interleave without touching
 // (two halves of one wider matrix) do not.

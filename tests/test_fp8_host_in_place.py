@@ -42,3 +42,16 @@ def test_named_inputs_stay_in_place(lib):
     for dg, du in ((A, 6 * A), (6 * A, A)):
         assert lib.taco_swiglu_fp8_backward(A, 256, fp8(2, 4, 256), fp8(3, 4, 256), BF16, 4, 256, dg, 256, du, 256,
                                             None) == CUDA
+
+
+def test_one_row_in_place_whatever_the_stride(lib):
+    """The stride of a single row describes nothing: dy as the first half of a [1, 2 F] gradient."""
+    for dg, du in ((A, A + 512), (A - 512, A)):
+        assert lib.taco_swiglu_fp8_backward(A, 256, fp8(2, 1, 256), fp8(3, 1, 256), BF16, 1, 256, dg, 512, du, 512,
+                                            None) == CUDA
+    assert _norm(lib, M=1, h=A, ldx=300, y=fp8(6, 1, 256), ck=fp8(7, 1, 256)) == CUDA
+    assert _norm_backward(lib, M=1, dx=A, lddy=300, ck=fp8(2, 1, 256)) == CUDA
+    assert lib.taco_matmul_fp8(fp8(1, 1, 256), fp8(2, 64, 256), 3 * A, 64, 3 * A, 128, F32, None) == CUDA
+    # another width or start of the same memory is still no input in place
+    assert lib.taco_swiglu_fp8_backward(A, 256, fp8(2, 1, 256), fp8(3, 1, 256), BF16, 1, 256, A + 64, 512, 6 * A, 512,
+                                        None) == ARG
