@@ -25,14 +25,15 @@
 // Every wait is bounded in time with a CTA-wide abort flag.
 //
 // Measured (twice the measured bf16 rate of a library product is 3.94 PFLOP/s):
-// 16384 x 4096 x 3584 to bf16 135 us, 3.56 PFLOP/s, tensor pipe 79% active, and
-// 160 us (3.0 PFLOP/s) in a second-long loop under the power limit; the MMAs
+// 16384 x 4096 x 3584 to bf16 136 us, 3.53 PFLOP/s, tensor pipe 80% active, and
+// 162 us (2.97 PFLOP/s) in a second-long loop under the power limit; the MMAs
 // without copies 120 us, the copies without MMAs 89 us: both go through shared
 // memory, 32 KB in and 32 KB or more out a block of 128 columns. 1600 x 4096 x
 // 8190 to f32 with add 54 us, 2.0 PFLOP/s, pipe 48%: a tile 128 columns wide
 // moves a third more bytes a product, and 224 tiles are 2.95 waves of pairs.
-// Few rows: 8 x 4096 x 4096 5.5 us, from launch to the last store of which the
-// weights' 16.8 MB would take 2.5; 1 x 16384 x 4096 13.5 us, 5.0 TB/s.
+// Few rows: 8 x 4096 x 4096 6.5 us over weights that come from memory, whose 16.8
+// MB would take 2.5, and 5.5 us where they are in L2 from the call before; 1 x
+// 16384 x 4096 13.6 us, 4.9 TB/s.
 
 #include "fp8_block.cuh"
 #include "tcgen05.cuh"
@@ -1072,10 +1073,10 @@ cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cuda
 // block of 128 columns of K takes either kernel about 0.25 us, and the cluster's
 // barriers and sums cost it about 4 us more than a pair's epilogue: the split
 // pays where it takes kFewSaves blocks off each CTA. N = K = 4096, bf16: 128
-// rows (24 blocks less) 7.9 us split, 8.5 in pairs; 256 rows (16 less) 10.4 and
-// 9.0; 256 rows at K = 16384 (64 less) 24.0 and 33.2. Pairs take tiles 128
-// columns wide where that is one wave (256 rows: 9.0 us, 13.5 at 256 wide),
-// else 256 wide (1024 rows: 15.6 us, 18.5 at 128 wide); f32 always 128, whose
+// rows (24 blocks less) 7.8 us split, 8.9 in pairs; 256 rows (16 less) 10.3 and
+// 9.4; 256 rows at K = 16384 (64 less) 23.8 and 32.9. Pairs take tiles 128
+// columns wide where that is one wave (256 rows: 9.4 us, 14.0 at 256 wide),
+// else 256 wide (1024 rows: 15.7 us, 18.4 at 128 wide); f32 always 128, whose
 // sum its epilogue can hold.
 constexpr int kFewSaves = 24;
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st) {

@@ -1,8 +1,8 @@
 """How the CTA pairs of the FP8 product order memory across the two CTAs, read
 from the source: what one CTA announces to the other goes through a release at
-cluster scope (or the fence of tensor memory) and an acquire at cluster scope, and a pair that gives up waits
-for the copies of both. A missing order need not show in a result, so no run
-can test it."""
+cluster scope (or the fence of tensor memory) and an acquire at cluster scope,
+and a pair that gives up waits for the copies of both. A missing order need not
+show in a result, so no run can test it."""
 
 from __future__ import annotations
 
