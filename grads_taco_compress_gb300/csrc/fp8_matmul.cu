@@ -26,7 +26,7 @@
 //
 // Measured (twice the measured bf16 rate of a library product is 3.94 PFLOP/s):
 // 16384 x 4096 x 3584 to bf16 136 us, 3.53 PFLOP/s, tensor pipe 80% active, and
-// 162 us (2.97 PFLOP/s) in a second-long loop under the power limit; the MMAs
+// 157 us (3.06 PFLOP/s) in a second-long loop under the power limit; the MMAs
 // without copies 120 us, the copies without MMAs 89 us: both go through shared
 // memory, 32 KB in and 32 KB or more out a block of 128 columns. 1600 x 4096 x
 // 8190 to f32 with add 54 us, 2.0 PFLOP/s, pipe 48%: a tile 128 columns wide

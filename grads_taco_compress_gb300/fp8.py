@@ -105,7 +105,8 @@ def taco_fp8_quantize(x, rows: bool = True, cols: bool = False, tile: int = 1, o
                       out_t: Fp8Tensor | None = None, stream=None):
     """x [M, K] (bf16, f16, f32 or an Fp8Tensor) -> (its rows as an Fp8Tensor
     [M, K] or None, its transpose as one [K, M] or None), from one read. tile:
-    128 for one scale per 128 x 128 tile (weights)."""
+    128 for one scale per 128 x 128 tile (weights). ``out`` and ``out_t`` are
+    where the two go; one whose flag is not set is left alone."""
     r = _binding().quantize(x, rows, cols, tile, out, out_t, _handle(stream))
     if type(r) is int:
         _check(r, "taco_fp8_quantize")
