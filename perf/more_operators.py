@@ -19,7 +19,7 @@ What is rounded to 8 bits, or to a 16-bit parameter that has no 32-bit master,
 in an AdamW step is rounded up or down by a threshold that runs through a Weyl
 sequence over steps and elements, so that changes far below half a step of the
 type are kept on average:
-    u = frac(i 0x9E3779B1 / 2^32 + t 0x85EBCA6B / 2^32),   element i, step t
+    u = frac(i 0xC13FA9A9 / 2^32 + t 0x9E3779B1 / 2^32),   element i, step t
     |x| -> step floor(|x| / step + u),  step: the type's at |x|
 A second moment that is not zero is never rounded to zero.
 
@@ -37,7 +37,7 @@ BLOCK = 128
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32, "fp8": torch.float8_e4m3fn}
 SIZE = {"bf16": 2, "f16": 2, "f32": 4, "fp8": 1}
 BETA1, BETA2, EPS, DECAY, LR = 0.9, 0.95, 1e-8, 0.1, 3e-4
-WEYL_I, WEYL_T = 0x9E3779B1, 0x85EBCA6B
+WEYL_I, WEYL_T = 0xC13FA9A9, 0x9E3779B1
 VECTOR = 32768   # parameters with fewer elements are norm weights and biases: 32 bits, no decay
 
 
