@@ -49,6 +49,7 @@ EXPORTED_SYMBOLS = (
     "taco_decompress_shards", "taco_decompress_shards_ptrs",
     "taco_e4m3_encode_f32", "taco_e4m3_decode_f32",
     "taco_fp8_quantize", "taco_fp8_requantize",
+    "taco_adamw", "taco_grad_norm", "taco_grad_norm_workspace_bytes",
     "taco_rms_norm_fp8", "taco_rms_norm_workspace_bytes", "taco_rms_norm_fp8_backward",
     "taco_swiglu_fp8", "taco_swiglu_fp8_backward", "taco_matmul_fp8",
     "taco_get_fault", "taco_selftest_wait_timeout",
@@ -74,8 +75,8 @@ def _lib() -> ctypes.CDLL:
                 f"libtaco is not built ({LIB_PATH} missing): run "
                 "`python -m grads_taco_compress_gb300.build_lib` first")
         lib = ctypes.CDLL(str(LIB_PATH))
-        i64, i32, sz, vp, f32 = (ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
-                                 ctypes.c_void_p, ctypes.c_float)
+        i64, i32, sz, vp, f32, f64 = (ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
+                                      ctypes.c_void_p, ctypes.c_float, ctypes.c_double)
         sig = {
             "taco_shard_bytes": (sz, [i64, i64, i32]),
             "taco_shard_scales_offset": (sz, [i64, i64, i32]),
@@ -112,6 +113,9 @@ def _lib() -> ctypes.CDLL:
             "taco_swiglu_fp8": (i32, [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, vp]),
             "taco_swiglu_fp8_backward": (i32, [vp, i64, vp, vp, i32, i64, i64, vp, i64, vp, i64, vp]),
             "taco_matmul_fp8": (i32, [vp, vp, vp, i64, vp, i64, i32, vp]),
+            "taco_adamw": (i32, [vp, i64, f64, vp, f64, f64, f64, vp, vp, vp]),
+            "taco_grad_norm_workspace_bytes": (sz, [i64]),
+            "taco_grad_norm": (i32, [vp, i64, f64, vp, vp, sz, vp]),
             "taco_get_fault": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
             "taco_selftest_wait_timeout": (i32, [ctypes.c_uint64, vp, vp]),
             "taco_status_string": (ctypes.c_char_p, [i32]),

@@ -1,4 +1,5 @@
-// Compiled argument marshalling of the FP8 block-tensor entry points (fp8.py).
+// Compiled argument marshalling of the FP8 block-tensor entry points (fp8.py)
+// and of those over many tensors (optim.py).
 //
 // These calls take and return several tensors each and run for a few
 // microseconds on small inputs, where building the arguments in Python took
@@ -19,6 +20,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include <ATen/ATen.h>
 #include <ATen/EmptyTensor.h>
@@ -493,6 +495,181 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------- many tensors ----
+// A list or tuple of the caller's, held while its items are used.
+class Items {
+ public:
+  Items(PyObject* o, const char* what) : what_(what) {
+    if (!PyList_Check(o) && !PyTuple_Check(o)) refuse(std::string(what) + " must be a list or a tuple");
+    fast_ = PySequence_Fast(o, "");
+    if (!fast_) throw std::bad_alloc();
+  }
+  Items(PyObject* o, const char* what, Py_ssize_t n) : Items(o, what) {
+    if (size() != n) {
+      Py_DECREF(fast_);
+      refuse(std::string(what) + " must have as many items as there are parameters");
+    }
+  }
+  Items(const Items&) = delete;
+  Items& operator=(const Items&) = delete;
+  ~Items() { Py_DECREF(fast_); }
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(fast_); }
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast_, i); }
+  std::string name(Py_ssize_t i) const { return std::string(what_) + "[" + std::to_string(i) + "]"; }
+
+ private:
+  const char* what_;
+  PyObject* fast_;
+};
+
+// The device that every tensor of a call is on.
+class Device {
+ public:
+  const at::Tensor& operator()(const at::Tensor& t, const std::string& what) {
+    if (!t.is_cuda()) refuse(what + " must be a CUDA tensor");
+    if (!device_) device_ = t.device();
+    if (*device_ != t.device())
+      refuse("the tensors of a call must be on one device, not on " + device_->str() + " and " + t.device().str());
+    return t;
+  }
+  c10::Device get() const { return *device_; }
+
+ private:
+  std::optional<c10::Device> device_;
+};
+
+double number(PyObject* o, const char* what) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(what) + " must be a number");
+  }
+  return v;
+}
+const at::Tensor& dense(const at::Tensor& t, const std::string& what) {
+  if (dtype_of(t.scalar_type()) < 0 || !t.is_contiguous())
+    refuse(what + " must be a contiguous bf16, f16 or f32 tensor");
+  return t;
+}
+const at::Tensor& dense_f32(const at::Tensor& t, const std::string& what, int64_t n) {
+  if (t.scalar_type() != at::kFloat || !t.is_contiguous() || t.numel() != n)
+    refuse(what + " must be a contiguous f32 tensor of " + std::to_string(n) + " elements");
+  return t;
+}
+// Codes and scales of a state [1, n].
+void state_pair(PyObject* o, const std::string& what, int64_t n, Device& device, void** codes, uint8_t** scales) {
+  const Pair p = pair_of(o, what.c_str());
+  device(p.codes, what);
+  device(p.scales, what);
+  const int64_t kb = (n + kBlock - 1) / kBlock;
+  if (p.codes.scalar_type() != at::kByte || p.scales.scalar_type() != at::kByte || p.codes.numel() != n ||
+      p.scales.numel() != kb || !p.codes.is_contiguous() || !p.scales.is_contiguous())
+    refuse(what + " must be contiguous uint8 codes [1, " + std::to_string(n) + "] and scales [1, " +
+           std::to_string(kb) + "]");
+  *codes = p.codes.data_ptr();
+  *scales = static_cast<uint8_t*>(p.scales.data_ptr());
+}
+
+// adamw(params, grads, states, counter, lr, beta1, beta2, eps, weight_decay, grad_scale, masters, stream)
+PyObject* adamw(PyObject*, PyObject* const* v, Py_ssize_t got) {
+  return guarded(v, got, 12, [&]() -> PyObject* {
+    const Items params(v[0], "params");
+    const Py_ssize_t n = params.size();
+    const Items grads(v[1], "grads", n), states(v[2], "states", n);
+    std::optional<Items> masters, decays;
+    if (given(v[10])) masters.emplace(v[10], "masters", n);
+    if (PyList_Check(v[8]) || PyTuple_Check(v[8])) decays.emplace(v[8], "weight_decay", n);
+    const double decay = decays ? 0.0 : number(v[8], "weight_decay");
+    Device device;
+    const at::Tensor& counter = device(tensor(v[3], "counter"), "counter");
+    if (counter.scalar_type() != at::kInt || counter.numel() != 2 || !counter.is_contiguous())
+      refuse("counter must be a contiguous int32 tensor [2]");
+    const float *lr_dev = nullptr, *scale = nullptr;
+    double lr = 0.0;
+    if (THPVariable_Check(v[4]))
+      lr_dev = static_cast<float*>(dense_f32(device(tensor(v[4], "lr"), "lr"), "lr", 1).data_ptr());
+    else
+      lr = number(v[4], "lr");
+    if (given(v[9]))
+      scale = static_cast<float*>(
+          dense_f32(device(tensor(v[9], "grad_scale"), "grad_scale"), "grad_scale", 1).data_ptr());
+    const double beta1 = number(v[5], "betas"), beta2 = number(v[6], "betas"), eps = number(v[7], "eps");
+    std::vector<taco_adamw_tensor> list(static_cast<size_t>(n));
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      taco_adamw_tensor& t = list[static_cast<size_t>(i)];
+      const at::Tensor& p = dense(device(tensor(params[i], "params"), params.name(i)), params.name(i));
+      const at::Tensor& g = dense(device(tensor(grads[i], "grads"), grads.name(i)), grads.name(i));
+      if (g.sizes() != p.sizes()) refuse(grads.name(i) + " must have its parameter's shape");
+      if (g.scalar_type() != p.scalar_type() && g.scalar_type() != at::kFloat)
+        refuse(grads.name(i) + " must have its parameter's type, or f32");
+      t.n = p.numel();
+      t.param = p.data_ptr();
+      t.grad = g.data_ptr();
+      t.param_dtype = dtype_of(p.scalar_type());
+      t.grad_dtype = dtype_of(g.scalar_type());
+      t.weight_decay = static_cast<float>(decays ? number((*decays)[i], "weight_decay") : decay);
+      if (masters && given((*masters)[i])) {
+        if (p.scalar_type() == at::kFloat) refuse(masters->name(i) + ": an f32 parameter has no master");
+        t.master = static_cast<float*>(
+            dense_f32(device(tensor((*masters)[i], "masters"), masters->name(i)), masters->name(i), t.n).data_ptr());
+      }
+      PyObject* const s = states[i];
+      if (!PyTuple_Check(s) || PyTuple_GET_SIZE(s) != 2) refuse(states.name(i) + " must be an AdamState");
+      PyObject *const m = PyTuple_GET_ITEM(s, 0), *const r = PyTuple_GET_ITEM(s, 1);
+      if (PyTuple_Check(m) != PyTuple_Check(r)) refuse(states.name(i) + ": both states in 8 bits, or both f32");
+      if (PyTuple_Check(m)) {
+        state_pair(m, states.name(i) + ".m", t.n, device, &t.m, &t.m_scales);
+        state_pair(r, states.name(i) + ".v", t.n, device, &t.v, &t.v_scales);
+      } else {
+        t.m = dense_f32(device(tensor(m, "states"), states.name(i)), states.name(i) + ".m", t.n).data_ptr();
+        t.v = dense_f32(device(tensor(r, "states"), states.name(i)), states.name(i) + ".v", t.n).data_ptr();
+      }
+    }
+    const OnStream on(v[11], counter);
+    void* stream = on.handle();
+    const taco_status st = call([&] {
+      return taco_adamw(list.data(), n, lr, lr_dev, beta1, beta2, eps, scale, static_cast<int32_t*>(counter.data_ptr()),
+                        stream);
+    });
+    return st != TACO_OK ? PyLong_FromLong(st) : none();
+  });
+}
+
+// grad_norm(grads, max_norm, out, workspace, stream) -> out
+PyObject* grad_norm(PyObject*, PyObject* const* v, Py_ssize_t got) {
+  return guarded(v, got, 5, [&]() -> PyObject* {
+    const Items grads(v[0], "grads");
+    const Py_ssize_t n = grads.size();
+    if (n == 0) refuse("grads must hold a tensor");
+    const double most = number(v[1], "max_norm");
+    Device device;
+    std::vector<taco_grad_tensor> list(static_cast<size_t>(n));
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const at::Tensor& g = dense(device(tensor(grads[i], "grads"), grads.name(i)), grads.name(i));
+      list[static_cast<size_t>(i)] = {g.data_ptr(), g.numel(), dtype_of(g.scalar_type())};
+    }
+    const OnStream on(v[4], THPVariable_Unpack(grads[0]));
+    const int64_t need = static_cast<int64_t>(taco_grad_norm_workspace_bytes(n));
+    at::Tensor out, ws;
+    if (given(v[2]))
+      out = dense_f32(device(tensor(v[2], "out"), "out"), "out", 2);
+    else
+      out = empty_vector(2, at::kFloat);
+    if (given(v[3])) {
+      ws = device(tensor(v[3], "workspace"), "workspace");
+      if (!ws.is_contiguous()) refuse("workspace must be a contiguous CUDA tensor");
+    } else {
+      ws = empty_vector(need, at::kByte);
+    }
+    void* stream = on.handle();
+    const taco_status st = call([&] {
+      return taco_grad_norm(list.data(), n, most, static_cast<float*>(out.data_ptr()), ws.data_ptr(), ws.nbytes(),
+                            stream);
+    });
+    return st != TACO_OK ? PyLong_FromLong(st) : object(out);
+  });
+}
+
 // types(Fp8Tensor, RmsNormOutput)
 PyObject* types(PyObject*, PyObject* const* v, Py_ssize_t n) {
   for (Py_ssize_t i = 0; i < n; ++i)
@@ -513,6 +690,7 @@ PyObject* types(PyObject*, PyObject* const* v, Py_ssize_t n) {
 PyMethodDef kMethods[] = {TACO_METHOD(types), TACO_METHOD(quantize), TACO_METHOD(rms_norm),
                           TACO_METHOD(rms_norm_backward),
                           TACO_METHOD(swiglu), TACO_METHOD(swiglu_backward), TACO_METHOD(matmul),
+                          TACO_METHOD(adamw), TACO_METHOD(grad_norm),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8_binding", "Argument marshalling of the FP8 entry points.", -1,
                        kMethods, nullptr, nullptr, nullptr, nullptr};

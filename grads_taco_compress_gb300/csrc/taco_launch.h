@@ -258,4 +258,46 @@ cudaError_t prepare_matmul(int* clusters);
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
 cudaError_t matmul_fault(unsigned int* bits, bool clear);
 
+// ---- Many tensors at once (adamw.cu, grad_norm.cu) ----
+struct AdamwEntry {
+  void* param;
+  const void* grad;
+  float* master;            // may be null
+  void* m;                  // fp32, or codes
+  void* v;                  // fp32, or codes of the root
+  uint8_t* m_scales;        // null: 32-bit states
+  uint8_t* v_scales;
+  int64_t n;
+  uint32_t first;           // number of its first chunk
+  float decay;
+  bool wide;                // every pointer to elements on 32 bytes
+};
+struct AdamwArgs {
+  uint32_t chunks;
+  bool last;                // of the step's launches: counts it
+  float b1, one_b1, b2, one_b2, log_b1, log_b2, eps, lr;
+  const float* lr_dev;      // null: lr
+  const float* factor;      // null: 1
+  int32_t* counter;         // steps done, CTAs arrived
+};
+// Tensors of one launch: a table that fits what launches cost least with, and
+// one that fills the 32764 bytes that a kernel's parameters may take.
+constexpr int kAdamwFew = 40, kAdamwMany = 400;
+// One launch over tensors of the same types and forms.
+cudaError_t launch_adamw(const AdamwArgs& a, const AdamwEntry* entries, int count, int param_dtype, int grad_dtype,
+                         bool small, bool vec, int sms, cudaStream_t st);
+struct GradEntry {
+  const void* p;
+  int64_t n;
+  uint32_t first;
+  int16_t dtype;
+  bool vec, wide;           // p on 16 bytes, on 32
+};
+constexpr int kNormFew = 128, kNormMany = 1300;
+constexpr int kNormCtas = 1024;   // most CTAs, and so partial sums, of a launch
+// Partial sums of squares of one launch to partial[0 .. the returned CTAs - 1].
+cudaError_t launch_grad_squares(const GradEntry* entries, int count, uint32_t chunks, int sms, double* partial,
+                                int* ctas, cudaStream_t st);
+cudaError_t launch_grad_norm(const double* partial, int count, float most, float* out, cudaStream_t st);
+
 }  // namespace taco

@@ -460,6 +460,77 @@ taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy,
 taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, const void* add,
                             int64_t ldadd, void* out, int64_t ldo, int dtype, void* stream);
 
+/* ---- Many tensors at once ---------------------------------------------------
+ * What a training step does with a model's gradients: their norm, and an AdamW
+ * step. A call takes a host array of `count` tensors (0 .. 2^20, read before
+ * the call returns), contiguous on the device, of n elements each (n == 0 is
+ * valid; 2^40 elements in all). Tensors that start on 16 bytes are read and
+ * written faster. What a call writes shares no byte with anything else that it
+ * is given. One launch takes up to 400 tensors of one combination of types
+ * (AdamW) or 1300 of any (norm); others follow in the same stream. */
+typedef struct taco_grad_tensor {
+  const void* data;
+  int64_t n;
+  int32_t dtype;
+} taco_grad_tensor;
+
+/* out[0] = the square root of the sum of the squares of all elements, out[1] =
+ * the factor that clips it: max_norm / out[0] where out[0] > max_norm, else 1,
+ * and NaN where out[0] is infinite or NaN (taco_adamw then changes nothing).
+ * Squares are formed and summed in fp32 by threads, their sums in fp64, all in
+ * a fixed order: magnitudes up to 2^63 and down to 2^-63 are fully counted.
+ * max_norm >= 0, infinity included. `workspace`: taco_grad_norm_workspace_bytes
+ * bytes, 8-byte aligned, need not be zeroed. */
+size_t taco_grad_norm_workspace_bytes(int64_t count);
+taco_status taco_grad_norm(const taco_grad_tensor* tensors, int64_t count, double max_norm, float* out,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* A parameter with its gradient and states. States in 32 bits: m and v are f32
+ * [n], the first and the second moment, and both scales are NULL. In 8 bits: m
+ * and v are E4M3 codes [n] (16-byte aligned) of the first moment and of the
+ * square ROOT of the second, with one E8M0 scale byte per 128 elements in
+ * m_scales and v_scales [ceil(n / 128)]: FP8 block tensors [1, n], tile_rows 1.
+ * All start at zero. master (f32 [n], NULL: none) holds a 16-bit parameter's
+ * exact value, of which `param` is then the rounded copy. grad_dtype is
+ * param_dtype or TACO_DTYPE_F32. */
+typedef struct taco_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* m_scales;
+  uint8_t* v_scales;
+  int64_t n;
+  float weight_decay;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+} taco_adamw_tensor;
+
+/* One AdamW step of all tensors, in place, in fp32. With t = counter[0] + 1,
+ * g = grad_scale * grad and x the parameter (or its master):
+ *   m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *   x = x (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * counter (device, int32 [2], zero at first) holds the steps done and a word
+ * of the call's own; the call counts one more, as its last act. lr_dev and
+ * grad_scale (device, f32; NULL: lr, and 1) are read when the step runs, so a
+ * captured call can be replayed with another rate and scale, and takes the next
+ * step each time. A grad_scale that is infinite or NaN leaves everything as it
+ * was, the counter too.
+ * Parameters with a master are rounded to nearest. States in 8 bits, and 16-bit
+ * parameters without a master, are rounded to floor(|x| / s + u) s, s the step
+ * of the type at x (of E4M3 under the block's scale, chosen as everywhere), by
+ * thresholds u = ((i 0xC13FA9A9 + t 0x9E3779B1) mod 2^32) / 2^32 of the element
+ * i of a tensor, which take all values in [0, 1) evenly over the steps: changes
+ * far below s are kept on average (a 16-bit parameter that this takes beyond its
+ * type's largest value becomes infinite). The root of a second moment that is not zero
+ * gets no zero code. A block with an infinity or a NaN becomes NaN.
+ * 0 <= beta1, beta2 < 1; eps > 0. Calls on the same tensors or counter must be
+ * in order on one stream. */
+taco_status taco_adamw(const taco_adamw_tensor* tensors, int64_t count, double lr, const float* lr_dev,
+                       double beta1, double beta2, double eps, const float* grad_scale, int32_t* counter,
+                       void* stream);
+
 /* ---- Device faults ---------------------------------------------------------
  * The kernels wait on shared-memory barriers for their bulk copies; each wait
  * gives up after one second of wall-clock time, sets a bit in a device-side
