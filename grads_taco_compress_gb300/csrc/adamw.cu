@@ -47,41 +47,97 @@ __device__ __forceinline__ float sqrt_approx(float v) {
   return r;
 }
 
-// E4M3 codes of |v| inv <= 448 rounded by the thresholds w (their upper 20
-// bits). Times 2^-120 the codes' smallest normal number is fp32's, so the fp32
-// bits are the code followed by 20 bits of what lies between two codes, for
-// codes' subnormals too, and a threshold is added as an integer. The sign comes
-// out in bit 7.
-constexpr float kToCode = 0x1p-120f;
-__device__ __forceinline__ uint32_t code_by_threshold(float v, float inv, uint32_t w20) {
-  const uint32_t bits = __float_as_uint(v * inv * kToCode);
-  const uint32_t r = (bits & 0x7fffffffu) + w20;
-  return ((r >> 20) & 0x7fu) | ((bits >> 24) & 0x80u);
+// Sixteen E4M3 codes of v over the scale with byte b (|v| / scale <= 448),
+// rounded by thresholds: element i's is (w + i kWeylI) / 2^32. Times 2^-120 the
+// codes' smallest normal number is fp32's, so the fp32 bits are the code, 20 bits
+// up, above what lies between two codes, and for codes' subnormals too; the
+// threshold's upper 20 bits are added as an integer. No conversion, and 4
+// instructions a code. SIGN: v may be negative.
+template <bool SIGN>
+__device__ __forceinline__ uint4 codes_by_threshold(const float (&value)[16], uint32_t b, uint32_t w) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = value[i];
+  float f = __uint_as_float((134u - b) << 23);   // 2^(127 - b) 2^-120
+  if (b >= 134u) {                               // that is no normal number: in two factors
+    const float low = 0x1p-120f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= low;
+    f = fp8_inverse_scale(b);
+  }
+  uint32_t c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t t[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const int i = 4 * q + j;
+      const f2 x = mul2(f2{v[i], v[i + 1]}, f2{f, f});
+      const uint32_t y0 = __float_as_uint(x.x) + ((w + i * kWeylI) >> 12);
+      const uint32_t y1 = __float_as_uint(x.y) + ((w + (i + 1) * kWeylI) >> 12);
+      t[j] = SIGN ? (y0 << 4) | (y0 & 0x80000000u) : y0 << 4;
+      t[j + 1] = SIGN ? (y1 << 4) | (y1 & 0x80000000u) : y1 << 4;
+    }
+    c[q] = __byte_perm(__byte_perm(t[0], t[1], 0x0073), __byte_perm(t[2], t[3], 0x0073), 0x5410);
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+// Whether a byte of the four words is zero.
+__device__ __forceinline__ bool any_zero_byte(const uint4& c) {
+  const auto z = [](uint32_t w) { return (w - 0x01010101u) & ~w; };
+  return ((z(c.x) | z(c.y) | z(c.z) | z(c.w)) & 0x80808080u) != 0u;
+}
+// The smallest code in the place of zero codes of values that are not zero.
+__device__ __forceinline__ void keep_nonzero(uint4& c, const float (&v)[16]) {
+  uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (((w[i >> 2] >> (8 * (i & 3))) & 0xffu) == 0u && v[i] > 0.0f) w[i >> 2] |= 1u << (8 * (i & 3));
+  c = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // x rounded to T by a threshold w: T's step at x is a power of two, and the
 // bits below it are a whole number that the threshold's upper bits are added to.
+// Not for infinities and NaN.
 template <typename T>
 __device__ __forceinline__ float round_by_threshold(float x, uint32_t w) {
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    const uint32_t b = __float_as_uint(x);
-    if ((b & 0x7f800000u) == 0x7f800000u) return x;
-    return __uint_as_float((b + (w >> 16)) & 0xffff0000u);
-  } else if constexpr (std::is_same<T, __half>::value) {
-    // times 2^-112, fp16's smallest normal number is fp32's
-    const float a = x * 0x1p-112f;
-    const uint32_t b = __float_as_uint(a);
-    if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) return x;
-    return __uint_as_float((b + (w >> 19)) & ~0x1fffu) * 0x1p112f;
+    return __uint_as_float((__float_as_uint(x) + (w >> 16)) & 0xffff0000u);
   } else {
-    return x;
+    // times 2^-112, fp16's smallest normal number is fp32's
+    return __uint_as_float((__float_as_uint(x * 0x1p-112f) + (w >> 19)) & ~0x1fffu) * 0x1p112f;
   }
 }
+// The sixteen of a thread as T.
+template <typename T>
+__device__ __forceinline__ Row16<T> pack_by_threshold(float (&x)[16], uint32_t w) {
+  if (amax_of(x) < __uint_as_float(0x7f800000u)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = round_by_threshold<T>(x[i], w + i * kWeylI);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (isfinite(x[i])) x[i] = round_by_threshold<T>(x[i], w + i * kWeylI);
+  }
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {   // exact already: the upper halves
+    Row16<T> r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r.w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
+    return r;
+  } else {
+    return pack<T>(x);
+  }
+}
+
+// CTAs per SM that the registers are held to.
+template <bool SMALL>
+constexpr int adamw_ctas() { return SMALL ? 3 : 3; }
 
 // P, G: element types of parameters and gradients; SMALL: states in FP8 blocks;
 // VEC: every tensor of the table starts on 16 bytes.
 template <typename P, typename G, bool SMALL, bool VEC, int CAP>
-__global__ void __launch_bounds__(kOptimThreads)
+__global__ void __launch_bounds__(kOptimThreads, adamw_ctas<SMALL>())
 adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
   const AdamwArgs& a = table.a;
   grid_launch_dependents();
@@ -93,6 +149,7 @@ adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
   const float t = static_cast<float>(step);
   const float rate = -lr / -expm1f(t * a.log_b1);            // of m' over the denominator
   const float root_c = rsqrtf(-expm1f(t * a.log_b2));
+  const float gm = factor * a.one_b1, gv = factor * a.root_one_b2;
   const int lane8 = threadIdx.x & 7;
   int e = 0;
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
@@ -103,8 +160,9 @@ adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
     if (VEC && __all_sync(kFullMask, n == 0)) continue;   // rows that start anywhere are stored by whole warps
     const bool wide = en.wide;
     const float keep = 1.0f - lr * en.decay;
+    // b1 m and b2 v, or the root of the latter
     float g[16], x[16], m[16], v[16];
-    unpack<G>(load16<G, VEC>(static_cast<const G*>(en.grad) + i0, n, wide), g);
+    const Row16<G> gr = load16<G, VEC>(static_cast<const G*>(en.grad) + i0, n, wide);
     if (en.master)
       unpack<float>(load16<float, VEC>(en.master + i0, n, wide), x);
     else
@@ -114,53 +172,60 @@ adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
       const bool any = n > 0;
       const uint4 cm = load_codes16(static_cast<const uint8_t*>(en.m) + i0, n);
       const uint4 cv = load_codes16(static_cast<const uint8_t*>(en.v) + i0, n);
-      decode16(cm, any ? fp8_scale(en.m_scales[blk]) : 1.0f, m);
-      decode16(cv, any ? fp8_scale(en.v_scales[blk]) : 1.0f, v);
-      if (n < 16) {   // a NaN scale must not reach elements that do not exist
+      const uint32_t sm = any ? en.m_scales[blk] : kScaleOne, sv = any ? en.v_scales[blk] : kScaleOne;
+      decode16(cm, fp8_scale(sm) * a.b1, m);
+      decode16(cv, fp8_scale(sv) * a.root_b2, v);
+      if (n < 16 && (sm == kScaleNan || sv == kScaleNan)) {   // which must not reach elements that do not exist
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (i >= n) m[i] = v[i] = 0.0f;
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= v[i];
     } else {
       unpack<float>(load16<float, VEC>(static_cast<const float*>(en.m) + i0, n, wide), m);
       unpack<float>(load16<float, VEC>(static_cast<const float*>(en.v) + i0, n, wide), v);
     }
+    unpack<G>(gr, g);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float gi = g[i] * factor;
-      m[i] = fmaf(a.b1, m[i], a.one_b1 * gi);
-      v[i] = fmaf(a.b2, v[i], a.one_b2 * gi * gi);
-      const float root = sqrt_approx(v[i]);
-      x[i] = fmaf(rate, __fdividef(m[i], fmaf(root, root_c, a.eps)), x[i] * keep);
-      if (SMALL) v[i] = root;
+    for (int i = 0; i < 16; i += 2) {
+      const f2 gi{g[i], g[i + 1]}, h = mul2(gi, f2{gv, gv});
+      f2 mi{m[i], m[i + 1]}, vi{v[i], v[i + 1]}, xi{x[i], x[i + 1]};
+      if (SMALL) {
+        mi = fma2(gi, f2{gm, gm}, mi);
+        vi = fma2(vi, vi, mul2(h, h));
+      } else {
+        mi = fma2(mi, f2{a.b1, a.b1}, mul2(gi, f2{gm, gm}));
+        vi = fma2(vi, f2{a.b2, a.b2}, mul2(h, h));
+      }
+      const f2 root{sqrt_approx(vi.x), sqrt_approx(vi.y)};
+      const f2 den = fma2(root, f2{root_c, root_c}, f2{a.eps, a.eps});
+      const f2 q{__fdividef(mi.x, den.x), __fdividef(mi.y, den.y)};
+      xi = fma2(q, f2{rate, rate}, mul2(xi, f2{keep, keep}));
+      m[i] = mi.x;
+      m[i + 1] = mi.y;
+      v[i] = SMALL ? root.x : vi.x;
+      v[i + 1] = SMALL ? root.y : vi.y;
+      x[i] = xi.x;
+      x[i + 1] = xi.y;
     }
-    const uint32_t w0 = static_cast<uint32_t>(i0) * kWeylI + step * kWeylT;
-    if (en.master) {
+    const uint32_t w = static_cast<uint32_t>(i0) * kWeylI + step * kWeylT;
+    if constexpr (std::is_same<P, float>::value) {
+      store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack<P>(x));
+    } else if (en.master) {
       store16<float, VEC>(en.master + i0, n, wide, pack<float>(x));
+      store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack<P>(x));
     } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = round_by_threshold<P>(x[i], w0 + i * kWeylI);
+      store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack_by_threshold<P>(x, w));
     }
-    store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack<P>(x));
     if constexpr (SMALL) {
       const int64_t blk = i0 / kFp8Block;
       const uint32_t bm = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(m)));
       const uint32_t bv = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(v)));
-      const float im = fp8_inverse_scale(bm), iv = fp8_inverse_scale(bv);
-      uint32_t cm[4] = {0, 0, 0, 0}, cv[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t w20 = (w0 + i * kWeylI) >> 12;
-        cm[i >> 2] |= code_by_threshold(m[i], im, w20) << (8 * (i & 3));
-        uint32_t q = code_by_threshold(v[i], iv, w20);
-        if (q == 0 && v[i] > 0.0f) q = 1;
-        cv[i >> 2] |= q << (8 * (i & 3));
-      }
+      const uint4 cm = codes_by_threshold<true>(m, bm, w);
+      uint4 cv = codes_by_threshold<false>(v, bv, w);
+      if (any_zero_byte(cv)) keep_nonzero(cv, v);
       if (n > 0) {
-        store_codes16(static_cast<uint8_t*>(en.m) + i0, n, make_uint4(cm[0], cm[1], cm[2], cm[3]));
-        store_codes16(static_cast<uint8_t*>(en.v) + i0, n, make_uint4(cv[0], cv[1], cv[2], cv[3]));
+        store_codes16(static_cast<uint8_t*>(en.m) + i0, n, cm);
+        store_codes16(static_cast<uint8_t*>(en.v) + i0, n, cv);
         if (lane8 == 0) {
           en.m_scales[blk] = static_cast<uint8_t>(bm);
           en.v_scales[blk] = static_cast<uint8_t>(bv);
@@ -197,7 +262,7 @@ cudaError_t launch_table(const AdamwArgs& a, const AdamwEntry* entries, int coun
 
 cudaError_t launch_adamw(const AdamwArgs& a, const AdamwEntry* entries, int count, int param_dtype, int grad_dtype,
                          bool small, bool vec, int sms, cudaStream_t st) {
-  const int ctas = sms * 4;
+  const int ctas = sms * (small ? adamw_ctas<true>() : adamw_ctas<false>());
   const auto go = [&](auto p, auto g, auto s, auto v) {
     using P = decltype(p);
     using G = decltype(g);

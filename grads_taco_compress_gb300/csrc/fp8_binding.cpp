@@ -496,6 +496,18 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
 }
 
 // ------------------------------------------------------- many tensors ----
+// What a message calls a tensor, put together only where there is a message.
+struct Name {
+  const char* what;
+  Py_ssize_t item = -1;
+  const char* part = "";
+  Name(const char* w, Py_ssize_t i = -1, const char* p = "") : what(w), item(i), part(p) {}
+  std::string text() const {
+    return item < 0 ? std::string(what) : std::string(what) + "[" + std::to_string(item) + "]" + part;
+  }
+};
+std::string operator+(const Name& n, const char* s) { return n.text() + s; }
+
 // A list or tuple of the caller's, held while its items are used.
 class Items {
  public:
@@ -515,7 +527,7 @@ class Items {
   ~Items() { Py_DECREF(fast_); }
   Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(fast_); }
   PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast_, i); }
-  std::string name(Py_ssize_t i) const { return std::string(what_) + "[" + std::to_string(i) + "]"; }
+  Name name(Py_ssize_t i, const char* part = "") const { return {what_, i, part}; }
 
  private:
   const char* what_;
@@ -525,7 +537,7 @@ class Items {
 // The device that every tensor of a call is on.
 class Device {
  public:
-  const at::Tensor& operator()(const at::Tensor& t, const std::string& what) {
+  const at::Tensor& operator()(const at::Tensor& t, const Name& what) {
     if (!t.is_cuda()) refuse(what + " must be a CUDA tensor");
     if (!device_) device_ = t.device();
     if (*device_ != t.device())
@@ -546,19 +558,19 @@ double number(PyObject* o, const char* what) {
   }
   return v;
 }
-const at::Tensor& dense(const at::Tensor& t, const std::string& what) {
+const at::Tensor& dense(const at::Tensor& t, const Name& what) {
   if (dtype_of(t.scalar_type()) < 0 || !t.is_contiguous())
     refuse(what + " must be a contiguous bf16, f16 or f32 tensor");
   return t;
 }
-const at::Tensor& dense_f32(const at::Tensor& t, const std::string& what, int64_t n) {
+const at::Tensor& dense_f32(const at::Tensor& t, const Name& what, int64_t n) {
   if (t.scalar_type() != at::kFloat || !t.is_contiguous() || t.numel() != n)
     refuse(what + " must be a contiguous f32 tensor of " + std::to_string(n) + " elements");
   return t;
 }
 // Codes and scales of a state [1, n].
-void state_pair(PyObject* o, const std::string& what, int64_t n, Device& device, void** codes, uint8_t** scales) {
-  const Pair p = pair_of(o, what.c_str());
+void state_pair(PyObject* o, const Name& what, int64_t n, Device& device, void** codes, uint8_t** scales) {
+  const Pair p = pair_of(o, what.what);
   device(p.codes, what);
   device(p.scales, what);
   const int64_t kb = (n + kBlock - 1) / kBlock;
@@ -618,11 +630,11 @@ PyObject* adamw(PyObject*, PyObject* const* v, Py_ssize_t got) {
       PyObject *const m = PyTuple_GET_ITEM(s, 0), *const r = PyTuple_GET_ITEM(s, 1);
       if (PyTuple_Check(m) != PyTuple_Check(r)) refuse(states.name(i) + ": both states in 8 bits, or both f32");
       if (PyTuple_Check(m)) {
-        state_pair(m, states.name(i) + ".m", t.n, device, &t.m, &t.m_scales);
-        state_pair(r, states.name(i) + ".v", t.n, device, &t.v, &t.v_scales);
+        state_pair(m, states.name(i, ".m"), t.n, device, &t.m, &t.m_scales);
+        state_pair(r, states.name(i, ".v"), t.n, device, &t.v, &t.v_scales);
       } else {
-        t.m = dense_f32(device(tensor(m, "states"), states.name(i)), states.name(i) + ".m", t.n).data_ptr();
-        t.v = dense_f32(device(tensor(r, "states"), states.name(i)), states.name(i) + ".v", t.n).data_ptr();
+        t.m = dense_f32(device(tensor(m, "states"), states.name(i)), states.name(i, ".m"), t.n).data_ptr();
+        t.v = dense_f32(device(tensor(r, "states"), states.name(i)), states.name(i, ".v"), t.n).data_ptr();
       }
     }
     const OnStream on(v[11], counter);
