@@ -544,7 +544,6 @@ class Device {
       refuse("the tensors of a call must be on one device, not on " + device_->str() + " and " + t.device().str());
     return t;
   }
-  c10::Device get() const { return *device_; }
 
  private:
   std::optional<c10::Device> device_;
@@ -660,19 +659,15 @@ PyObject* grad_norm(PyObject*, PyObject* const* v, Py_ssize_t got) {
       const at::Tensor& g = dense(device(tensor(grads[i], "grads"), grads.name(i)), grads.name(i));
       list[static_cast<size_t>(i)] = {g.data_ptr(), g.numel(), dtype_of(g.scalar_type())};
     }
-    const OnStream on(v[4], THPVariable_Unpack(grads[0]));
-    const int64_t need = static_cast<int64_t>(taco_grad_norm_workspace_bytes(n));
     at::Tensor out, ws;
-    if (given(v[2]))
-      out = dense_f32(device(tensor(v[2], "out"), "out"), "out", 2);
-    else
-      out = empty_vector(2, at::kFloat);
+    if (given(v[2])) out = dense_f32(device(tensor(v[2], "out"), "out"), "out", 2);
     if (given(v[3])) {
       ws = device(tensor(v[3], "workspace"), "workspace");
       if (!ws.is_contiguous()) refuse("workspace must be a contiguous CUDA tensor");
-    } else {
-      ws = empty_vector(need, at::kByte);
     }
+    const OnStream on(v[4], THPVariable_Unpack(grads[0]));
+    if (!out.defined()) out = empty_vector(2, at::kFloat);
+    if (!ws.defined()) ws = empty_vector(static_cast<int64_t>(taco_grad_norm_workspace_bytes(n)), at::kByte);
     void* stream = on.handle();
     const taco_status st = call([&] {
       return taco_grad_norm(list.data(), n, most, static_cast<float*>(out.data_ptr()), ws.data_ptr(), ws.nbytes(),

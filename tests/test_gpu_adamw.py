@@ -316,3 +316,17 @@ def test_offsets_past_32_bits(bits):
         at = (torch.arange(n - tail, n, device="cuda") // 128) - ((n + 127) // 128 - s.numel())
         have = (m8 * s[at]).cpu().numpy()
         assert (np.abs(have - m) <= 2.0 ** -3 * np.abs(m) + 2.0 ** -8 * np.abs(m).max()).all()
+
+
+def test_statuses_become_errors():
+    c = Case(13, [(100, "bf16", "f32", 32, False)])
+    for kw in (dict(betas=(1.0, 0.9)), dict(eps=0.0), dict(lr=float("nan"))):
+        with pytest.raises(taco.TacoError):
+            c.step(0.0, **kw)
+    with pytest.raises(taco.TacoError):     # the parameter itself
+        taco.taco_adamw(c.params, c.params, c.states, c.counter, lr=1e-3)
+    with pytest.raises(taco.TacoError):     # twice in a call
+        taco.taco_adamw(c.params * 2, c.grads * 2, c.states * 2, c.counter, lr=1e-3)
+    with pytest.raises(taco.TacoError):
+        taco.taco_grad_norm(c.grads, max_norm=-1.0)
+    assert c.counter.tolist() == [0, 0]
