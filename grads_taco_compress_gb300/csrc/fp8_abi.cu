@@ -150,6 +150,29 @@ taco_status quantize_common(QuantizeArgs& a, int dtype, int vec, const Region* i
   return done(launch_quantize(a, dtype, vec, static_cast<cudaStream_t>(stream)));
 }
 
+void set_operands(MatmulArgs& m, const taco_fp8_tensor& a, const taco_fp8_tensor& b) {
+  m.a = a.codes;
+  m.b = b.codes;
+  m.lda = a.ld_codes;
+  m.ldb = b.ld_codes;
+  m.sa = a.scales;
+  m.sb = b.scales;
+  m.lda_s = a.ld_scales;
+  m.ldb_s = b.ld_scales;
+  m.tile_a = a.tile_rows;
+  m.tile_b = b.tile_rows;
+  m.M = a.rows;
+  m.N = b.rows;
+  m.K = a.cols;
+  m.vec_sa = addr(a.scales) % 16 == 0 && a.ld_scales % 16 == 0;
+  m.vec_sb = addr(b.scales) % 16 == 0 && b.ld_scales % 16 == 0;
+}
+// Whether the rows of codes of a tensor all start on 32 bytes.
+bool wide_codes(const taco_fp8_tensor& t) {
+  return addr(t.codes) % 32 == 0 && (t.rows <= 1 || t.ld_codes % 32 == 0);
+}
+bool valid_act(int a) { return a >= TACO_ACT_NONE && a <= TACO_ACT_RELU; }
+
 }  // namespace
 
 }  // namespace taco
@@ -391,25 +414,11 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   if (M == 0 || N == 0) return TACO_OK;
   if (((M + 127) / 128) * ((N + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
   MatmulArgs m{};
-  m.a = a->codes;
-  m.b = b->codes;
-  m.lda = a->ld_codes;
-  m.ldb = b->ld_codes;
-  m.sa = a->scales;
-  m.sb = b->scales;
-  m.lda_s = a->ld_scales;
-  m.ldb_s = b->ld_scales;
-  m.tile_a = a->tile_rows;
-  m.tile_b = b->tile_rows;
-  m.M = M;
-  m.N = N;
-  m.K = a->cols;
+  set_operands(m, *a, *b);
   m.add = add;
   m.ldadd = ldadd;
   m.out = out;
   m.ldo = ldo;
-  m.vec_sa = addr(a->scales) % 16 == 0 && a->ld_scales % 16 == 0;
-  m.vec_sb = addr(b->scales) % 16 == 0 && b->ld_scales % 16 == 0;
   m.vec_add = vec_add != kVecNone;
   m.tma_add = vec_add != kVecNone && (ldadd * elem(dtype)) % 16 == 0;
   // a tensor map wants a row stride of 16 bytes even where there is one row
@@ -417,6 +426,63 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   const DeviceFacts* dev = nullptr;
   if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
   return done(launch_matmul(m, dtype, dev->sms, dev->clusters, static_cast<cudaStream_t>(stream)));
+}
+
+taco_status taco_linear_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, const void* bias, int bias_dtype,
+                            int activation, const void* residual, int64_t ldr, void* out, int64_t ldo, int dtype,
+                            const taco_fp8_tensor* y_fp8, const taco_fp8_tensor* checkpoint, void* stream) {
+  if (!a || !b) return TACO_ERR_NULL;
+  if (!valid_act(activation) || (bias && !valid_dtype(bias_dtype))) return TACO_ERR_ARG;
+  if (!y_fp8 && !valid_dtype(dtype)) return TACO_ERR_ARG;
+  if (y_fp8 && (out || residual)) return TACO_ERR_ARG;
+  if (a->cols != b->cols) return TACO_ERR_SHAPE;
+  Region in[6], o[5];
+  TACO_TRY(check_fp8(a, a->rows, a->cols, true, &in[0], &in[1]));
+  TACO_TRY(check_fp8(b, b->rows, b->cols, true, &in[2], &in[3]));
+  const int64_t M = a->rows, N = b->rows;
+  int vec_add = kVec32, vec_out = kVec32;
+  if (bias && N > 0) TACO_TRY(check_matrix(bias, 1, N, N, bias_dtype, &in[4], nullptr));
+  if (residual) TACO_TRY(check_matrix(residual, M, N, ldr, dtype, &in[5], &vec_add));
+  // an FP8 block tensor has a column at least
+  if (N == 0 && (y_fp8 || checkpoint)) return TACO_ERR_SHAPE;
+  if (y_fp8)
+    TACO_TRY(check_fp8(y_fp8, M, N, false, &o[1], &o[2]));
+  else if (N > 0)
+    TACO_TRY(check_matrix(out, M, N, ldo, dtype, &o[0], &vec_out));
+  if (checkpoint) TACO_TRY(check_fp8(checkpoint, M, N, false, &o[3], &o[4]));
+  TACO_TRY(check_apart(in, 6, o, 5, input(5)));   // out may be the residual
+  if (M == 0 || N == 0) return TACO_OK;
+  if (((M + 127) / 128) * ((N + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
+  LinearArgs l{};
+  set_operands(l, *a, *b);
+  l.bias = bias;
+  l.bias_dtype = bias_dtype;
+  l.act = activation;
+  l.add = residual;
+  l.ldadd = ldr;
+  l.out = out;
+  l.ldo = ldo;
+  l.vec_add = vec_add != kVecNone;
+  l.wide_add = vec_add == kVec32;
+  l.vec_out = l.tma_out = vec_out != kVecNone;
+  l.wide_out = vec_out == kVec32;
+  if (y_fp8) {
+    l.y_codes = y_fp8->codes;
+    l.y_scales = y_fp8->scales;
+    l.y_ld = y_fp8->ld_codes;
+    l.y_lds = y_fp8->ld_scales;
+    l.wide_y = wide_codes(*y_fp8);
+  }
+  if (checkpoint) {
+    l.k_codes = checkpoint->codes;
+    l.k_scales = checkpoint->scales;
+    l.k_ld = checkpoint->ld_codes;
+    l.k_lds = checkpoint->ld_scales;
+    l.wide_k = wide_codes(*checkpoint);
+  }
+  const DeviceFacts* dev = nullptr;
+  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
+  return done(launch_linear(l, dtype, dev->sms, dev->clusters, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

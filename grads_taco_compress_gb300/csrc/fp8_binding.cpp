@@ -62,6 +62,16 @@ int dtype_of(at::ScalarType t) {
   return t == at::kBFloat16 ? TACO_DTYPE_BF16 : t == at::kHalf ? TACO_DTYPE_F16 : t == at::kFloat ? TACO_DTYPE_F32 : -1;
 }
 
+// TACO_ACT_* of None or an activation's name.
+int activation(PyObject* o) {
+  if (!given(o)) return TACO_ACT_NONE;
+  static constexpr const char* kNames[] = {"gelu", "gelu_tanh", "silu", "relu"};
+  if (PyUnicode_Check(o))
+    for (int i = 0; i < 4; ++i)
+      if (PyUnicode_CompareWithASCIIString(o, kNames[i]) == 0) return TACO_ACT_GELU + i;
+  refuse("activation must be None, 'gelu', 'gelu_tanh', 'silu' or 'relu'");
+}
+
 struct Matrix {
   void* p = nullptr;
   int64_t rows = 0, cols = 0, ld = 0;
@@ -495,6 +505,67 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// linear(a, b, bias, activation, residual, out, out_dtype, checkpoint, stream) -> y, checkpoint
+PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(v, n, 9, [&]() -> PyObject* {
+    const Pair a = pair_of(v[0], "x"), b = pair_of(v[1], "w");
+    const taco_fp8_tensor ad = describe(a.codes, a.scales, "x"), bd = describe(b.codes, b.scales, "w");
+    const int act = activation(v[3]);
+    at::Tensor bias, out;
+    void* bp = nullptr;
+    if (given(v[2])) {
+      bias = tensor(v[2], "bias");
+      bp = vector(bias, "bias", bd.rows, false);
+    }
+    std::optional<Pair> y, kept;
+    const bool keep = PyTuple_Check(v[7]) || flag(v[7], "checkpoint");
+    at::ScalarType type = at::kBFloat16;
+    if (!given(v[5])) {
+      if (!THPDtype_Check(v[6])) refuse("out_dtype must be a torch.dtype");
+      type = reinterpret_cast<THPDtype*>(v[6])->scalar_type;
+      if (type != at::kFloat8_e4m3fn && dtype_of(type) < 0) refuse("out_dtype must be bf16, f16, f32 or float8_e4m3fn");
+    }
+    const bool small = given(v[5]) ? PyTuple_Check(v[5]) : type == at::kFloat8_e4m3fn;
+    if (small && given(v[4])) refuse("residual takes an output of 16 or 32 bits");
+    if ((small || keep) && bd.rows == 0) refuse("an Fp8Tensor has a column at least");
+    Matrix o, res;
+    if (given(v[5]) && small) {
+      y = pair_of(v[5], "out");
+    } else if (given(v[5])) {
+      out = tensor(v[5], "out");
+      o = matrix(out, "out");
+      if (o.rows != ad.rows || o.cols != bd.rows) refuse("out must have the rows of x and of w");
+    }
+    if (given(v[4])) {
+      const at::Tensor& r = tensor(v[4], "residual");
+      res = like(r, "residual", ad.rows, bd.rows, given(v[5]) ? o.dtype : dtype_of(type));
+    }
+    if (PyTuple_Check(v[7])) kept = pair_of(v[7], "checkpoint");
+    taco_fp8_tensor yd{}, kd{};
+    if (y) yd = describe(y->codes, y->scales, "out");
+    if (kept) kd = describe(kept->codes, kept->scales, "checkpoint");
+    const OnStream on(v[8], a.codes);
+    if (small && !y) {
+      y = new_fp8({ad.rows, bd.rows}, 1);
+      yd = describe(y->codes, y->scales, "out");
+    } else if (!small && !out.defined()) {
+      out = empty_matrix(ad.rows, bd.rows, type);
+      o = matrix(out, "out");
+    }
+    if (keep && !kept) {
+      kept = new_fp8({ad.rows, bd.rows}, 1);
+      kd = describe(kept->codes, kept->scales, "checkpoint");
+    }
+    void* stream = on.handle();
+    const taco_status st = call([&] {
+      return taco_linear_fp8(&ad, &bd, bp, bp ? dtype_of(bias.scalar_type()) : 0, act, res.p, res.ld, o.p, o.ld, o.dtype,
+                             y ? &yd : nullptr, kept ? &kd : nullptr, stream);
+    });
+    if (st != TACO_OK) return PyLong_FromLong(st);
+    return tuple(&PyTuple_Type, {y ? object(y) : object(out), object(kept)});
+  });
+}
+
 // ------------------------------------------------------- many tensors ----
 // What a message calls a tensor, put together only where there is a message.
 struct Name {
@@ -697,7 +768,7 @@ PyObject* types(PyObject*, PyObject* const* v, Py_ssize_t n) {
 PyMethodDef kMethods[] = {TACO_METHOD(types), TACO_METHOD(quantize), TACO_METHOD(rms_norm),
                           TACO_METHOD(rms_norm_backward),
                           TACO_METHOD(swiglu), TACO_METHOD(swiglu_backward), TACO_METHOD(matmul),
-                          TACO_METHOD(adamw), TACO_METHOD(grad_norm),
+                          TACO_METHOD(linear), TACO_METHOD(adamw), TACO_METHOD(grad_norm),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8_binding", "Argument marshalling of the FP8 entry points.", -1,
                        kMethods, nullptr, nullptr, nullptr, nullptr};

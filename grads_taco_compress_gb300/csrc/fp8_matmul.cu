@@ -35,7 +35,7 @@
 // MB would take 2.5, and 5.5 us where they are in L2 from the call before; 1 x
 // 16384 x 4096 13.6 us, 4.9 TB/s.
 
-#include "fp8_block.cuh"
+#include "fp8_activation.cuh"
 #include "tcgen05.cuh"
 
 namespace taco {
@@ -337,12 +337,243 @@ struct Pair {
 // below an accumulator's last bit, and a long sum drifts.
 constexpr int kSegment = 8;
 
-template <typename T, int TN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constant__ CUtensorMap out_map,
-                   const __grid_constant__ CUtensorMap add_map, MatmulArgs a) {
+// ------------------------------------------------- a layer's epilogue ----
+// The arguments say which epilogue a kernel has: none (MatmulArgs), a layer's
+// with its output in T (LinearArgs) or in FP8 blocks.
+struct LinearFp8Args : LinearArgs {
+  explicit LinearFp8Args(const LinearArgs& a) : LinearArgs(a) {}
+};
+template <typename Args>
+constexpr bool kFp8Out = std::is_same<Args, LinearFp8Args>::value;
+template <typename Args>
+constexpr int pair_threads() { return std::is_same<Args, MatmulArgs>::value ? kThreads : kThreads + 128; }
+
+__device__ __forceinline__ float bias_at(const LinearArgs& a, int64_t n) {
+  if (!a.bias) return 0.0f;
+  if (a.bias_dtype == TACO_DTYPE_F32) return static_cast<const float*>(a.bias)[n];
+  if (a.bias_dtype == TACO_DTYPE_BF16) return to_f32(static_cast<const __nv_bfloat16*>(a.bias)[n]);
+  return to_f32(static_cast<const __half*>(a.bias)[n]);
+}
+// A warp's 128 columns of a row, 4 a lane (of which `left` exist, the others
+// are zero), to a block of codes and its scale.
+__device__ __forceinline__ void store_block4(const float (&v)[4], int64_t left, uint8_t* codes, uint8_t* scale) {
+  const uint32_t b = fp8_scale_byte(group_umax<32>(amax_of(v)));
+  const float inv = fp8_inverse_scale(b);
+  const uint32_t w = e4m3x4_from_f32(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  if (left >= 4) {
+    *reinterpret_cast<uint32_t*>(codes) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) codes[i] = static_cast<uint8_t>(w >> (8 * i));
+  }
+  if ((threadIdx.x & 31) == 0) *scale = static_cast<uint8_t>(b);
+}
+
+// The layer's epilogue has 8 warps: two share 32 rows of the accumulator, and
+// each takes 64 of the 128 columns of a block, a row a lane. So a lane's 64
+// values stay in registers from the accumulator to the last rounding, whatever
+// is made of them, and the largest magnitude of a block is two lanes' to
+// exchange, through shared memory and a barrier of the two warps. Rows go out
+// by whole 32-byte sectors of a lane. Half the values a thread (and 4 registers
+// a value less) also halve the time an accumulator is held.
+constexpr int kHalf = kFp8Block / 2;
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory"); }
+// Whether `pred` holds in any lane of the two warps, the same in all of them.
+__device__ __forceinline__ bool pair_any(int id, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r) : "r"(static_cast<uint32_t>(pred)), "r"(id) : "memory");
+  return r != 0;
+}
+// Shared memory of the epilogue in the place of the output's staging: each
+// warp's bias for the two blocks of a tile, and two slots of largest magnitudes.
+struct LinearShared {
+  static constexpr uint32_t bias = 0, kBias = 2 * kHalf * 4;
+  static constexpr uint32_t amax = 8 * kBias, kSlot = 8 * 32 * 4;
+  static constexpr uint32_t bytes = amax + 2 * kSlot;
+};
+
+// Scale byte of the lane's block, from its 64 values and the other warp's.
+// `turn` counts the exchanges: a slot is written again two barriers after it was
+// read.
+__device__ __forceinline__ uint32_t block_scale(const float (&v)[kHalf], uint32_t slots, int quad, int half,
+                                                uint32_t& turn) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t at = slots + (turn & 1u) * LinearShared::kSlot + (quad * 32 + lane) * 4;
+  const uint32_t mine = __float_as_uint(amax_of(v));
+  asm volatile("st.shared.u32 [%0], %1;" :: "r"(at + half * 512), "r"(mine) : "memory");
+  pair_sync(1 + quad);
+  ++turn;
+  return fp8_scale_byte(max(mine, lds_u32(at + (half ^ 1) * 512)));
+}
+// 64 codes of a row of which `left` exist.
+__device__ __forceinline__ void store_codes64(const float (&v)[kHalf], uint32_t b, uint8_t* p, int64_t left, bool wide) {
+  const float inv = fp8_inverse_scale(b);
+#pragma unroll
+  for (int q = 0; q < kHalf; q += 32) {
+    uint4 c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = v[q + 16 * h + i];
+      c[h] = codes16(t, inv);
+    }
+    if (left >= q + 32) {
+      store_words8(p + q, wide, reinterpret_cast<const uint32_t*>(c));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) store_codes16(p + q + 16 * h, clamp16(left - q - 16 * h), c[h]);
+    }
+  }
+}
+// v += 64 elements of a row, and 64 elements to a row, of which `left` exist.
+template <typename T>
+__device__ __forceinline__ void add_row64(float (&v)[kHalf], const T* p, int64_t left, bool vec, bool wide) {
+  constexpr int kPer = 32 / static_cast<int>(sizeof(T));
+#pragma unroll
+  for (int q = 0; q < kHalf; q += kPer) {
+    if (vec && left >= q + kPer) {
+      alignas(16) uint32_t w[8];
+      load_words8(p + q, wide, w);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[q + i] += to_f32(reinterpret_cast<const T*>(w)[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (q + i < left) v[q + i] += to_f32(p[q + i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_row64(const float (&v)[kHalf], T* p, int64_t left, bool vec, bool wide) {
+  constexpr int kPer = 32 / static_cast<int>(sizeof(T));
+#pragma unroll
+  for (int q = 0; q < kHalf; q += kPer) {
+    if (vec && left >= q + kPer) {
+      uint4 w[2] = {pack16<T>(&v[q]), pack16<T>(&v[q + kPer / 2])};
+      store_words8(p + q, wide, reinterpret_cast<const uint32_t*>(w));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (q + i < left) p[q + i] = from_f32<T>(v[q + i]);
+    }
+  }
+}
+
+// Warps 4 - 11 of the pair kernel. Neither of two warps leaves a tile's barriers
+// to the other: they decide together whether its sums have arrived.
+template <typename T, int TN, typename Args>
+__device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm, int64_t tiles, int64_t pair,
+                                                int64_t pairs, int kb, uint32_t base, uint32_t tmem, uint32_t rank,
+                                                volatile uint32_t* abort_flag) {
   using S = Pair<TN>;
+  static_assert(LinearShared::bytes <= 4 * S::kBoxes * 4096, "in the place of the staging");
   constexpr bool kSeg = std::is_same<T, float>::value;
+  constexpr int kBlocks = TN / kFp8Block;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, quad = warp & 3, half = (warp - 4) >> 2;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t biases = base + S::staging + LinearShared::bias + (warp - 4) * LinearShared::kBias;
+  const uint32_t slots = base + S::staging + LinearShared::amax;
+  const uint32_t tempty0 = in_cta(base + S::tempty, 0);
+  uint32_t u = 0, turn = 0;
+  for (int64_t t = pair; t < tiles; t += pairs) {
+    int64_t mt, nt;
+    tm.at(t, mt, nt);
+    const int64_t m = mt * 256 + rank * 128 + quad * 32 + lane, n0 = nt * TN + half * kHalf;
+    const bool row = m < a.M;
+    __syncwarp();   // the last tile's bias has been read
+#pragma unroll
+    for (int c = 0; c < 2 * kBlocks; ++c) {
+      const int64_t n = n0 + (c >> 1) * kFp8Block + (c & 1) * 32 + lane;
+      const float b = n < a.N ? bias_at(a, n) : 0.0f;
+      asm volatile("st.shared.f32 [%0], %1;" :: "r"(biases + 4 * (c * 32 + lane)), "f"(b) : "memory");
+    }
+    __syncwarp();
+    float v[kHalf];
+    bool ok = true;
+    const int segments = kSeg ? (kb + kSegment - 1) / kSegment : 1;
+    if constexpr (kSeg) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) v[i] = 0.0f;
+    }
+    for (int g = 0; g < segments && ok; ++g) {
+      ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if constexpr (kSeg) {
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 32) {
+          float part[32];
+          tmem_ld32(tmem + lanes + (u & 1u) * S::kAcc1 + half * kHalf + c, part);
+          tmem_ready32(part);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[c + i] += part[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_even_read(tempty0 + 8 * (u & 1u));
+        ++u;
+      }
+    }
+    if (pair_any(1 + quad, !ok)) break;
+#pragma unroll
+    for (int c = 0; c < kBlocks; ++c) {
+      // the columns that the accumulators share first: accumulator 0's last, accumulator 1's first
+      const int block = kBlocks == 2 && (u & 1u) == 0u ? 1 - c : c;
+      if constexpr (!kSeg) {
+        const uint32_t acc = tmem + lanes + (u & 1u) * S::kAcc1 + block * kFp8Block + half * kHalf;
+#pragma unroll
+        for (int i = 0; i < kHalf; i += 16) tmem_ld16(acc + i, v + i);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < kHalf; i += 16) reg_fence16(v + i);
+        if (c == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_even_read(tempty0 + 8 * (u & 1u));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kHalf; i += 4) {
+        const uint4 b = lds128(biases + 4 * (block * kHalf + i));
+        v[i] += __uint_as_float(b.x);
+        v[i + 1] += __uint_as_float(b.y);
+        v[i + 2] += __uint_as_float(b.z);
+        v[i + 3] += __uint_as_float(b.w);
+      }
+      const int64_t n = n0 + block * kFp8Block, left = row ? a.N - n : 0;
+      const int64_t kblock = n / kFp8Block;
+      const bool scales = row && half == 0 && n < a.N;
+      if (a.k_codes) {
+        const uint32_t b = block_scale(v, slots, quad, half, turn);
+        store_codes64(v, b, a.k_codes + m * a.k_ld + n, left, a.wide_k);
+        if (scales) a.k_scales[m * a.k_lds + kblock] = static_cast<uint8_t>(b);
+      }
+      activate(v, a.act);
+      if constexpr (kFp8Out<Args>) {
+        const uint32_t b = block_scale(v, slots, quad, half, turn);
+        store_codes64(v, b, a.y_codes + m * a.y_ld + n, left, a.wide_y);
+        if (scales) a.y_scales[m * a.y_lds + kblock] = static_cast<uint8_t>(b);
+      } else {
+        if (a.add) add_row64(v, static_cast<const T*>(a.add) + m * a.ldadd + n, left, a.vec_add, a.wide_add);
+        store_row64(v, static_cast<T*>(a.out) + m * a.ldo + n, left, a.vec_out, a.wide_out);
+      }
+    }
+    if constexpr (!kSeg) ++u;
+  }
+}
+
+template <typename T, int TN, typename Args>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Args>(), 1)
+matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constant__ CUtensorMap out_map,
+                   const __grid_constant__ CUtensorMap add_map, Args a) {
+  using S = Pair<TN>;
+  constexpr bool kSeg = std::is_same<T, float>::value, kLinear = !std::is_same<Args, MatmulArgs>::value;
   static_assert(!kSeg || TN == 128, "the segments' sum is held in registers");
   extern __shared__ unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -368,7 +599,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     for (int s = 0; s < 2; ++s) {
       mbar_init(base + S::sdone + 8 * s, 1);
       mbar_init(base + S::tfull + 8 * s, 1);
-      mbar_init(base + S::tempty + 8 * s, 8);   // 4 epilogue warps of both CTAs
+      mbar_init(base + S::tempty + 8 * s, kLinear ? 16 : 8);   // the epilogue warps of both CTAs
     }
     for (int w = 0; w < 4; ++w) mbar_init(base + S::added + 8 * w, 1);
     mbar_init(base + S::done, 1);
@@ -567,6 +798,8 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
       }
       if (t < tiles) fetch();
     }
+  } else if (kLinear && warp >= 4) {
+    if constexpr (kLinear) linear_epilogue<T, TN>(a, tm, tiles, pair, pairs, kb, base, tmem, rank, abort_flag);
   } else if (warp >= 4) {
     // -------------------------------------------------------- epilogue ----
     const int quad = warp & 3;
@@ -739,11 +972,11 @@ struct Few {
   static_assert(kColScales + 16 <= kTmemCols, "tensor memory");
 };
 
-template <typename T, int TT>
+template <typename T, int TT, typename Args>
 __global__ void __launch_bounds__(kThreads, 1)
-matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int splits) {
+matmul_few_kernel(const __grid_constant__ MatmulMaps maps, Args a, int splits) {
   using S = Few<TT>;
-  constexpr bool kSeg = std::is_same<T, float>::value;
+  constexpr bool kSeg = std::is_same<T, float>::value, kLinear = !std::is_same<Args, MatmulArgs>::value;
   constexpr uint32_t kDesc = ((TT >> 3) << 17) | (1u << 23) | (1u << 27);   // mx_desc(128, TT)
   extern __shared__ unsigned char smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -929,6 +1162,12 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
     // a warp takes a token at a time, 4 columns a lane, all splits' parts in flight
     const int64_t n = n0 + 4 * lane, left = a.N - n;
     const int rows = static_cast<int>(a.M - m0 < TT ? a.M - m0 : TT);
+    float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (kLinear) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) bias[i] = bias_at(a, n + i);
+    }
     uint32_t from[kMaxSplits];
 #pragma unroll
     for (int r = 0; r < kMaxSplits; ++r) from[r] = in_cta(base + S::stages + 16 * lane, r < splits ? r : 0);
@@ -949,6 +1188,18 @@ matmul_few_kernel(const __grid_constant__ MatmulMaps maps, MatmulArgs a, int spl
           s[2] += v[r].z;
           s[3] += v[r].w;
         }
+      if constexpr (kLinear) {
+        // a warp holds the 128 columns of a block
+        const int64_t m = m0 + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += bias[i];
+        if (a.k_codes) store_block4(s, left, a.k_codes + m * a.k_ld + n, a.k_scales + m * a.k_lds + n0 / kFp8Block);
+        activate(s, a.act);
+        if constexpr (kFp8Out<Args>) {
+          store_block4(s, left, a.y_codes + m * a.y_ld + n, a.y_scales + m * a.y_lds + n0 / kFp8Block);
+          continue;
+        }
+      }
       if (a.add) add_row<T, 4>(s, static_cast<const T*>(a.add) + (m0 + c) * a.ldadd + n, left, a.vec_add);
       store_row4<T>(static_cast<T*>(a.out) + (m0 + c) * a.ldo + n, s, left, a.tma_out);
     }
@@ -1015,48 +1266,55 @@ cudaError_t prepare_matmul(int* clusters) {
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(bytes));
   };
-  set(matmul_pair_kernel<__nv_bfloat16, 256>, Pair<256>::bytes);
-  set(matmul_pair_kernel<__half, 256>, Pair<256>::bytes);
-  set(matmul_pair_kernel<__nv_bfloat16, 128>, Pair<128>::bytes);
-  set(matmul_pair_kernel<__half, 128>, Pair<128>::bytes);
-  set(matmul_pair_kernel<float, 128>, Pair<128>::bytes);
-  const auto few = [&](auto t) {
+  const auto all = [&](auto t, auto* args) {
     using T = decltype(t);
-    set(matmul_few_kernel<T, 16>, Few<16>::bytes);
-    set(matmul_few_kernel<T, 32>, Few<32>::bytes);
-    set(matmul_few_kernel<T, 64>, Few<64>::bytes);
-    set(matmul_few_kernel<T, 128>, Few<128>::bytes);
+    using Args = std::remove_pointer_t<decltype(args)>;
+    if constexpr (!std::is_same<T, float>::value) set(matmul_pair_kernel<T, 256, Args>, Pair<256>::bytes);
+    set(matmul_pair_kernel<T, 128, Args>, Pair<128>::bytes);
+    set(matmul_few_kernel<T, 16, Args>, Few<16>::bytes);
+    set(matmul_few_kernel<T, 32, Args>, Few<32>::bytes);
+    set(matmul_few_kernel<T, 64, Args>, Few<64>::bytes);
+    set(matmul_few_kernel<T, 128, Args>, Few<128>::bytes);
   };
-  few(__nv_bfloat16{});
-  few(__half{});
-  few(float{});
+  MatmulArgs* const plain = nullptr;
+  LinearArgs* const layer = nullptr;
+  LinearFp8Args* const layer_fp8 = nullptr;
+  all(__nv_bfloat16{}, plain);
+  all(__half{}, plain);
+  all(float{}, plain);
+  all(__nv_bfloat16{}, layer);
+  all(__half{}, layer);
+  all(float{}, layer);
+  all(__nv_bfloat16{}, layer_fp8);
   // one CTA per SM in every form: the count is the same for all of them
   for (int splits = 1; splits <= kMaxSplits && e == cudaSuccess; ++splits) {
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = few_config(splits, splits, 1, Few<128>::bytes, nullptr, attr);
-    e = cudaOccupancyMaxActiveClusters(&clusters[splits], matmul_few_kernel<__nv_bfloat16, 128>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&clusters[splits], matmul_few_kernel<__nv_bfloat16, 128, MatmulArgs>, &cfg);
   }
   return e;
 }
 
 // One 256 x TN tile per CTA pair, at most one pair per two SMs.
-template <typename T, int TN>
-cudaError_t launch_pair(EncodeTiled encode, const MatmulArgs& a, int sms, cudaStream_t st) {
+template <typename T, int TN, typename Args>
+cudaError_t launch_pair(EncodeTiled encode, const Args& a, int sms, cudaStream_t st) {
   MatmulMaps maps;
   if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, 128) ||
       !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, TN / 2))
     return cudaErrorInvalidValue;
   CUtensorMap out = maps.a, add = maps.a;
-  if (a.tma_out && !encode_out<T>(encode, &out, a, a.out, a.ldo)) return cudaErrorInvalidValue;
-  if (a.add && a.tma_add && !encode_out<T>(encode, &add, a, a.add, a.ldadd)) return cudaErrorInvalidValue;
+  if (std::is_same<Args, MatmulArgs>::value) {
+    if (a.tma_out && !encode_out<T>(encode, &out, a, a.out, a.ldo)) return cudaErrorInvalidValue;
+    if (a.add && a.tma_add && !encode_out<T>(encode, &add, a, a.add, a.ldadd)) return cudaErrorInvalidValue;
+  }
   const int64_t tiles = ((a.M + 255) / 256) * ((a.N + TN - 1) / TN);
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  return launch_dependent(matmul_pair_kernel<T, TN>, dim3(static_cast<unsigned>(2 * pairs)), kThreads,
-                          Pair<TN>::bytes, st, maps, out, add, a);
+  return launch_dependent(matmul_pair_kernel<T, TN, Args>, dim3(static_cast<unsigned>(2 * pairs)),
+                          pair_threads<Args>(), Pair<TN>::bytes, st, maps, out, add, a);
 }
 
-template <typename T, int TT>
-cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cudaStream_t st) {
+template <typename T, int TT, typename Args>
+cudaError_t launch_few(EncodeTiled encode, const Args& a, int splits, cudaStream_t st) {
   MatmulMaps maps;
   if (!encode_codes(encode, &maps.a, a.a, a.M, a.K, a.lda, TT) ||
       !encode_codes(encode, &maps.b, a.b, a.N, a.K, a.ldb, 128))
@@ -1064,7 +1322,7 @@ cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cuda
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = few_config(splits, static_cast<unsigned>((a.N + 127) / 128 * splits),
                                             static_cast<unsigned>((a.M + TT - 1) / TT), Few<TT>::bytes, st, attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_few_kernel<T, TT>, maps, a, splits);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, matmul_few_kernel<T, TT, Args>, maps, a, splits);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -1079,26 +1337,31 @@ cudaError_t launch_few(EncodeTiled encode, const MatmulArgs& a, int splits, cuda
 // else 256 wide (1024 rows: 15.7 us, 18.4 at 128 wide); f32 always 128, whose
 // sum its epilogue can hold.
 constexpr int kFewSaves = 24;
-cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st) {
+template <typename T, typename Args>
+cudaError_t launch_product(const Args& a, int sms, const int* clusters, cudaStream_t st) {
   EncodeTiled encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
-  return with_dtype(dtype, [&](auto t) {
-    using T = decltype(t);
-    const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
-    const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 127) / 128);
-    int s = 1;
-    while (s < kMaxSplits && s < kb && tiles <= clusters[s + 1]) ++s;
-    if (a.M <= 16) return launch_few<T, 16>(encode, a, s, st);
-    if (a.M <= 32) return launch_few<T, 32>(encode, a, s, st);
-    if (a.M <= 64) return launch_few<T, 64>(encode, a, s, st);
-    if (kb - (kb + s - 1) / s >= kFewSaves) return launch_few<T, 128>(encode, a, s, st);
-    if constexpr (std::is_same<T, float>::value) {
-      return launch_pair<T, 128>(encode, a, sms, st);
-    } else {
-      const int64_t narrow = ((a.M + 255) / 256) * ((a.N + 127) / 128);
-      return narrow <= sms / 2 ? launch_pair<T, 128>(encode, a, sms, st) : launch_pair<T, 256>(encode, a, sms, st);
-    }
-  });
+  const int64_t kb = (a.K + kFp8Block - 1) / kFp8Block;
+  const int64_t tiles = ((a.N + 127) / 128) * ((a.M + 127) / 128);
+  int s = 1;
+  while (s < kMaxSplits && s < kb && tiles <= clusters[s + 1]) ++s;
+  if (a.M <= 16) return launch_few<T, 16>(encode, a, s, st);
+  if (a.M <= 32) return launch_few<T, 32>(encode, a, s, st);
+  if (a.M <= 64) return launch_few<T, 64>(encode, a, s, st);
+  if (kb - (kb + s - 1) / s >= kFewSaves) return launch_few<T, 128>(encode, a, s, st);
+  if constexpr (std::is_same<T, float>::value) {
+    return launch_pair<T, 128>(encode, a, sms, st);
+  } else {
+    const int64_t narrow = ((a.M + 255) / 256) * ((a.N + 127) / 128);
+    return narrow <= sms / 2 ? launch_pair<T, 128>(encode, a, sms, st) : launch_pair<T, 256>(encode, a, sms, st);
+  }
+}
+cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st) {
+  return with_dtype(dtype, [&](auto t) { return launch_product<decltype(t)>(a, sms, clusters, st); });
+}
+cudaError_t launch_linear(const LinearArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st) {
+  if (a.y_codes) return launch_product<__nv_bfloat16>(LinearFp8Args(a), sms, clusters, st);
+  return with_dtype(dtype, [&](auto t) { return launch_product<decltype(t)>(a, sms, clusters, st); });
 }
 
 cudaError_t matmul_fault(unsigned int* bits, bool clear) {

@@ -243,6 +243,22 @@ struct MatmulArgs {
   bool tma_add, tma_out;    // add's, out's do, and the stride is one that a tensor copy takes
 };
 
+// The product with an epilogue: add is the residual, out unused where the
+// output is an FP8 block tensor.
+struct LinearArgs : MatmulArgs {
+  const void* bias;         // may be null
+  int bias_dtype;
+  int act;                  // TACO_ACT_*
+  uint8_t* y_codes;         // FP8 output; null: out
+  uint8_t* y_scales;
+  int64_t y_ld, y_lds;
+  uint8_t* k_codes;         // what the activation was applied to; may be null
+  uint8_t* k_scales;
+  int64_t k_ld, k_lds;
+  bool vec_out;                                // out's rows all start on 16 bytes
+  bool wide_out, wide_add, wide_y, wide_k;     // rows all start on 32 bytes
+};
+
 cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, cudaStream_t st);
 // Most CTAs, and so rows of partial sums, of the norm's backward pass on rows of
 // H (512 at 2048 columns and more, up to 2048 of shorter rows).
@@ -256,6 +272,7 @@ cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, int vec, cudaStrea
 // Fills clusters[1 .. 8]: how many clusters of that many CTAs run at once.
 cudaError_t prepare_matmul(int* clusters);
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
+cudaError_t launch_linear(const LinearArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
 cudaError_t matmul_fault(unsigned int* bits, bool clear);
 
 // ---- Many tensors at once (adamw.cu, grad_norm.cu) ----

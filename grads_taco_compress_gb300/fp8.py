@@ -170,3 +170,19 @@ def taco_matmul_fp8(a: Fp8Tensor, b: Fp8Tensor, out: torch.Tensor | None = None,
     if type(r) is int:
         _check(r, "taco_matmul_fp8")
     return r
+
+
+def taco_linear_fp8(x: Fp8Tensor, w: Fp8Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
+                    residual: torch.Tensor | None = None, out: torch.Tensor | Fp8Tensor | None = None,
+                    out_dtype: torch.dtype = torch.bfloat16, checkpoint: bool | Fp8Tensor = False, stream=None):
+    """y = act(x w^T + bias) + residual of x [M, K] and w [N, K], in one launch.
+    activation: None, "gelu", "gelu_tanh", "silu" or "relu". ``out_dtype``
+    torch.float8_e4m3fn (or ``out`` an Fp8Tensor) gives y as an Fp8Tensor, as
+    the next product reads it; it takes no residual then. With ``checkpoint``
+    (True or a preallocated Fp8Tensor) what the activation is applied to is kept
+    in 8 bits for taco_linear_fp8_backward. ``residual``, of the output's type,
+    may be ``out`` (in place). Returns (y, checkpoint or None)."""
+    r = _binding().linear(x, w, bias, activation, residual, out, out_dtype, checkpoint, _handle(stream))
+    if type(r) is int:
+        _check(r, "taco_linear_fp8")
+    return r

@@ -460,6 +460,20 @@ taco_status taco_swiglu_fp8_backward(const void* dy, int64_t lddy,
 taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, const void* add,
                             int64_t ldadd, void* out, int64_t ldo, int dtype, void* stream);
 
+/* The same product with a layer's epilogue, before anything is rounded:
+ *   pre = a b^T + bias,   y = act(pre) + residual
+ * bias [N] (bias_dtype), residual [M, N] (dtype) and `checkpoint` may be NULL.
+ * y goes to `out` (dtype), or quantised to y_fp8 (tile_rows 1; out and residual
+ * NULL then, dtype unused): exactly one of the two. `checkpoint` (tile_rows 1)
+ * keeps pre in 8 bits for the backward pass. residual may be out itself.
+ * Activations: GELU x Phi(x); GELU_TANH x (1 + tanh(sqrt(2 / pi) (x + 0.044715
+ * x^3))) / 2; SILU x / (1 + exp(-x)); RELU max(x, 0), of a NaN NaN. */
+enum { TACO_ACT_NONE = 0, TACO_ACT_GELU = 1, TACO_ACT_GELU_TANH = 2, TACO_ACT_SILU = 3, TACO_ACT_RELU = 4 };
+taco_status taco_linear_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, const void* bias,
+                            int bias_dtype, int activation, const void* residual, int64_t ldr,
+                            void* out, int64_t ldo, int dtype, const taco_fp8_tensor* y_fp8,
+                            const taco_fp8_tensor* checkpoint, void* stream);
+
 /* ---- Many tensors at once ---------------------------------------------------
  * What a training step does with a model's gradients: their norm, and an AdamW
  * step. A call takes a host array of `count` tensors (0 .. 2^20, read before

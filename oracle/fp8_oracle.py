@@ -8,6 +8,8 @@ gated activation, their gradients, and the matrix product.
 
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 from .taco_oracle import e4m3_decode, e4m3_encode
@@ -96,3 +98,31 @@ def swiglu(gate, up):
 def swiglu_backward(dy, gate, up):
     s = sigmoid(gate)
     return dy * up * s * (1 + gate * (1 - s)), dy * gate * s
+
+
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+GELU_C, GELU_A = math.sqrt(2 / math.pi), 0.044715
+
+
+def activate(x, kind):
+    """The activation `kind` (None: none) of x."""
+    if kind == "gelu":
+        return x * 0.5 * _erfc(-x / math.sqrt(2))
+    if kind == "gelu_tanh":
+        return 0.5 * x * (1 + np.tanh(GELU_C * (x + GELU_A * x ** 3)))
+    if kind == "silu":
+        return x * sigmoid(x)
+    return np.where(x < 0, 0.0, x) if kind == "relu" else x
+
+
+def activation_slope(x, kind):
+    """Its derivative (0 at 0 for relu)."""
+    if kind == "gelu":
+        return 0.5 * _erfc(-x / math.sqrt(2)) + x * np.exp(-x * x / 2) / math.sqrt(2 * math.pi)
+    if kind == "gelu_tanh":
+        t = np.tanh(GELU_C * (x + GELU_A * x ** 3))
+        return 0.5 * (1 + t) + 0.5 * x * (1 - t * t) * GELU_C * (1 + 3 * GELU_A * x * x)
+    if kind == "silu":
+        s = sigmoid(x)
+        return s + x * s * (1 - s)
+    return (x > 0).astype(np.float64) if kind == "relu" else np.ones_like(x)
