@@ -106,6 +106,16 @@ __device__ __forceinline__ T load_staged(uint32_t addr) {
     return v;
   }
 }
+template <typename T>
+__device__ __forceinline__ void store_staged(uint32_t addr, T v) {
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("st.shared.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+  } else {
+    uint16_t r;
+    memcpy(&r, &v, 2);
+    asm volatile("st.shared.u16 [%0], %1;" :: "r"(addr), "h"(r) : "memory");
+  }
+}
 // v += the `left` (or COLS) elements of a row of `add`; vec: rows of it start on
 // 16 bytes (and p on as many as COLS elements take, at most 16).
 template <typename T, int COLS>
@@ -393,7 +403,8 @@ __device__ __forceinline__ bool pair_any(int id, bool pred) {
 struct LinearShared {
   static constexpr uint32_t bias = 0, kBias = 2 * kHalf * 4;
   static constexpr uint32_t amax = 8 * kBias, kSlot = 8 * 32 * 4;
-  static constexpr uint32_t bytes = amax + 2 * kSlot;
+  static constexpr uint32_t box = amax + 2 * kSlot, kBox = 32 * 32;   // a warp's, 32 rows of 32 bytes
+  static constexpr uint32_t bytes = box + 8 * kBox;
 };
 
 // Scale byte of the lane's block, from its 64 values and the other warp's.
@@ -430,13 +441,14 @@ __device__ __forceinline__ void store_codes64(const float (&v)[kHalf], uint32_t 
     }
   }
 }
-// v += 64 elements of a row, and 64 elements to a row, of which `left` exist.
+// v += 64 elements of a row, and 64 elements to a row, of which `left` exist;
+// the rows start on 16 bytes.
 template <typename T>
-__device__ __forceinline__ void add_row64(float (&v)[kHalf], const T* p, int64_t left, bool vec, bool wide) {
+__device__ __forceinline__ void add_row64(float (&v)[kHalf], const T* p, int64_t left, bool wide) {
   constexpr int kPer = 32 / static_cast<int>(sizeof(T));
 #pragma unroll
   for (int q = 0; q < kHalf; q += kPer) {
-    if (vec && left >= q + kPer) {
+    if (left >= q + kPer) {
       alignas(16) uint32_t w[8];
       load_words8(p + q, wide, w);
 #pragma unroll
@@ -449,11 +461,11 @@ __device__ __forceinline__ void add_row64(float (&v)[kHalf], const T* p, int64_t
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_row64(const float (&v)[kHalf], T* p, int64_t left, bool vec, bool wide) {
+__device__ __forceinline__ void store_row64(const float (&v)[kHalf], T* p, int64_t left, bool wide) {
   constexpr int kPer = 32 / static_cast<int>(sizeof(T));
 #pragma unroll
   for (int q = 0; q < kHalf; q += kPer) {
-    if (vec && left >= q + kPer) {
+    if (left >= q + kPer) {
       uint4 w[2] = {pack16<T>(&v[q]), pack16<T>(&v[q + kPer / 2])};
       store_words8(p + q, wide, reinterpret_cast<const uint32_t*>(w));
     } else {
@@ -461,6 +473,61 @@ __device__ __forceinline__ void store_row64(const float (&v)[kHalf], T* p, int64
       for (int i = 0; i < kPer; ++i)
         if (q + i < left) p[q + i] = from_f32<T>(v[q + i]);
     }
+  }
+}
+// Rows that start anywhere go through the warp's box, 32 bytes of each of its 32
+// rows at a time, so that consecutive lanes hold consecutive elements. p: element
+// (0, 0) of the warp's 32 x 64; rows, cols: how many of them exist.
+template <typename T>
+struct Box {
+  static constexpr int kPer = 32 / static_cast<int>(sizeof(T)), kRows = 32 / kPer;   // elements; rows an access
+  static __device__ __forceinline__ uint32_t piece(uint32_t box, int row, int p) {
+    return box + row * 32 + 16 * (p ^ ((row >> 2) & 1));
+  }
+  static __device__ __forceinline__ uint32_t element(uint32_t box, int row, int e) {
+    constexpr int kEs = sizeof(T);
+    return piece(box, row, (e * kEs) >> 4) + ((e * kEs) & 15);
+  }
+};
+template <typename T>
+__device__ __forceinline__ void add_rows_anywhere(float (&v)[kHalf], const T* p, int64_t ld, int rows, int cols,
+                                                  uint32_t box) {
+  using B = Box<T>;
+  const int lane = threadIdx.x & 31, e = lane % B::kPer, r0 = lane / B::kPer;
+#pragma unroll
+  for (int q = 0; q < kHalf; q += B::kPer) {
+    T in[B::kPer];
+#pragma unroll
+    for (int k = 0; k < B::kPer; ++k) {
+      const int r = r0 + k * B::kRows;
+      in[k] = r < rows && q + e < cols ? p[r * ld + q + e] : from_f32<T>(0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < B::kPer; ++k) store_staged<T>(B::element(box, r0 + k * B::kRows, e), in[k]);
+    __syncwarp();
+    alignas(16) uint4 w[2] = {lds128(B::piece(box, lane, 0)), lds128(B::piece(box, lane, 1))};
+#pragma unroll
+    for (int i = 0; i < B::kPer; ++i) v[q + i] += to_f32(reinterpret_cast<const T*>(w)[i]);
+    __syncwarp();
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_rows_anywhere(const float (&v)[kHalf], T* p, int64_t ld, int rows, int cols,
+                                                    uint32_t box) {
+  using B = Box<T>;
+  const int lane = threadIdx.x & 31, e = lane % B::kPer, r0 = lane / B::kPer;
+#pragma unroll
+  for (int q = 0; q < kHalf; q += B::kPer) {
+    sts128(B::piece(box, lane, 0), pack16<T>(&v[q]));
+    sts128(B::piece(box, lane, 1), pack16<T>(&v[q + B::kPer / 2]));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < B::kPer; ++k) {
+      const int r = r0 + k * B::kRows;
+      const T out = load_staged<T>(B::element(box, r, e));
+      if (r < rows && q + e < cols) p[r * ld + q + e] = out;
+    }
+    __syncwarp();
   }
 }
 
@@ -478,6 +545,7 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t biases = base + S::staging + LinearShared::bias + (warp - 4) * LinearShared::kBias;
   const uint32_t slots = base + S::staging + LinearShared::amax;
+  const uint32_t box = base + S::staging + LinearShared::box + (warp - 4) * LinearShared::kBox;
   const uint32_t tempty0 = in_cta(base + S::tempty, 0);
   uint32_t u = 0, turn = 0;
   for (int64_t t = pair; t < tiles; t += pairs) {
@@ -560,8 +628,20 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
         store_codes64(v, b, a.y_codes + m * a.y_ld + n, left, a.wide_y);
         if (scales) a.y_scales[m * a.y_lds + kblock] = static_cast<uint8_t>(b);
       } else {
-        if (a.add) add_row64(v, static_cast<const T*>(a.add) + m * a.ldadd + n, left, a.vec_add, a.wide_add);
-        store_row64(v, static_cast<T*>(a.out) + m * a.ldo + n, left, a.vec_out, a.wide_out);
+        const int rows = static_cast<int>(a.M - (m - lane) < 32 ? a.M - (m - lane) : 32);
+        const int cols = static_cast<int>(a.N - n < kHalf ? a.N - n : kHalf);
+        if (a.add) {
+          const T* const p = static_cast<const T*>(a.add) + n;
+          if (a.vec_add)
+            add_row64(v, p + m * a.ldadd, left, a.wide_add);
+          else
+            add_rows_anywhere(v, p + (m - lane) * a.ldadd, a.ldadd, rows, cols, box);
+        }
+        T* const p = static_cast<T*>(a.out) + n;
+        if (a.vec_out)
+          store_row64(v, p + m * a.ldo, left, a.wide_out);
+        else
+          store_rows_anywhere(v, p + (m - lane) * a.ldo, a.ldo, rows, cols, box);
       }
     }
     if constexpr (!kSeg) ++u;
