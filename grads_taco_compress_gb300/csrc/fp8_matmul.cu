@@ -355,8 +355,9 @@ struct LinearFp8Args : LinearArgs {
 };
 template <typename Args>
 constexpr bool kFp8Out = std::is_same<Args, LinearFp8Args>::value;
+constexpr int kEpilogueWarps = 16;
 template <typename Args>
-constexpr int pair_threads() { return std::is_same<Args, MatmulArgs>::value ? kThreads : kThreads + 128; }
+constexpr int pair_threads() { return std::is_same<Args, MatmulArgs>::value ? kThreads : 128 + 32 * kEpilogueWarps; }
 
 __device__ __forceinline__ float bias_at(const LinearArgs& a, int64_t n) {
   if (!a.bias) return 0.0f;
@@ -380,74 +381,60 @@ __device__ __forceinline__ void store_block4(const float (&v)[4], int64_t left, 
   if ((threadIdx.x & 31) == 0) *scale = static_cast<uint8_t>(b);
 }
 
-// The layer's epilogue has 8 warps: two share 32 rows of the accumulator, and
-// each takes 64 of the 128 columns of a block, a row a lane. So a lane's 64
-// values stay in registers from the accumulator to the last rounding, whatever
-// is made of them, and the largest magnitude of a block is two lanes' to
-// exchange, through shared memory and a barrier of the two warps. Rows go out
-// by whole 32-byte sectors of a lane. Half the values a thread (and 4 registers
-// a value less) also halve the time an accumulator is held.
-constexpr int kHalf = kFp8Block / 2;
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" :: "r"(id) : "memory"); }
-// Whether `pred` holds in any lane of the two warps, the same in all of them.
-__device__ __forceinline__ bool pair_any(int id, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r) : "r"(static_cast<uint32_t>(pred)), "r"(id) : "memory");
-  return r != 0;
-}
+// The layer's epilogue has 16 warps: four share 32 rows of the accumulator, and
+// each takes 32 of the 128 columns of a block, a row a lane. So a lane's values
+// stay in registers from the accumulator to the last rounding, whatever is made
+// of them, and the largest magnitude of a block is four lanes' to exchange,
+// through shared memory and a barrier of the four warps. Rows go out by whole
+// 32-byte sectors of a lane.
+constexpr int kPart = kFp8Block / 4;
 // Shared memory of the epilogue in the place of the output's staging: each
 // warp's bias for the two blocks of a tile, and two slots of largest magnitudes.
 struct LinearShared {
-  static constexpr uint32_t bias = 0, kBias = 2 * kHalf * 4;
-  static constexpr uint32_t amax = 8 * kBias, kSlot = 8 * 32 * 4;
-  static constexpr uint32_t box = amax + 2 * kSlot, kBox = 32 * 32;   // a warp's, 32 rows of 32 bytes
-  static constexpr uint32_t bytes = box + 8 * kBox;
+  static constexpr uint32_t bias = 0, kBias = 2 * kPart * 4;
+  static constexpr uint32_t amax = kEpilogueWarps * kBias, kSlot = kEpilogueWarps * 32 * 4;
+  static constexpr uint32_t box = amax + 2 * kSlot, kBox = 32 * 16;   // a warp's, 32 rows of 16 bytes
+  static constexpr uint32_t bytes = box + kEpilogueWarps * kBox;
 };
 
-// Scale byte of the lane's block, from its 64 values and the other warp's.
-// `turn` counts the exchanges: a slot is written again two barriers after it was
-// read.
-__device__ __forceinline__ uint32_t block_scale(const float (&v)[kHalf], uint32_t slots, int quad, int half,
+// Scale byte of the lane's block, from its values and those of the other three
+// warps. `turn` counts the exchanges: a slot is written again two barriers after
+// it was read.
+__device__ __forceinline__ uint32_t block_scale(const float (&v)[kPart], uint32_t slots, int quad, int part,
                                                 uint32_t& turn) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t at = slots + (turn & 1u) * LinearShared::kSlot + (quad * 32 + lane) * 4;
+  const uint32_t at = slots + (turn & 1u) * LinearShared::kSlot + (quad * 32 + (threadIdx.x & 31)) * 16;
   const uint32_t mine = __float_as_uint(amax_of(v));
-  asm volatile("st.shared.u32 [%0], %1;" :: "r"(at + half * 512), "r"(mine) : "memory");
-  pair_sync(1 + quad);
+  asm volatile("st.shared.u32 [%0], %1;" :: "r"(at + 4 * part), "r"(mine) : "memory");
+  group_sync(1 + quad);
   ++turn;
-  return fp8_scale_byte(max(mine, lds_u32(at + (half ^ 1) * 512)));
+  const uint4 all = lds128(at);
+  return fp8_scale_byte(max(max(all.x, all.y), max(all.z, all.w)));
 }
-// 64 codes of a row of which `left` exist.
-__device__ __forceinline__ void store_codes64(const float (&v)[kHalf], uint32_t b, uint8_t* p, int64_t left, bool wide) {
+// 32 codes of a row of which `left` exist.
+__device__ __forceinline__ void store_codes32(const float (&v)[kPart], uint32_t b, uint8_t* p, int64_t left, bool wide) {
   const float inv = fp8_inverse_scale(b);
+  uint4 c[2];
 #pragma unroll
-  for (int q = 0; q < kHalf; q += 32) {
-    uint4 c[2];
+  for (int h = 0; h < 2; ++h) {
+    float t[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float t[16];
+    for (int i = 0; i < 16; ++i) t[i] = v[16 * h + i];
+    c[h] = codes16(t, inv);
+  }
+  if (left >= kPart) {
+    store_words8(p, wide, reinterpret_cast<const uint32_t*>(c));
+  } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = v[q + 16 * h + i];
-      c[h] = codes16(t, inv);
-    }
-    if (left >= q + 32) {
-      store_words8(p + q, wide, reinterpret_cast<const uint32_t*>(c));
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) store_codes16(p + q + 16 * h, clamp16(left - q - 16 * h), c[h]);
-    }
+    for (int h = 0; h < 2; ++h) store_codes16(p + 16 * h, clamp16(left - 16 * h), c[h]);
   }
 }
-// v += 64 elements of a row, and 64 elements to a row, of which `left` exist;
+// v += 32 elements of a row, and 32 elements to a row, of which `left` exist;
 // the rows start on 16 bytes.
 template <typename T>
-__device__ __forceinline__ void add_row64(float (&v)[kHalf], const T* p, int64_t left, bool wide) {
+__device__ __forceinline__ void add_row32(float (&v)[kPart], const T* p, int64_t left, bool wide) {
   constexpr int kPer = 32 / static_cast<int>(sizeof(T));
 #pragma unroll
-  for (int q = 0; q < kHalf; q += kPer) {
+  for (int q = 0; q < kPart; q += kPer) {
     if (left >= q + kPer) {
       alignas(16) uint32_t w[8];
       load_words8(p + q, wide, w);
@@ -461,10 +448,10 @@ __device__ __forceinline__ void add_row64(float (&v)[kHalf], const T* p, int64_t
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_row64(const float (&v)[kHalf], T* p, int64_t left, bool wide) {
+__device__ __forceinline__ void store_row32(const float (&v)[kPart], T* p, int64_t left, bool wide) {
   constexpr int kPer = 32 / static_cast<int>(sizeof(T));
 #pragma unroll
-  for (int q = 0; q < kHalf; q += kPer) {
+  for (int q = 0; q < kPart; q += kPer) {
     if (left >= q + kPer) {
       uint4 w[2] = {pack16<T>(&v[q]), pack16<T>(&v[q + kPer / 2])};
       store_words8(p + q, wide, reinterpret_cast<const uint32_t*>(w));
@@ -475,27 +462,21 @@ __device__ __forceinline__ void store_row64(const float (&v)[kHalf], T* p, int64
     }
   }
 }
-// Rows that start anywhere go through the warp's box, 32 bytes of each of its 32
+// Rows that start anywhere go through the warp's box, 16 bytes of each of its 32
 // rows at a time, so that consecutive lanes hold consecutive elements. p: element
-// (0, 0) of the warp's 32 x 64; rows, cols: how many of them exist.
+// (0, 0) of the warp's 32 x 32; rows, cols: how many of them exist.
 template <typename T>
 struct Box {
-  static constexpr int kPer = 32 / static_cast<int>(sizeof(T)), kRows = 32 / kPer;   // elements; rows an access
-  static __device__ __forceinline__ uint32_t piece(uint32_t box, int row, int p) {
-    return box + row * 32 + 16 * (p ^ ((row >> 2) & 1));
-  }
-  static __device__ __forceinline__ uint32_t element(uint32_t box, int row, int e) {
-    constexpr int kEs = sizeof(T);
-    return piece(box, row, (e * kEs) >> 4) + ((e * kEs) & 15);
-  }
+  static constexpr int kPer = 16 / static_cast<int>(sizeof(T)), kRows = 32 / kPer;   // elements; rows an access
 };
 template <typename T>
-__device__ __forceinline__ void add_rows_anywhere(float (&v)[kHalf], const T* p, int64_t ld, int rows, int cols,
+__device__ __forceinline__ void add_rows_anywhere(float (&v)[kPart], const T* p, int64_t ld, int rows, int cols,
                                                   uint32_t box) {
   using B = Box<T>;
   const int lane = threadIdx.x & 31, e = lane % B::kPer, r0 = lane / B::kPer;
+  const uint32_t mine = box + lane * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
-  for (int q = 0; q < kHalf; q += B::kPer) {
+  for (int q = 0; q < kPart; q += B::kPer) {
     T in[B::kPer];
 #pragma unroll
     for (int k = 0; k < B::kPer; ++k) {
@@ -503,36 +484,36 @@ __device__ __forceinline__ void add_rows_anywhere(float (&v)[kHalf], const T* p,
       in[k] = r < rows && q + e < cols ? p[r * ld + q + e] : from_f32<T>(0.0f);
     }
 #pragma unroll
-    for (int k = 0; k < B::kPer; ++k) store_staged<T>(B::element(box, r0 + k * B::kRows, e), in[k]);
+    for (int k = 0; k < B::kPer; ++k) store_staged<T>(mine + 32 * k * static_cast<uint32_t>(sizeof(T)), in[k]);
     __syncwarp();
-    alignas(16) uint4 w[2] = {lds128(B::piece(box, lane, 0)), lds128(B::piece(box, lane, 1))};
+    const uint4 w = lds128(box + 16 * lane);
 #pragma unroll
-    for (int i = 0; i < B::kPer; ++i) v[q + i] += to_f32(reinterpret_cast<const T*>(w)[i]);
+    for (int i = 0; i < B::kPer; ++i) v[q + i] += to_f32(reinterpret_cast<const T*>(&w)[i]);
     __syncwarp();
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_rows_anywhere(const float (&v)[kHalf], T* p, int64_t ld, int rows, int cols,
+__device__ __forceinline__ void store_rows_anywhere(const float (&v)[kPart], T* p, int64_t ld, int rows, int cols,
                                                     uint32_t box) {
   using B = Box<T>;
   const int lane = threadIdx.x & 31, e = lane % B::kPer, r0 = lane / B::kPer;
+  const uint32_t mine = box + lane * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
-  for (int q = 0; q < kHalf; q += B::kPer) {
-    sts128(B::piece(box, lane, 0), pack16<T>(&v[q]));
-    sts128(B::piece(box, lane, 1), pack16<T>(&v[q + B::kPer / 2]));
+  for (int q = 0; q < kPart; q += B::kPer) {
+    sts128(box + 16 * lane, pack16<T>(&v[q]));
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < B::kPer; ++k) {
       const int r = r0 + k * B::kRows;
-      const T out = load_staged<T>(B::element(box, r, e));
+      const T out = load_staged<T>(mine + 32 * k * static_cast<uint32_t>(sizeof(T)));
       if (r < rows && q + e < cols) p[r * ld + q + e] = out;
     }
     __syncwarp();
   }
 }
 
-// Warps 4 - 11 of the pair kernel. Neither of two warps leaves a tile's barriers
-// to the other: they decide together whether its sums have arrived.
+// Warps 4 - 19 of the pair kernel. None of four warps leaves a tile's barriers
+// to the others: they decide together whether its sums have arrived.
 template <typename T, int TN, typename Args>
 __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm, int64_t tiles, int64_t pair,
                                                 int64_t pairs, int kb, uint32_t base, uint32_t tmem, uint32_t rank,
@@ -541,7 +522,7 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
   static_assert(LinearShared::bytes <= 4 * S::kBoxes * 4096, "in the place of the staging");
   constexpr bool kSeg = std::is_same<T, float>::value;
   constexpr int kBlocks = TN / kFp8Block;
-  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, quad = warp & 3, half = (warp - 4) >> 2;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t biases = base + S::staging + LinearShared::bias + (warp - 4) * LinearShared::kBias;
   const uint32_t slots = base + S::staging + LinearShared::amax;
@@ -551,22 +532,22 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
   for (int64_t t = pair; t < tiles; t += pairs) {
     int64_t mt, nt;
     tm.at(t, mt, nt);
-    const int64_t m = mt * 256 + rank * 128 + quad * 32 + lane, n0 = nt * TN + half * kHalf;
+    const int64_t m = mt * 256 + rank * 128 + quad * 32 + lane, n0 = nt * TN + part * kPart;
     const bool row = m < a.M;
     __syncwarp();   // the last tile's bias has been read
 #pragma unroll
-    for (int c = 0; c < 2 * kBlocks; ++c) {
-      const int64_t n = n0 + (c >> 1) * kFp8Block + (c & 1) * 32 + lane;
+    for (int c = 0; c < kBlocks; ++c) {
+      const int64_t n = n0 + c * kFp8Block + lane;
       const float b = n < a.N ? bias_at(a, n) : 0.0f;
       asm volatile("st.shared.f32 [%0], %1;" :: "r"(biases + 4 * (c * 32 + lane)), "f"(b) : "memory");
     }
     __syncwarp();
-    float v[kHalf];
+    float v[kPart];
     bool ok = true;
     const int segments = kSeg ? (kb + kSegment - 1) / kSegment : 1;
     if constexpr (kSeg) {
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) v[i] = 0.0f;
+      for (int i = 0; i < kPart; ++i) v[i] = 0.0f;
     }
     for (int g = 0; g < segments && ok; ++g) {
       ok = wait_pair(base + S::tfull + 8 * (u & 1u), (u >> 1) & 1u, abort_flag) && *abort_flag == 0u;
@@ -575,12 +556,12 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
       tc_fence_after();
       if constexpr (kSeg) {
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 32) {
-          float part[32];
-          tmem_ld32(tmem + lanes + (u & 1u) * S::kAcc1 + half * kHalf + c, part);
-          tmem_ready32(part);
+        for (int c = 0; c < kPart; c += 32) {
+          float seg[32];
+          tmem_ld32(tmem + lanes + (u & 1u) * S::kAcc1 + part * kPart + c, seg);
+          tmem_ready32(seg);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[c + i] += part[i];
+          for (int i = 0; i < 32; ++i) v[c + i] += seg[i];
         }
         tc_fence_before();
         __syncwarp();
@@ -588,18 +569,18 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
         ++u;
       }
     }
-    if (pair_any(1 + quad, !ok)) break;
-#pragma unroll
+    if (group_any(1 + quad, !ok)) break;
+#pragma unroll 1
     for (int c = 0; c < kBlocks; ++c) {
       // the columns that the accumulators share first: accumulator 0's last, accumulator 1's first
       const int block = kBlocks == 2 && (u & 1u) == 0u ? 1 - c : c;
       if constexpr (!kSeg) {
-        const uint32_t acc = tmem + lanes + (u & 1u) * S::kAcc1 + block * kFp8Block + half * kHalf;
+        const uint32_t acc = tmem + lanes + (u & 1u) * S::kAcc1 + block * kFp8Block + part * kPart;
 #pragma unroll
-        for (int i = 0; i < kHalf; i += 16) tmem_ld16(acc + i, v + i);
+        for (int i = 0; i < kPart; i += 16) tmem_ld16(acc + i, v + i);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < kHalf; i += 16) reg_fence16(v + i);
+        for (int i = 0; i < kPart; i += 16) reg_fence16(v + i);
         if (c == 0) {
           tc_fence_before();
           __syncwarp();
@@ -607,8 +588,8 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
         }
       }
 #pragma unroll
-      for (int i = 0; i < kHalf; i += 4) {
-        const uint4 b = lds128(biases + 4 * (block * kHalf + i));
+      for (int i = 0; i < kPart; i += 4) {
+        const uint4 b = lds128(biases + 4 * (block * kPart + i));
         v[i] += __uint_as_float(b.x);
         v[i + 1] += __uint_as_float(b.y);
         v[i + 2] += __uint_as_float(b.z);
@@ -616,30 +597,30 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
       }
       const int64_t n = n0 + block * kFp8Block, left = row ? a.N - n : 0;
       const int64_t kblock = n / kFp8Block;
-      const bool scales = row && half == 0 && n < a.N;
+      const bool scales = row && part == 0 && n < a.N;
       if (a.k_codes) {
-        const uint32_t b = block_scale(v, slots, quad, half, turn);
-        store_codes64(v, b, a.k_codes + m * a.k_ld + n, left, a.wide_k);
+        const uint32_t b = block_scale(v, slots, quad, part, turn);
+        store_codes32(v, b, a.k_codes + m * a.k_ld + n, left, a.wide_k);
         if (scales) a.k_scales[m * a.k_lds + kblock] = static_cast<uint8_t>(b);
       }
       activate(v, a.act);
       if constexpr (kFp8Out<Args>) {
-        const uint32_t b = block_scale(v, slots, quad, half, turn);
-        store_codes64(v, b, a.y_codes + m * a.y_ld + n, left, a.wide_y);
+        const uint32_t b = block_scale(v, slots, quad, part, turn);
+        store_codes32(v, b, a.y_codes + m * a.y_ld + n, left, a.wide_y);
         if (scales) a.y_scales[m * a.y_lds + kblock] = static_cast<uint8_t>(b);
       } else {
         const int rows = static_cast<int>(a.M - (m - lane) < 32 ? a.M - (m - lane) : 32);
-        const int cols = static_cast<int>(a.N - n < kHalf ? a.N - n : kHalf);
+        const int cols = static_cast<int>(a.N - n < kPart ? a.N - n : kPart);
         if (a.add) {
           const T* const p = static_cast<const T*>(a.add) + n;
           if (a.vec_add)
-            add_row64(v, p + m * a.ldadd, left, a.wide_add);
+            add_row32(v, p + m * a.ldadd, left, a.wide_add);
           else
             add_rows_anywhere(v, p + (m - lane) * a.ldadd, a.ldadd, rows, cols, box);
         }
         T* const p = static_cast<T*>(a.out) + n;
         if (a.vec_out)
-          store_row64(v, p + m * a.ldo, left, a.wide_out);
+          store_row32(v, p + m * a.ldo, left, a.wide_out);
         else
           store_rows_anywhere(v, p + (m - lane) * a.ldo, a.ldo, rows, cols, box);
       }
@@ -679,7 +660,7 @@ matmul_pair_kernel(const __grid_constant__ MatmulMaps maps, const __grid_constan
     for (int s = 0; s < 2; ++s) {
       mbar_init(base + S::sdone + 8 * s, 1);
       mbar_init(base + S::tfull + 8 * s, 1);
-      mbar_init(base + S::tempty + 8 * s, kLinear ? 16 : 8);   // the epilogue warps of both CTAs
+      mbar_init(base + S::tempty + 8 * s, kLinear ? 2 * kEpilogueWarps : 8);   // the epilogue warps of both CTAs
     }
     for (int w = 0; w < 4; ++w) mbar_init(base + S::added + 8 * w, 1);
     mbar_init(base + S::done, 1);
