@@ -18,7 +18,8 @@ from .binding import (  # noqa: F401
     workspace_bytes,
 )
 from .fp8 import (  # noqa: F401
-    Fp8Tensor, RmsNormOutput, fp8_empty, taco_fp8_quantize, taco_linear_fp8, taco_matmul_fp8,
+    Fp8Tensor, RmsNormOutput, fp8_empty, taco_fp8_quantize, taco_linear_fp8,
+    taco_linear_fp8_backward, taco_matmul_fp8,
     taco_rms_norm_fp8, taco_rms_norm_fp8_backward, taco_swiglu_fp8, taco_swiglu_fp8_backward,
 )
 from .optim import AdamState, AdamW, taco_adam_state, taco_adamw, taco_grad_norm  # noqa: F401

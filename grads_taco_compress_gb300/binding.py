@@ -52,6 +52,7 @@ EXPORTED_SYMBOLS = (
     "taco_adamw", "taco_grad_norm", "taco_grad_norm_workspace_bytes",
     "taco_rms_norm_fp8", "taco_rms_norm_workspace_bytes", "taco_rms_norm_fp8_backward",
     "taco_swiglu_fp8", "taco_swiglu_fp8_backward", "taco_matmul_fp8", "taco_linear_fp8",
+    "taco_linear_backward_workspace_bytes", "taco_linear_fp8_backward",
     "taco_get_fault", "taco_selftest_wait_timeout",
     "taco_status_string", "taco_abi_version",
 )
@@ -114,6 +115,8 @@ def _lib() -> ctypes.CDLL:
             "taco_swiglu_fp8_backward": (i32, [vp, i64, vp, vp, i32, i64, i64, vp, i64, vp, i64, vp]),
             "taco_matmul_fp8": (i32, [vp, vp, vp, i64, vp, i64, i32, vp]),
             "taco_linear_fp8": (i32, [vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp, vp, vp]),
+            "taco_linear_backward_workspace_bytes": (sz, [i64, i64]),
+            "taco_linear_fp8_backward": (i32, [vp, i64, i32, i64, i64, vp, i32, vp, vp, vp, vp, sz, vp]),
             "taco_adamw": (i32, [vp, i64, f64, vp, f64, f64, f64, vp, vp, vp]),
             "taco_grad_norm_workspace_bytes": (sz, [i64]),
             "taco_grad_norm": (i32, [vp, i64, f64, vp, vp, sz, vp]),

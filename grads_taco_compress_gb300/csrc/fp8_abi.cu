@@ -485,4 +485,64 @@ taco_status taco_linear_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
   return done(launch_linear(l, dtype, dev->sms, dev->clusters, static_cast<cudaStream_t>(stream)));
 }
 
+size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N) {
+  if (M < 0 || N < 1 || M > kMaxSide || N > kMaxSide || M <= 128) return 0;
+  return static_cast<size_t>((M + 127) / 128) * static_cast<size_t>(N) * sizeof(float);
+}
+
+taco_status taco_linear_fp8_backward(const void* dy, int64_t lddy, int dtype, int64_t M, int64_t N,
+                                     const taco_fp8_tensor* checkpoint, int activation,
+                                     const taco_fp8_tensor* rows_out, const taco_fp8_tensor* cols_out, float* db,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype) || !valid_act(activation)) return TACO_ERR_ARG;
+  if (M < 0 || N < 1 || M > kMaxSide || N > kMaxSide) return TACO_ERR_SHAPE;
+  if (!rows_out && !cols_out && !db) return TACO_ERR_NULL;
+  if (activation != TACO_ACT_NONE && !checkpoint) return TACO_ERR_NULL;
+  if (activation == TACO_ACT_NONE && checkpoint) return TACO_ERR_ARG;
+  Region in[3], out[6];
+  int vec = kVec32;
+  TACO_TRY(check_matrix(dy, M, N, lddy, dtype, &in[0], &vec));
+  if (checkpoint) TACO_TRY(check_fp8(checkpoint, M, N, false, &in[1], &in[2]));
+  if (rows_out) TACO_TRY(check_fp8(rows_out, M, N, false, &out[0], &out[1]));
+  // a transpose of no rows has no columns: nothing to describe or write
+  const bool nothing = cols_out && M == 0 && cols_out->rows == N && cols_out->cols == 0;
+  if (cols_out && !nothing) TACO_TRY(check_fp8(cols_out, N, M, false, &out[2], &out[3]));
+  if (db) TACO_TRY(check_matrix(db, 1, N, N, TACO_DTYPE_F32, &out[4], nullptr));
+  const size_t need = db ? taco_linear_backward_workspace_bytes(M, N) : 0;
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return TACO_ERR_WORKSPACE;
+    if (addr(workspace) % 16) return TACO_ERR_ALIGN;
+    out[5] = Region{addr(workspace), 1, static_cast<int64_t>(need), static_cast<int64_t>(need)};
+  }
+  TACO_TRY(check_apart(in, 3, out, 6));
+  if (((M + 127) / 128) * ((N + 127) / 128) > kMaxSide) return TACO_ERR_SHAPE;
+  const auto st = static_cast<cudaStream_t>(stream);
+  if (M == 0) return db ? done(cudaMemsetAsync(db, 0, static_cast<size_t>(N) * sizeof(float), st)) : TACO_OK;
+  LinearBackwardArgs a{};
+  a.dy = dy;
+  a.lddy = lddy;
+  a.M = M;
+  a.N = N;
+  a.act = activation;
+  if (checkpoint) {
+    a.k_codes = checkpoint->codes;
+    a.k_scales = checkpoint->scales;
+    a.k_ld = checkpoint->ld_codes;
+    a.k_lds = checkpoint->ld_scales;
+  }
+  if (rows_out) {
+    a.codes = rows_out->codes;
+    a.scales = rows_out->scales;
+    a.ldc = rows_out->ld_codes;
+    a.lds = rows_out->ld_scales;
+  }
+  if (cols_out) {
+    a.t_codes = cols_out->codes;
+    a.t_scales = cols_out->scales;
+    a.t_ldc = cols_out->ld_codes;
+    a.t_lds = cols_out->ld_scales;
+  }
+  return done(launch_linear_backward(a, dtype, vec, db, static_cast<float*>(workspace), st));
+}
+
 }  // extern "C"

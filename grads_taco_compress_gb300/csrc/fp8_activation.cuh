@@ -69,6 +69,20 @@ __device__ __forceinline__ f2 activate2(f2 x) {
   }
 }
 
+// x within [-limit, limit], a NaN as it is. Beyond the limits below a slope is 0
+// or 1 to fp32's last bit, and within them 2^t stays below 2^126.
+__device__ __forceinline__ f2 clamp2(f2 x, float limit) {
+  f2 r;
+  asm("{ .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3; }" : "=f"(r.x) : "f"(x.x), "f"(limit), "f"(-limit));
+  asm("{ .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3; }" : "=f"(r.y) : "f"(x.y), "f"(limit), "f"(-limit));
+  return r;
+}
+// s (1 + w (1 - s)) of s = 1 / (1 + e), with 1 - s = e s to its own precision.
+__device__ __forceinline__ f2 logistic_slope(f2 e, f2 w) {
+  const f2 d = add2(e, both(1.0f)), s{reciprocal(d.x), reciprocal(d.y)};
+  return mul2(s, fma2(w, mul2(e, s), both(1.0f)));
+}
+
 template <int ACT>
 __device__ __forceinline__ f2 slope2(f2 x) {
   if constexpr (ACT == TACO_ACT_GELU) {
@@ -77,19 +91,15 @@ __device__ __forceinline__ f2 slope2(f2 x) {
     const f2 phi{x.x < 0.0f ? h.x : 1.0f - h.x, x.y < 0.0f ? h.y : 1.0f - h.y};
     return fma2(mul2(x, e), both(0.39894228f), phi);
   } else if constexpr (ACT == TACO_ACT_GELU_TANH) {
-    // s (1 + x (1 - s) c (1 + 3 a x^2)): where s is 0 or 1 the product with 1 - s
-    // is small against 1 or the whole is, and x^3 stays far below infinity
-    const f2 q = mul2(x, x);
-    const f2 t = fma2(q, both(-kTanhC * kTanhA * kLog2e), both(-kTanhC * kLog2e));
-    const f2 s = logistic2(mul2(x, t));
-    const f2 r = fma2(s, both(-1.0f), both(1.0f));
-    const f2 w = mul2(x, fma2(q, both(3.0f * kTanhC * kTanhA), both(kTanhC)));
-    return mul2(s, fma2(w, r, both(1.0f)));
+    const f2 c = clamp2(x, 9.5f), q = mul2(c, c);
+    const f2 e = ex2_2(mul2(c, fma2(q, both(-kTanhC * kTanhA * kLog2e), both(-kTanhC * kLog2e))));
+    return logistic_slope(e, mul2(c, fma2(q, both(3.0f * kTanhC * kTanhA), both(kTanhC))));
   } else if constexpr (ACT == TACO_ACT_SILU) {
-    const f2 s = logistic2(mul2(x, both(-kLog2e)));
-    return mul2(s, fma2(x, fma2(s, both(-1.0f), both(1.0f)), both(1.0f)));
+    const f2 c = clamp2(x, 64.0f);
+    return logistic_slope(ex2_2(mul2(c, both(-kLog2e))), c);
   } else if constexpr (ACT == TACO_ACT_RELU) {
-    return f2{x.x > 0.0f ? 1.0f : 0.0f, x.y > 0.0f ? 1.0f : 0.0f};
+    const auto step = [](float v) { return v > 0.0f ? 1.0f : v <= 0.0f ? 0.0f : v; };   // a NaN stays one
+    return f2{step(x.x), step(x.y)};
   } else {
     return both(1.0f);
   }

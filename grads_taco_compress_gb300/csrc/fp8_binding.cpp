@@ -566,6 +566,60 @@ PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// linear_backward(dy, checkpoint, activation, rows, cols, bias, out, out_t, db, workspace, stream)
+//   -> rows, transpose, db
+PyObject* linear_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(v, n, 11, [&]() -> PyObject* {
+    const at::Tensor& dy = tensor(v[0], "dy");
+    const Matrix m = matrix(dy, "dy");
+    if (m.cols < 1) refuse("dy must have a column");
+    const int act = activation(v[2]);
+    std::optional<Pair> ck, out, out_t;
+    taco_fp8_tensor cd{}, a{}, b{};
+    if (given(v[1])) {
+      ck = pair_of(v[1], "checkpoint");
+      cd = describe(ck->codes, ck->scales, "checkpoint");
+    }
+    if ((act != TACO_ACT_NONE) != ck.has_value())
+      refuse(ck ? "a checkpoint is read where there is an activation" : "an activation's slope takes the checkpoint");
+    const bool rows = flag(v[3], "rows"), cols = flag(v[4], "cols"), bias = flag(v[5], "bias");
+    if (!rows && !cols && !bias) refuse("nothing to compute: rows, cols and bias are all false");
+    at::Tensor db, ws;
+    if (rows && given(v[6])) out = pair_of(v[6], "out");
+    if (cols && given(v[7])) out_t = pair_of(v[7], "out_t");
+    if (bias && given(v[8])) {
+      db = tensor(v[8], "db");
+      vector(db, "db", m.cols, true);
+    }
+    if (out) a = describe(out->codes, out->scales, "out");
+    if (out_t) b = describe(out_t->codes, out_t->scales, "out_t");
+    if (given(v[9])) {
+      ws = tensor(v[9], "workspace");
+      if (!ws.is_cuda() || !ws.is_contiguous()) refuse("workspace must be a contiguous CUDA tensor");
+    }
+    const OnStream on(v[10], dy);
+    if (rows && !out) {
+      out = new_fp8({m.rows, m.cols}, 1);
+      a = describe(out->codes, out->scales, "out");
+    }
+    if (cols && !out_t) {
+      out_t = new_fp8({m.cols, m.rows}, 1);
+      b = describe(out_t->codes, out_t->scales, "out_t");
+    }
+    if (bias && !db.defined()) db = empty_vector(m.cols, at::kFloat);
+    if (bias && !ws.defined())
+      ws = empty_vector(static_cast<int64_t>(taco_linear_backward_workspace_bytes(m.rows, m.cols)), at::kByte);
+    void* stream = on.handle();
+    const taco_status st = call([&] {
+      return taco_linear_fp8_backward(m.p, m.ld, m.dtype, m.rows, m.cols, ck ? &cd : nullptr, act, out ? &a : nullptr,
+                                      out_t ? &b : nullptr, bias ? static_cast<float*>(db.data_ptr()) : nullptr,
+                                      ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream);
+    });
+    if (st != TACO_OK) return PyLong_FromLong(st);
+    return tuple(&PyTuple_Type, {object(out), object(out_t), bias ? object(db) : none()});
+  });
+}
+
 // ------------------------------------------------------- many tensors ----
 // What a message calls a tensor, put together only where there is a message.
 struct Name {
@@ -768,7 +822,7 @@ PyObject* types(PyObject*, PyObject* const* v, Py_ssize_t n) {
 PyMethodDef kMethods[] = {TACO_METHOD(types), TACO_METHOD(quantize), TACO_METHOD(rms_norm),
                           TACO_METHOD(rms_norm_backward),
                           TACO_METHOD(swiglu), TACO_METHOD(swiglu_backward), TACO_METHOD(matmul),
-                          TACO_METHOD(linear), TACO_METHOD(adamw), TACO_METHOD(grad_norm),
+                          TACO_METHOD(linear), TACO_METHOD(linear_backward), TACO_METHOD(adamw), TACO_METHOD(grad_norm),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8_binding", "Argument marshalling of the FP8 entry points.", -1,
                        kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -259,6 +259,22 @@ struct LinearArgs : MatmulArgs {
   bool wide_out, wide_add, wide_y, wide_k;     // rows all start on 32 bytes
 };
 
+struct LinearBackwardArgs {
+  const void* dy;
+  int64_t lddy, M, N;
+  int act;                  // TACO_ACT_NONE: no checkpoint
+  const uint8_t* k_codes;
+  const uint8_t* k_scales;
+  int64_t k_ld, k_lds;
+  uint8_t* codes;           // rows out; may be null
+  uint8_t* scales;
+  int64_t ldc, lds;
+  uint8_t* t_codes;         // transpose out; may be null
+  uint8_t* t_scales;
+  int64_t t_ldc, t_lds;
+  float* sums;              // column sums of each 128 rows; may be null
+};
+
 cudaError_t launch_norm(const NormArgs& a, int dtype, int vec, cudaStream_t st);
 // Most CTAs, and so rows of partial sums, of the norm's backward pass on rows of
 // H (512 at 2048 columns and more, up to 2048 of shorter rows).
@@ -274,6 +290,9 @@ cudaError_t prepare_matmul(int* clusters);
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
 cudaError_t launch_linear(const LinearArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
 cudaError_t matmul_fault(unsigned int* bits, bool clear);
+// db: the columns' sums (null: none), through `workspace` where there are more than 128 rows.
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, int dtype, int vec, float* db, float* workspace,
+                                   cudaStream_t st);
 
 // ---- Many tensors at once (adamw.cu, grad_norm.cu) ----
 struct AdamwEntry {

@@ -186,3 +186,19 @@ def taco_linear_fp8(x: Fp8Tensor, w: Fp8Tensor, bias: torch.Tensor | None = None
     if type(r) is int:
         _check(r, "taco_linear_fp8")
     return r
+
+
+def taco_linear_fp8_backward(dy: torch.Tensor, checkpoint: Fp8Tensor | None = None, activation: str | None = None,
+                             rows: bool = True, cols: bool = True, bias: bool = True, out: Fp8Tensor | None = None,
+                             out_t: Fp8Tensor | None = None, db: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """d = dy act'(pre) of dy [M, N], from taco_linear_fp8's checkpoint of pre (no
+    activation: d is dy, without one), as the products of the input's and of the
+    weight's gradient read it. Returns (d as an Fp8Tensor [M, N], its transpose as
+    one [N, M], the bias's gradient f32 [N]), None for each whose flag is not set.
+    ``workspace``: taco_linear_backward_workspace_bytes(M, N) bytes."""
+    r = _binding().linear_backward(dy, checkpoint, activation, rows, cols, bias, out, out_t, db, workspace,
+                                   _handle(stream))
+    if type(r) is int:
+        _check(r, "taco_linear_fp8_backward")
+    return r

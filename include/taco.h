@@ -474,6 +474,20 @@ taco_status taco_linear_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
                             void* out, int64_t ldo, int dtype, const taco_fp8_tensor* y_fp8,
                             const taco_fp8_tensor* checkpoint, void* stream);
 
+/* Its gradient at pre, d = dy * act'(pre), quantised once from fp32 as the two
+ * products that follow read it: its rows [M, N] to rows_out (dx = d b), its
+ * transpose [N, M] to cols_out (db = d^T a), and db [N] (f32), the sum of d's
+ * rows in a fixed order; any of the three may be NULL, not all. pre is read from
+ * `checkpoint` (tile_rows 1); without an activation d is dy, and checkpoint is
+ * NULL. Outputs have tile_rows 1. RELU's slope at 0 is 0. `workspace`
+ * (taco_linear_backward_workspace_bytes bytes, 16-byte aligned, not zeroed) may
+ * be NULL where db is, or where M <= 128. M == 0 zeroes db. */
+size_t taco_linear_backward_workspace_bytes(int64_t M, int64_t N);
+taco_status taco_linear_fp8_backward(const void* dy, int64_t lddy, int dtype, int64_t M, int64_t N,
+                                     const taco_fp8_tensor* checkpoint, int activation,
+                                     const taco_fp8_tensor* rows_out, const taco_fp8_tensor* cols_out,
+                                     float* db, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- Many tensors at once ---------------------------------------------------
  * What a training step does with a model's gradients: their norm, and an AdamW
  * step. A call takes a host array of `count` tensors (0 .. 2^20, read before
