@@ -69,16 +69,22 @@ __device__ __forceinline__ f2 activate2(f2 x) {
   }
 }
 
-// x within [-limit, limit], a NaN as it is. Beyond the limits below a slope is 0
-// or 1 to fp32's last bit, and within them 2^t stays below 2^126.
-__device__ __forceinline__ f2 clamp2(f2 x, float limit) {
-  f2 r;
-  asm("{ .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3; }" : "=f"(r.x) : "f"(x.x), "f"(limit), "f"(-limit));
-  asm("{ .reg .f32 t;\n min.NaN.f32 t, %1, %2;\n max.NaN.f32 %0, t, %3; }" : "=f"(r.y) : "f"(x.y), "f"(limit), "f"(-limit));
-  return r;
+// Slopes take values up to 448 * 2^10 as they are (x^3 is far from fp32's end);
+// larger ones are brought within [-64, 64] first, where every slope is 0 or 1 to
+// fp32's last bit already, a NaN as it is. Whole blocks share the check, by their
+// scale: above 2^kSlopeBinades.
+constexpr uint32_t kSlopeBinades = 10;
+template <int ACT, int N>
+__device__ __forceinline__ void limit_for_slope(float (&x)[N]) {
+  if (ACT == TACO_ACT_RELU) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm("{ .reg .f32 t;\n min.NaN.f32 t, %0, 0f42800000;\n max.NaN.f32 %0, t, 0fC2800000; }" : "+f"(x[i]));
 }
-// s (1 + w (1 - s)) of s = 1 / (1 + e), with 1 - s = e s to its own precision.
-__device__ __forceinline__ f2 logistic_slope(f2 e, f2 w) {
+// s (1 + w (1 - s)) of s = 1 / (1 + 2^t), with 1 - s = 2^t s to its own
+// precision. 2^t is held at 2^100, where s is small enough for any w (below 2^60).
+__device__ __forceinline__ f2 logistic_slope(f2 t, f2 w) {
+  const f2 e = ex2_2(f2{fminf(t.x, 100.0f), fminf(t.y, 100.0f)});
   const f2 d = add2(e, both(1.0f)), s{reciprocal(d.x), reciprocal(d.y)};
   return mul2(s, fma2(w, mul2(e, s), both(1.0f)));
 }
@@ -91,12 +97,11 @@ __device__ __forceinline__ f2 slope2(f2 x) {
     const f2 phi{x.x < 0.0f ? h.x : 1.0f - h.x, x.y < 0.0f ? h.y : 1.0f - h.y};
     return fma2(mul2(x, e), both(0.39894228f), phi);
   } else if constexpr (ACT == TACO_ACT_GELU_TANH) {
-    const f2 c = clamp2(x, 9.5f), q = mul2(c, c);
-    const f2 e = ex2_2(mul2(c, fma2(q, both(-kTanhC * kTanhA * kLog2e), both(-kTanhC * kLog2e))));
-    return logistic_slope(e, mul2(c, fma2(q, both(3.0f * kTanhC * kTanhA), both(kTanhC))));
+    const f2 q = mul2(x, x);
+    const f2 t = mul2(x, fma2(q, both(-kTanhC * kTanhA * kLog2e), both(-kTanhC * kLog2e)));
+    return logistic_slope(t, mul2(x, fma2(q, both(3.0f * kTanhC * kTanhA), both(kTanhC))));
   } else if constexpr (ACT == TACO_ACT_SILU) {
-    const f2 c = clamp2(x, 64.0f);
-    return logistic_slope(ex2_2(mul2(c, both(-kLog2e))), c);
+    return logistic_slope(mul2(x, both(-kLog2e)), x);
   } else if constexpr (ACT == TACO_ACT_RELU) {
     const auto step = [](float v) { return v > 0.0f ? 1.0f : v <= 0.0f ? 0.0f : v; };   // a NaN stays one
     return f2{step(x.x), step(x.y)};

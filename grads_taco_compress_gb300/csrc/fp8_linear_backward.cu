@@ -4,118 +4,239 @@
 // of dy and of the checkpoint. d itself is never written: it is quantised from
 // fp32, rounded once.
 //
-// A CTA takes a 128 x 128 tile, each thread 4 consecutive rows of 16 columns,
-// whose d stay in registers. Largest magnitudes and sums of the columns meet in
-// shared memory. Tiles write their column sums; a second kernel adds them in the
-// order of the rows.
+// A CTA takes a 128 x 128 tile, each of 512 threads 4 consecutive rows of 8
+// columns, whose d stay in registers (with 256 threads and 16 columns they take
+// twice the registers, and half the warps could not hide the latencies of the
+// tile's phases). Largest magnitudes and sums of the columns meet in shared
+// memory; the transposed codes go through it, 4 rows of a column to a word, so that
+// they leave as whole 128-byte rows. Tiles write their column sums; a second kernel
+// adds them in the order of the rows.
 
 #include "fp8_activation.cuh"
-#include "fp8_tile.cuh"
 
 namespace taco {
 
 namespace {
 
+constexpr int kThreads = 512;
+constexpr int kCols = 8;                        // of a thread
+constexpr int kLanes = kFp8Block / kCols;       // that share a row's block
+
+// Eight consecutive elements of a row, as they lie in memory.
+template <typename T>
+struct Row8 {
+  static constexpr int kWords = 2 * static_cast<int>(sizeof(T));
+  uint32_t w[kWords];
+};
+// n (0 .. 8) of them exist, the others read as zero. VEC: p is 16-byte aligned.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kTileThreads, 2)
-linear_backward_kernel(LinearBackwardArgs a, Divider per_row, bool wide) {
+__device__ __forceinline__ Row8<T> load8(const T* p, int n) {
+  Row8<T> r;
+  if (VEC && n == kCols) {
+#pragma unroll
+    for (int i = 0; i < Row8<T>::kWords / 4; ++i)
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(r.w[4 * i]), "=r"(r.w[4 * i + 1]), "=r"(r.w[4 * i + 2]), "=r"(r.w[4 * i + 3])
+                   : "l"(reinterpret_cast<const char*>(p) + 16 * i));
+  } else if constexpr (VEC) {   // the end of a row
+    alignas(16) T v[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] = i < n ? p[i] : from_f32<T>(0.0f);
+    memcpy(r.w, v, sizeof(v));
+  } else {
+    load_shifted(p, n, r.w);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void unpack8(const Row8<T>& r, float (&v)[kCols]) {
+#pragma unroll
+  for (int i = 0; i < kCols / 2; ++i) {
+    if constexpr (std::is_same<T, float>::value) {
+      v[2 * i] = __uint_as_float(r.w[2 * i]);
+      v[2 * i + 1] = __uint_as_float(r.w[2 * i + 1]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = bf16_lo(r.w[i]);
+      v[2 * i + 1] = bf16_hi(r.w[i]);
+    }
+  }
+}
+__device__ __forceinline__ uint2 load_codes8(const uint8_t* p, int n) {
+  if (n == kCols) {
+    uint2 c;
+    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(c.x), "=r"(c.y) : "l"(p));
+    return c;
+  }
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kCols; ++i)
+    if (i < n) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes8(uint8_t* p, int n, uint2 c) {
+  if (n == kCols) {
+    *reinterpret_cast<uint2*>(p) = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+      if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+  }
+}
+__device__ __forceinline__ uint32_t codes4(f2 a, f2 b, float inv) {
+  const f2 x = mul2(a, both(inv)), y = mul2(b, both(inv));
+  return e4m3x4_from_f32(x.x, x.y, y.x, y.y);
+}
+
+// Word of the transposed tile that holds rows 4 r4 .. 4 r4 + 3 of column c: 32
+// words a column, in the order r4 ^ 2 (c / 8), so that a warp, which writes one
+// column of each of its 16 lane groups at a time, in two words, meets 32 banks.
+__device__ __forceinline__ int word_of_tile(int c, int r4) { return c * 32 + (r4 ^ (2 * (c / kCols))); }
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBackwardArgs a, Divider per_row) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ __align__(16) uint32_t words[kFp8Block * 32];
-  __shared__ __align__(16) uint32_t col_max[kTileThreads / 32][kFp8Block];
-  __shared__ __align__(16) float col_sum[kTileThreads / 32][kFp8Block];
+  __shared__ __align__(16) uint32_t col_max[kWarps][kFp8Block];
+  __shared__ __align__(16) float col_sum[kWarps][kFp8Block];
   __shared__ __align__(16) float col_inv[kFp8Block];
   const int64_t rb = per_row.quotient(blockIdx.x);
   const int64_t cb = blockIdx.x - rb * static_cast<int64_t>(per_row.d);
-  const int lane8 = threadIdx.x & 7, r4 = threadIdx.x >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x & (kLanes - 1), r4 = threadIdx.x / kLanes, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
-  const int64_t row = r0 + 4 * r4, col = c0 + 16 * lane8;
-  const int n = clamp16(a.N - col), rows = clamp4(a.M - row);
+  const int64_t row = r0 + 4 * r4, col = c0 + kCols * group;
+  const int n = static_cast<int>(a.N - col < 0 ? 0 : a.N - col < kCols ? a.N - col : kCols);
+  const int rows = static_cast<int>(a.M - row < 0 ? 0 : a.M - row < 4 ? a.M - row : 4);
   grid_launch_dependents();
   grid_dependency_wait();
 
-  const T* const p = static_cast<const T*>(a.dy) + row * a.lddy + col;
-  float d[4][16];
+  float d[4][kCols];
   {
-    Row16<T> g[4];
-    uint4 codes[4];
+    Row8<T> g[4];
+    uint2 codes[4];
     uint32_t scale[4];
+    const T* const p = static_cast<const T*>(a.dy) + row * a.lddy + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) g[i] = load16<T, VEC>(p + i * a.lddy, i < rows ? n : 0, wide);
+    for (int i = 0; i < 4; ++i) g[i] = load8<T, VEC>(p + i * a.lddy, i < rows ? n : 0);
     if (a.act != TACO_ACT_NONE) {
+      const uint8_t* const k = a.k_codes + row * a.k_ld + col;
+      const uint8_t* const s = a.k_scales + row * a.k_lds + cb;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool any = i < rows && n > 0;
-        codes[i] = load_codes16(a.k_codes + (row + i) * a.k_ld + col, any ? n : 0);
-        scale[i] = any ? a.k_scales[(row + i) * a.k_lds + cb] : kScaleOne;
+        codes[i] = load_codes8(k + i * a.k_ld, any ? n : 0);
+        scale[i] = any ? s[i * a.k_lds] : kScaleOne;
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack<T>(g[i], d[i]);
+    for (int i = 0; i < 4; ++i) unpack8<T>(g[i], d[i]);
     with_act(a.act, [&](auto kind) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float x[16];
-        decode16(codes[i], fp8_scale(scale[i]), x);
+        float x[kCols];
+        const float s = fp8_scale(scale[i]);
+        decode4(codes[i].x, s, x);
+        decode4(codes[i].y, s, x + 4);
+        // beyond this values no slope's arithmetic holds as it is
+        if (scale[i] > kScaleOne + kSlopeBinades) limit_for_slope<decltype(kind)::value>(x);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
+        for (int e = 0; e < kCols; e += 2) {
           const f2 y = mul2(f2{d[i][e], d[i][e + 1]}, slope2<decltype(kind)::value>(f2{x[e], x[e + 1]}));
           d[i][e] = y.x;
           d[i][e + 1] = y.y;
         }
         if (scale[i] == kScaleNan) {   // which must not reach columns that do not exist
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < kCols; ++e)
             if (e >= n) d[i][e] = 0.0f;
         }
       }
     });
   }
   if (a.codes) {
+    uint8_t* const q = a.codes + row * a.ldc + col;
+    uint8_t* const s = a.scales + row * a.lds + cb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      quantize16(d[i], i < rows ? n : 0, a.codes + (row + i) * a.ldc + col, a.scales + (row + i) * a.lds + cb, lane8);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = fp8_scale_byte(group_umax<kLanes>(amax_of(d[i])));
+      const float inv = fp8_inverse_scale(b);
+      if (i < rows && n > 0) {
+        store_codes8(q + i * a.ldc, n,
+                     make_uint2(codes4(f2{d[i][0], d[i][1]}, f2{d[i][2], d[i][3]}, inv),
+                                codes4(f2{d[i][4], d[i][5]}, f2{d[i][6], d[i][7]}, inv)));
+        if (group == 0) s[i * a.lds] = static_cast<uint8_t>(b);
+      }
+    }
   }
+  {
+    // The columns of the warp's two lanes that hold other rows of them: each hands
+    // half of its columns to the other and keeps the other half.
+    uint32_t top[kCols];
+    float sum[kCols];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    // over the thread's 4 rows and the 4 lanes of the warp with the same columns
-    uint32_t top = __float_as_uint(amax3(amax3(0.0f, d[0][e], d[1][e]), d[2][e], d[3][e]));
-    float sum = (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
+    for (int e = 0; e < kCols; ++e) {
+      top[e] = __float_as_uint(amax3(amax3(0.0f, d[0][e], d[1][e]), d[2][e], d[3][e]));
+      sum[e] = (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
+    }
+    const bool high = lane & 16;
+    uint32_t t[4];
+    float u[4];
 #pragma unroll
-    for (int m = 8; m < 32; m <<= 1) {
-      top = max(top, __shfl_xor_sync(kFullMask, top, m));
-      sum += __shfl_xor_sync(kFullMask, sum, m);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t other = __shfl_xor_sync(kFullMask, high ? top[e] : top[e + 4], 16);
+      t[e] = max(high ? top[e + 4] : top[e], other);
+      const float more = __shfl_xor_sync(kFullMask, high ? sum[e] : sum[e + 4], 16);
+      u[e] = (high ? sum[e + 4] : sum[e]) + more;
     }
-    if (lane < 8) {
-      col_max[warp][16 * lane8 + e] = top;
-      col_sum[warp][16 * lane8 + e] = sum;
-    }
+    const int c = kCols * group + (high ? 4 : 0);
+    *reinterpret_cast<uint4*>(&col_max[warp][c]) = make_uint4(t[0], t[1], t[2], t[3]);
+    *reinterpret_cast<float4*>(&col_sum[warp][c]) = make_float4(u[0], u[1], u[2], u[3]);
   }
   __syncthreads();
-  if (threadIdx.x < kFp8Block) {
-    const int c = threadIdx.x;
-    uint32_t top = 0;
-    float sum = 0.0f;
+  if (threadIdx.x < 2 * kFp8Block) {   // 128 threads join the maxima, 128 the sums
+    const int c = threadIdx.x & (kFp8Block - 1);
+    const bool exists = c0 + c < a.N;
+    if (threadIdx.x < kFp8Block) {
+      uint32_t top = 0;
 #pragma unroll
-    for (int w = 0; w < kTileThreads / 32; ++w) {
-      top = max(top, col_max[w][c]);
-      sum += col_sum[w][c];
-    }
-    const uint32_t b = fp8_scale_byte(top);
-    col_inv[c] = fp8_inverse_scale(b);
-    if (c0 + c < a.N) {
-      if (a.t_codes) a.t_scales[(c0 + c) * a.t_lds + rb] = static_cast<uint8_t>(b);
-      if (a.sums) a.sums[rb * a.N + c0 + c] = sum;
+      for (int w = 0; w < kWarps; ++w) top = max(top, col_max[w][c]);
+      const uint32_t b = fp8_scale_byte(top);
+      col_inv[c] = fp8_inverse_scale(b);
+      if (exists && a.t_codes) a.t_scales[(c0 + c) * a.t_lds + rb] = static_cast<uint8_t>(b);
+    } else if (a.sums) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += col_sum[w][c];
+      if (exists) a.sums[rb * a.N + c0 + c] = sum;
     }
   }
   if (!a.t_codes) return;
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int c = 16 * lane8 + e;
-    const float inv = col_inv[c];
-    words[tile_word(c, r4)] = e4m3x4_from_f32(d[0][e] * inv, d[1][e] * inv, d[2][e] * inv, d[3][e] * inv);
+  for (int e = 0; e < kCols; e += 4) {
+    const float4 inv = *reinterpret_cast<const float4*>(&col_inv[kCols * group + e]);
+    const float f[4] = {inv.x, inv.y, inv.z, inv.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      words[word_of_tile(kCols * group + e + j, r4)] =
+          codes4(f2{d[0][e + j], d[1][e + j]}, f2{d[2][e + j], d[3][e + j]}, f[j]);
   }
   __syncthreads();
-  store_transposed(a.t_codes, a.t_ldc, a.M, a.N, words, r0, c0, lane8, r4);
+  // 8 lanes write the 128 codes of a column, 16 each
+  const int lane8 = threadIdx.x & 7;
+  const int left = clamp16(a.M - r0 - 16 * lane8);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = (threadIdx.x >> 3) + 64 * i;
+    const int swap = 2 * ((c / kCols) & 1);   // the order's last bit but one, within four words
+    uint4 w = *reinterpret_cast<const uint4*>(&words[word_of_tile(c, 4 * lane8) & ~3]);
+    if (swap) w = make_uint4(w.z, w.w, w.x, w.y);
+    if (c0 + c < a.N) store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, left, w);
+  }
 }
 
 // Sums of the columns of [rows, N], a warp 32 columns of every eighth row, joined
@@ -152,8 +273,8 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& args, int dtype, in
   const dim3 grid(static_cast<unsigned>(per_row.d * tiles));
   const cudaError_t e = with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return vec ? launch_dependent(linear_backward_kernel<T, true>, grid, kTileThreads, 0, st, a, per_row, vec == kVec32)
-               : launch_dependent(linear_backward_kernel<T, false>, grid, kTileThreads, 0, st, a, per_row, false);
+    return launch_dependent(vec ? linear_backward_kernel<T, true> : linear_backward_kernel<T, false>, grid, kThreads, 0,
+                            st, a, per_row);
   });
   if (e != cudaSuccess || !db || tiles == 1) return e;
   return launch_dependent(column_sums_kernel, dim3(static_cast<unsigned>((a.N + 31) / 32)), 256, 0, st,

@@ -18,13 +18,13 @@
 // the transpose of 8192 x 1600 codes 8.1 us at 780 instructions a thread, 53% of
 // the issue slots and 1.4 waves of CTAs (13.7 us and 1500 in fp32).
 
-#include "fp8_tile.cuh"
+#include "fp8_block.cuh"
 
 namespace taco {
 
 namespace {
 
-constexpr int kThreads = kTileThreads;
+constexpr int kThreads = 256;
 
 struct Fp8Source {};   // the source is codes and scales
 
@@ -130,6 +130,12 @@ __device__ __forceinline__ void read_tile(const QuantizeArgs& a, int64_t rb, int
     for (int i = 0; i < 4; ++i) r[i] = load16<T, VEC>(p + i * a.ldx, i < rows ? n : 0, wide);
   }
 }
+__device__ __forceinline__ int clamp4(int64_t left) { return left < 0 ? 0 : (left > 4 ? 4 : static_cast<int>(left)); }
+
+// Word of the transposed tile that holds rows 4 r4 .. 4 r4 + 3 of column c: 32
+// words a column, in the order r4 ^ 4 (c / 16 % 8). A warp writes one column
+// of each of its 8 lane groups at a time, 4 words apiece: 32 banks.
+__device__ __forceinline__ int tile_word(int c, int r4) { return c * 32 + (r4 ^ (4 * ((c >> 4) & 7))); }
 
 // The largest magnitudes of a tile's columns. 16-bit types (and re-blocked
 // codes, below) stay packed, pairs of columns to a word: with the sign cleared
@@ -187,6 +193,19 @@ __device__ __forceinline__ void pair_bits(uint32_t w, uint32_t (&b)[2]) {
   } else {
     b[0] = w << 16;
     b[1] = w & 0xffff0000u;
+  }
+}
+
+// 8 lanes write the 128 codes of one column of the transposed tile, 16 each.
+__device__ __forceinline__ void store_transposed(const QuantizeArgs& a, const uint32_t* words, int64_t r0, int64_t c0,
+                                                 int lane8, int r4) {
+  const int n = clamp16(a.M - r0 - 16 * lane8);
+  const int64_t left = a.K - c0 - r4;
+  uint8_t* const p = a.t_codes + (c0 + r4) * a.t_ldc + r0 + 16 * lane8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(&words[tile_word(32 * i + r4, 4 * lane8)]);
+    store_codes16(p + 32 * i * a.t_ldc, 32 * i < left ? n : 0, w);
   }
 }
 
@@ -370,7 +389,7 @@ transpose_codes_kernel(QuantizeArgs a, Divider per_row) {
     }
   }
   __syncthreads();
-  store_transposed(a.t_codes, a.t_ldc, a.M, a.K, words, r0, c0, lane8, r4);
+  store_transposed(a, words, r0, c0, lane8, r4);
 }
 
 // CTAs per SM that the tile kernel's registers are held to, with 2, 3 and 4 (and
@@ -490,7 +509,7 @@ quantize_tile_kernel(QuantizeArgs a, Divider per_row, bool wide) {
       }
     }
     __syncthreads();
-    store_transposed(a.t_codes, a.t_ldc, a.M, a.K, words, r0, c0, lane8, r4);
+    store_transposed(a, words, r0, c0, lane8, r4);
   }
 }
 
