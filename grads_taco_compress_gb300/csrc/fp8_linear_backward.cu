@@ -96,23 +96,22 @@ __device__ __forceinline__ uint32_t codes4(f2 a, f2 b, float inv) {
 // column of each of its 16 lane groups at a time, in two words, meets 32 banks.
 __device__ __forceinline__ int word_of_tile(int c, int r4) { return c * 32 + (r4 ^ (2 * (c / kCols))); }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBackwardArgs a, Divider per_row) {
+struct TileShared {
+  uint4 words[kFp8Block * 32 / 4];              // the transposed codes
+  uint4 tops[kThreads / 32][kFp8Block / 4];     // of a warp's rows, by column
+  float4 sums[kThreads / 32][kFp8Block / 4];
+  float4 inv[kFp8Block / 4];
+};
+// One tile. FULL: all of it exists, and nothing is checked.
+template <typename T, bool VEC, bool FULL>
+__device__ __forceinline__ void backward_tile(const LinearBackwardArgs& a, int64_t rb, int64_t cb, TileShared& sh) {
   constexpr int kWarps = kThreads / 32;
-  __shared__ __align__(16) uint32_t words[kFp8Block * 32];
-  __shared__ __align__(16) uint32_t col_max[kWarps][kFp8Block];
-  __shared__ __align__(16) float col_sum[kWarps][kFp8Block];
-  __shared__ __align__(16) float col_inv[kFp8Block];
-  const int64_t rb = per_row.quotient(blockIdx.x);
-  const int64_t cb = blockIdx.x - rb * static_cast<int64_t>(per_row.d);
   const int group = threadIdx.x & (kLanes - 1), r4 = threadIdx.x / kLanes, lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
   const int64_t row = r0 + 4 * r4, col = c0 + kCols * group;
-  const int n = static_cast<int>(a.N - col < 0 ? 0 : a.N - col < kCols ? a.N - col : kCols);
-  const int rows = static_cast<int>(a.M - row < 0 ? 0 : a.M - row < 4 ? a.M - row : 4);
-  grid_launch_dependents();
-  grid_dependency_wait();
+  const int n = FULL ? kCols : static_cast<int>(a.N - col < 0 ? 0 : a.N - col < kCols ? a.N - col : kCols);
+  const int rows = FULL ? 4 : static_cast<int>(a.M - row < 0 ? 0 : a.M - row < 4 ? a.M - row : 4);
 
   float d[4][kCols];
   {
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBack
           d[i][e] = y.x;
           d[i][e + 1] = y.y;
         }
-        if (scale[i] == kScaleNan) {   // which must not reach columns that do not exist
+        if (!FULL && scale[i] == kScaleNan) {   // which must not reach columns that do not exist
 #pragma unroll
           for (int e = 0; e < kCols; ++e)
             if (e >= n) d[i][e] = 0.0f;
@@ -158,18 +157,34 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBack
     });
   }
   if (a.codes) {
+    // The largest magnitudes of the 4 rows over their 16 lanes: two exchanges hand
+    // half of a lane's rows to the partner, so that lane l joins row l / 4 % 4 alone
+    // and forms one scale.
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __float_as_uint(amax_of(d[i]));
+    const bool b8 = lane & 8, b4 = lane & 4;
+    const uint32_t o0 = __shfl_xor_sync(kFullMask, b8 ? m[0] : m[2], 8);
+    const uint32_t o1 = __shfl_xor_sync(kFullMask, b8 ? m[1] : m[3], 8);
+    const uint32_t k0 = max(b8 ? m[2] : m[0], o0), k1 = max(b8 ? m[3] : m[1], o1);
+    uint32_t top = max(b4 ? k1 : k0, __shfl_xor_sync(kFullMask, b4 ? k0 : k1, 4));
+    top = max(top, __shfl_xor_sync(kFullMask, top, 2));
+    top = max(top, __shfl_xor_sync(kFullMask, top, 1));
+    const uint32_t b = fp8_scale_byte(top);
+    const float inv = fp8_inverse_scale(b);
+    const int mine = (lane >> 2) & 3;
+    if ((lane & 3) == 0 && (FULL || (row + mine < a.M)))
+      a.scales[(row + mine) * a.lds + cb] = static_cast<uint8_t>(b);
     uint8_t* const q = a.codes + row * a.ldc + col;
-    uint8_t* const s = a.scales + row * a.lds + cb;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = fp8_scale_byte(group_umax<kLanes>(amax_of(d[i])));
-      const float inv = fp8_inverse_scale(b);
-      if (i < rows && n > 0) {
-        store_codes8(q + i * a.ldc, n,
-                     make_uint2(codes4(f2{d[i][0], d[i][1]}, f2{d[i][2], d[i][3]}, inv),
-                                codes4(f2{d[i][4], d[i][5]}, f2{d[i][6], d[i][7]}, inv)));
-        if (group == 0) s[i * a.lds] = static_cast<uint8_t>(b);
-      }
+      const float f = __shfl_sync(kFullMask, inv, (lane & 16) + 4 * i);
+      const uint2 c = make_uint2(codes4(f2{d[i][0], d[i][1]}, f2{d[i][2], d[i][3]}, f),
+                                 codes4(f2{d[i][4], d[i][5]}, f2{d[i][6], d[i][7]}, f));
+      if (FULL)
+        *reinterpret_cast<uint2*>(q + i * a.ldc) = c;
+      else
+        store_codes8(q + i * a.ldc, i < rows ? n : 0, c);
     }
   }
   {
@@ -180,7 +195,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBack
 #pragma unroll
     for (int e = 0; e < kCols; ++e) {
       top[e] = __float_as_uint(amax3(amax3(0.0f, d[0][e], d[1][e]), d[2][e], d[3][e]));
-      sum[e] = (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kCols; e += 2) {
+      const auto pair = [&](int r) { return f2{d[r][e], d[r][e + 1]}; };
+      const f2 s = add2(add2(pair(0), pair(1)), add2(pair(2), pair(3)));
+      sum[e] = s.x;
+      sum[e + 1] = s.y;
     }
     const bool high = lane & 16;
     uint32_t t[4];
@@ -193,32 +214,33 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBack
       u[e] = (high ? sum[e + 4] : sum[e]) + more;
     }
     const int c = kCols * group + (high ? 4 : 0);
-    *reinterpret_cast<uint4*>(&col_max[warp][c]) = make_uint4(t[0], t[1], t[2], t[3]);
-    *reinterpret_cast<float4*>(&col_sum[warp][c]) = make_float4(u[0], u[1], u[2], u[3]);
+    sh.tops[warp][c / 4] = make_uint4(t[0], t[1], t[2], t[3]);
+    sh.sums[warp][c / 4] = make_float4(u[0], u[1], u[2], u[3]);
   }
   __syncthreads();
   if (threadIdx.x < 2 * kFp8Block) {   // 128 threads join the maxima, 128 the sums
     const int c = threadIdx.x & (kFp8Block - 1);
-    const bool exists = c0 + c < a.N;
+    const bool exists = FULL || c0 + c < a.N;
     if (threadIdx.x < kFp8Block) {
       uint32_t top = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = max(top, col_max[w][c]);
+      for (int w = 0; w < kWarps; ++w) top = max(top, reinterpret_cast<const uint32_t*>(sh.tops[w])[c]);
       const uint32_t b = fp8_scale_byte(top);
-      col_inv[c] = fp8_inverse_scale(b);
+      reinterpret_cast<float*>(sh.inv)[c] = fp8_inverse_scale(b);
       if (exists && a.t_codes) a.t_scales[(c0 + c) * a.t_lds + rb] = static_cast<uint8_t>(b);
     } else if (a.sums) {
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += col_sum[w][c];
+      for (int w = 0; w < kWarps; ++w) sum += reinterpret_cast<const float*>(sh.sums[w])[c];
       if (exists) a.sums[rb * a.N + c0 + c] = sum;
     }
   }
   if (!a.t_codes) return;
   __syncthreads();
+  uint32_t* const words = reinterpret_cast<uint32_t*>(sh.words);
 #pragma unroll
   for (int e = 0; e < kCols; e += 4) {
-    const float4 inv = *reinterpret_cast<const float4*>(&col_inv[kCols * group + e]);
+    const float4 inv = sh.inv[2 * group + e / 4];
     const float f[4] = {inv.x, inv.y, inv.z, inv.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -228,15 +250,28 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBack
   __syncthreads();
   // 8 lanes write the 128 codes of a column, 16 each
   const int lane8 = threadIdx.x & 7;
-  const int left = clamp16(a.M - r0 - 16 * lane8);
+  const int left = FULL ? 16 : clamp16(a.M - r0 - 16 * lane8);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int c = (threadIdx.x >> 3) + 64 * i;
     const int swap = 2 * ((c / kCols) & 1);   // the order's last bit but one, within four words
     uint4 w = *reinterpret_cast<const uint4*>(&words[word_of_tile(c, 4 * lane8) & ~3]);
     if (swap) w = make_uint4(w.z, w.w, w.x, w.y);
-    if (c0 + c < a.N) store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, left, w);
+    if (FULL || c0 + c < a.N) store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, left, w);
   }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearBackwardArgs a, Divider per_row) {
+  __shared__ TileShared sh;
+  const int64_t rb = per_row.quotient(blockIdx.x);
+  const int64_t cb = blockIdx.x - rb * static_cast<int64_t>(per_row.d);
+  grid_launch_dependents();
+  grid_dependency_wait();
+  if (VEC && (rb + 1) * kFp8Block <= a.M && (cb + 1) * kFp8Block <= a.N)
+    backward_tile<T, VEC, true>(a, rb, cb, sh);
+  else
+    backward_tile<T, VEC, false>(a, rb, cb, sh);
 }
 
 // Sums of the columns of [rows, N], a warp 32 columns of every eighth row, joined

@@ -3,8 +3,8 @@
 Tolerance: a slope is a sum of a few factors of at most 1.2, each to some 2^-21
 of itself (reciprocal and exponential to 2^-22, the error function's formula to
 1.5e-7 / 2, the exponent's rounding), 2^-19 in all; d rounds once more. The
-bias's gradient adds 4 rows a thread, 4 lanes, 8 warps and then every eighth
-tile of 128 rows, 8 of those: 26 + M / 1024 roundings of at most 2^-24 of the
+bias's gradient adds 4 rows a thread, 32 threads' and then every eighth
+tile of 128 rows, 8 of those: less than 26 + M / 1024 roundings of at most 2^-24 of the
 magnitudes' sum.
 """
 
