@@ -241,11 +241,15 @@ __device__ __forceinline__ void backward_tile(const LinearBackwardArgs& a, int64
 #pragma unroll
   for (int e = 0; e < kCols; e += 4) {
     const float4 inv = sh.inv[2 * group + e / 4];
-    const float f[4] = {inv.x, inv.y, inv.z, inv.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      words[word_of_tile(kCols * group + e + j, r4)] =
-          codes4(f2{d[0][e + j], d[1][e + j]}, f2{d[2][e + j], d[3][e + j]}, f[j]);
+    for (int j = 0; j < 4; j += 2) {   // columns in pairs, which lie in pairs of registers
+      const f2 f = j ? f2{inv.z, inv.w} : f2{inv.x, inv.y};
+      f2 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = mul2(f2{d[i][e + j], d[i][e + j + 1]}, f);
+      words[word_of_tile(kCols * group + e + j, r4)] = e4m3x4_from_f32(x[0].x, x[1].x, x[2].x, x[3].x);
+      words[word_of_tile(kCols * group + e + j + 1, r4)] = e4m3x4_from_f32(x[0].y, x[1].y, x[2].y, x[3].y);
+    }
   }
   __syncthreads();
   // 8 lanes write the 128 codes of a column, 16 each
@@ -254,9 +258,9 @@ __device__ __forceinline__ void backward_tile(const LinearBackwardArgs& a, int64
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int c = (threadIdx.x >> 3) + 64 * i;
-    const int swap = 2 * ((c / kCols) & 1);   // the order's last bit but one, within four words
-    uint4 w = *reinterpret_cast<const uint4*>(&words[word_of_tile(c, 4 * lane8) & ~3]);
-    if (swap) w = make_uint4(w.z, w.w, w.x, w.y);
+    const int at = word_of_tile(c, 4 * lane8);   // two words, the other two at ^ 2
+    const uint2 lo = *reinterpret_cast<const uint2*>(&words[at]), hi = *reinterpret_cast<const uint2*>(&words[at ^ 2]);
+    const uint4 w = make_uint4(lo.x, lo.y, hi.x, hi.y);
     if (FULL || c0 + c < a.N) store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, left, w);
   }
 }
