@@ -41,6 +41,11 @@ struct AdamwTable {
   AdamwEntry t[CAP];
 };
 
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float sqrt_approx(float v) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -136,6 +141,108 @@ constexpr int adamw_ctas() { return SMALL ? 3 : 3; }
 
 // P, G: element types of parameters and gradients; SMALL: states in FP8 blocks;
 // VEC: every tensor of the table starts on 16 bytes.
+// What every chunk of a launch shares.
+struct StepFacts {
+  float gm, gv;        // factor (1 - b1); factor sqrt(1 - b2)
+  float rate;          // of m' over the denominator
+  float root_c, lr;
+  uint32_t weyl;       // of element 0 at this step
+};
+
+// The 16 elements of a thread in the chunk that begins at element `base` of a
+// tensor. WHOLE: the chunk's 4096 all exist; else n of the thread's do.
+template <typename P, typename G, bool SMALL, bool VEC, bool WHOLE>
+__device__ __forceinline__ void step16(const AdamwArgs& a, const AdamwEntry& en, const StepFacts& f, int64_t base,
+                                       int count) {
+  const uint32_t i0 = 16 * threadIdx.x;
+  const int n = WHOLE ? 16 : count;
+  const bool wide = en.wide;
+  const float keep = 1.0f - f.lr * en.decay;
+  P* const param = static_cast<P*>(en.param) + base + i0;
+  // b1 m and b2 v, or the root of the latter
+  float g[16], x[16], m[16], v[16];
+  const Row16<G> gr = load16<G, VEC>(static_cast<const G*>(en.grad) + base + i0, n, wide);
+  if (en.master)
+    unpack<float>(load16<float, VEC>(en.master + base + i0, n, wide), x);
+  else
+    unpack<P>(load16<P, VEC>(param, n, wide), x);
+  uint8_t *mc = nullptr, *vc = nullptr, *ms = nullptr, *vs = nullptr;
+  float *mf = nullptr, *vf = nullptr;
+  if constexpr (SMALL) {
+    mc = static_cast<uint8_t*>(en.m) + base + i0;
+    vc = static_cast<uint8_t*>(en.v) + base + i0;
+    ms = en.m_scales + base / kFp8Block + threadIdx.x / kBlockLanes;
+    vs = en.v_scales + base / kFp8Block + threadIdx.x / kBlockLanes;
+    const uint4 cm = load_codes16(mc, n), cv = load_codes16(vc, n);
+    const bool any = WHOLE || n > 0;
+    const uint32_t sm = any ? *ms : kScaleOne, sv = any ? *vs : kScaleOne;
+    decode16(cm, fp8_scale(sm) * a.b1, m);
+    decode16(cv, fp8_scale(sv) * a.root_b2, v);
+    if (!WHOLE && (sm == kScaleNan || sv == kScaleNan)) {   // which must not reach elements that do not exist
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i >= n) m[i] = v[i] = 0.0f;
+    }
+  } else {
+    mf = static_cast<float*>(en.m) + base + i0;
+    vf = static_cast<float*>(en.v) + base + i0;
+    unpack<float>(load16<float, VEC>(mf, n, wide), m);
+    unpack<float>(load16<float, VEC>(vf, n, wide), v);
+  }
+  unpack<G>(gr, g);
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    const f2 gi{g[i], g[i + 1]}, h = mul2(gi, f2{f.gv, f.gv});
+    f2 mi{m[i], m[i + 1]}, vi{v[i], v[i + 1]}, xi{x[i], x[i + 1]};
+    if (SMALL) {
+      mi = fma2(gi, f2{f.gm, f.gm}, mi);
+      vi = fma2(vi, vi, mul2(h, h));
+    } else {
+      mi = fma2(mi, f2{a.b1, a.b1}, mul2(gi, f2{f.gm, f.gm}));
+      vi = fma2(vi, f2{a.b2, a.b2}, mul2(h, h));
+    }
+    const f2 root{sqrt_approx(vi.x), sqrt_approx(vi.y)};
+    const f2 den = fma2(root, f2{f.root_c, f.root_c}, f2{a.eps, a.eps});
+    const f2 q = mul2(mi, f2{reciprocal(den.x), reciprocal(den.y)});
+    xi = fma2(q, f2{f.rate, f.rate}, mul2(xi, f2{keep, keep}));
+    m[i] = mi.x;
+    m[i + 1] = mi.y;
+    v[i] = SMALL ? root.x : vi.x;
+    v[i + 1] = SMALL ? root.y : vi.y;
+    x[i] = xi.x;
+    x[i + 1] = xi.y;
+  }
+  const uint32_t w = (static_cast<uint32_t>(base) + i0) * kWeylI + f.weyl;
+  if constexpr (std::is_same<P, float>::value) {
+    store16<P, VEC>(param, n, wide, pack<P>(x));
+  } else if (en.master) {
+    store16<float, VEC>(en.master + base + i0, n, wide, pack<float>(x));
+    store16<P, VEC>(param, n, wide, pack<P>(x));
+  } else {
+    store16<P, VEC>(param, n, wide, pack_by_threshold<P>(x, w));
+  }
+  if constexpr (SMALL) {
+    const uint32_t bm = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(m)));
+    const uint32_t bv = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(v)));
+    const uint4 cm = codes_by_threshold<true>(m, bm, w);
+    uint4 cv = codes_by_threshold<false>(v, bv, w);
+    if (any_zero_byte(cv)) keep_nonzero(cv, v);
+    if (WHOLE || n > 0) {
+      store_codes16(mc, n, cm);
+      store_codes16(vc, n, cv);
+      if (threadIdx.x % kBlockLanes == 0) {
+        *ms = static_cast<uint8_t>(bm);
+        *vs = static_cast<uint8_t>(bv);
+      }
+    }
+  } else {
+    store16<float, VEC>(mf, n, wide, pack<float>(m));
+    store16<float, VEC>(vf, n, wide, pack<float>(v));
+  }
+}
+
+// P, G: element types of parameters and gradients; SMALL: states in FP8 blocks;
+// VEC: every tensor of the table starts on 16 bytes.
 template <typename P, typename G, bool SMALL, bool VEC, int CAP>
 __global__ void __launch_bounds__(kOptimThreads, adamw_ctas<SMALL>())
 adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
@@ -147,93 +254,24 @@ adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
   const uint32_t step = static_cast<uint32_t>(*a.counter) + 1u;
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const float t = static_cast<float>(step);
-  const float rate = -lr / -expm1f(t * a.log_b1);            // of m' over the denominator
-  const float root_c = rsqrtf(-expm1f(t * a.log_b2));
-  const float gm = factor * a.one_b1, gv = factor * a.root_one_b2;
-  const int lane8 = threadIdx.x & 7;
+  StepFacts f;
+  f.gm = factor * a.one_b1;
+  f.gv = factor * a.root_one_b2;
+  f.rate = -lr / -expm1f(t * a.log_b1);
+  f.root_c = rsqrtf(-expm1f(t * a.log_b2));
+  f.lr = lr;
+  f.weyl = step * kWeylT;
   int e = 0;
   for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     e = tensor_of(table, c, e);
     const AdamwEntry& en = table.t[e];
-    const int64_t i0 = static_cast<int64_t>(c - en.first) * kOptimChunk + 16 * threadIdx.x;
-    const int n = clamp16(en.n - i0);
-    if (VEC && __all_sync(kFullMask, n == 0)) continue;   // rows that start anywhere are stored by whole warps
-    const bool wide = en.wide;
-    const float keep = 1.0f - lr * en.decay;
-    // b1 m and b2 v, or the root of the latter
-    float g[16], x[16], m[16], v[16];
-    const Row16<G> gr = load16<G, VEC>(static_cast<const G*>(en.grad) + i0, n, wide);
-    if (en.master)
-      unpack<float>(load16<float, VEC>(en.master + i0, n, wide), x);
-    else
-      unpack<P>(load16<P, VEC>(static_cast<const P*>(en.param) + i0, n, wide), x);
-    if constexpr (SMALL) {
-      const int64_t blk = i0 / kFp8Block;
-      const bool any = n > 0;
-      const uint4 cm = load_codes16(static_cast<const uint8_t*>(en.m) + i0, n);
-      const uint4 cv = load_codes16(static_cast<const uint8_t*>(en.v) + i0, n);
-      const uint32_t sm = any ? en.m_scales[blk] : kScaleOne, sv = any ? en.v_scales[blk] : kScaleOne;
-      decode16(cm, fp8_scale(sm) * a.b1, m);
-      decode16(cv, fp8_scale(sv) * a.root_b2, v);
-      if (n < 16 && (sm == kScaleNan || sv == kScaleNan)) {   // which must not reach elements that do not exist
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i >= n) m[i] = v[i] = 0.0f;
-      }
+    const int64_t base = static_cast<int64_t>(c - en.first) * kOptimChunk;
+    if (VEC && base + kOptimChunk <= en.n) {
+      step16<P, G, SMALL, VEC, true>(a, en, f, base, 16);
     } else {
-      unpack<float>(load16<float, VEC>(static_cast<const float*>(en.m) + i0, n, wide), m);
-      unpack<float>(load16<float, VEC>(static_cast<const float*>(en.v) + i0, n, wide), v);
-    }
-    unpack<G>(gr, g);
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const f2 gi{g[i], g[i + 1]}, h = mul2(gi, f2{gv, gv});
-      f2 mi{m[i], m[i + 1]}, vi{v[i], v[i + 1]}, xi{x[i], x[i + 1]};
-      if (SMALL) {
-        mi = fma2(gi, f2{gm, gm}, mi);
-        vi = fma2(vi, vi, mul2(h, h));
-      } else {
-        mi = fma2(mi, f2{a.b1, a.b1}, mul2(gi, f2{gm, gm}));
-        vi = fma2(vi, f2{a.b2, a.b2}, mul2(h, h));
-      }
-      const f2 root{sqrt_approx(vi.x), sqrt_approx(vi.y)};
-      const f2 den = fma2(root, f2{root_c, root_c}, f2{a.eps, a.eps});
-      const f2 q{__fdividef(mi.x, den.x), __fdividef(mi.y, den.y)};
-      xi = fma2(q, f2{rate, rate}, mul2(xi, f2{keep, keep}));
-      m[i] = mi.x;
-      m[i + 1] = mi.y;
-      v[i] = SMALL ? root.x : vi.x;
-      v[i + 1] = SMALL ? root.y : vi.y;
-      x[i] = xi.x;
-      x[i + 1] = xi.y;
-    }
-    const uint32_t w = static_cast<uint32_t>(i0) * kWeylI + step * kWeylT;
-    if constexpr (std::is_same<P, float>::value) {
-      store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack<P>(x));
-    } else if (en.master) {
-      store16<float, VEC>(en.master + i0, n, wide, pack<float>(x));
-      store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack<P>(x));
-    } else {
-      store16<P, VEC>(static_cast<P*>(en.param) + i0, n, wide, pack_by_threshold<P>(x, w));
-    }
-    if constexpr (SMALL) {
-      const int64_t blk = i0 / kFp8Block;
-      const uint32_t bm = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(m)));
-      const uint32_t bv = fp8_scale_byte(group_umax<kBlockLanes>(amax_of(v)));
-      const uint4 cm = codes_by_threshold<true>(m, bm, w);
-      uint4 cv = codes_by_threshold<false>(v, bv, w);
-      if (any_zero_byte(cv)) keep_nonzero(cv, v);
-      if (n > 0) {
-        store_codes16(static_cast<uint8_t*>(en.m) + i0, n, cm);
-        store_codes16(static_cast<uint8_t*>(en.v) + i0, n, cv);
-        if (lane8 == 0) {
-          en.m_scales[blk] = static_cast<uint8_t>(bm);
-          en.v_scales[blk] = static_cast<uint8_t>(bv);
-        }
-      }
-    } else {
-      store16<float, VEC>(static_cast<float*>(en.m) + i0, n, wide, pack<float>(m));
-      store16<float, VEC>(static_cast<float*>(en.v) + i0, n, wide, pack<float>(v));
+      const int n = clamp16(en.n - base - 16 * threadIdx.x);
+      if (VEC && __all_sync(kFullMask, n == 0)) continue;   // unaligned rows are stored by whole warps
+      step16<P, G, SMALL, VEC, false>(a, en, f, base, n);
     }
   }
   if (a.last) {
