@@ -8,6 +8,10 @@ namespace taco {
 
 namespace {
 
+// CTAs per SM. 64 bytes a thread at a time, 134M f32 and bf16 elements: 4: 86, 43.7 us,
+// 6: 79.6 and 41.8 us (1.00 and 0.95 of the copy peak).
+constexpr int kNormPerSm = 6;
+
 template <int CAP>
 struct GradTable {
   uint32_t chunks;
@@ -15,13 +19,33 @@ struct GradTable {
   GradEntry t[CAP];
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ float squares16(const void* p, int64_t i0, int n, bool wide) {
-  float v[16];
-  unpack<T>(load16<T, VEC>(static_cast<const T*>(p) + i0, n, wide), v);
-  f2 s{0.0f, 0.0f};
+// Of the thread's elements in a tensor's chunk, 64 bytes of them: 16 of every
+// 4096, all loaded before the first is used.
+template <typename T>
+__device__ __forceinline__ float squares(const GradEntry& en, uint32_t chunk) {
+  constexpr int64_t kElems = kNormChunkBytes / static_cast<int64_t>(sizeof(T));
+  constexpr int kParts = static_cast<int>(kElems / kOptimChunk);
+  const int64_t base = static_cast<int64_t>(chunk) * kElems + 16 * threadIdx.x;
+  const T* const p = static_cast<const T*>(en.p) + base;
+  Row16<T> r[kParts];
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) s = fma2(f2{v[i], v[i + 1]}, f2{v[i], v[i + 1]}, s);
+  for (int k = 0; k < kParts; ++k) {
+    const int n = clamp16(en.n - base - k * kOptimChunk);
+    const T* const q = n > 0 ? p + k * kOptimChunk : static_cast<const T*>(en.p);
+    r[k] = en.vec ? load16<T, true>(q, n, en.wide) : load16<T, false>(q, n, false);
+  }
+  f2 s{0.0f, 0.0f}, t{0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) {
+    float v[16];
+    unpack<T>(r[k], v);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      s = fma2(f2{v[i], v[i + 1]}, f2{v[i], v[i + 1]}, s);
+      t = fma2(f2{v[i + 2], v[i + 3]}, f2{v[i + 2], v[i + 3]}, t);
+    }
+  }
+  s = add2(s, t);
   return s.x + s.y;
 }
 
@@ -32,7 +56,7 @@ __device__ __forceinline__ double warp_sum64(double v) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kOptimThreads)
+__global__ void __launch_bounds__(kOptimThreads, kNormPerSm)
 grad_squares_kernel(const __grid_constant__ GradTable<CAP> table, double* partial) {
   __shared__ double sums[kOptimThreads / 32];
   grid_launch_dependents();
@@ -42,16 +66,12 @@ grad_squares_kernel(const __grid_constant__ GradTable<CAP> table, double* partia
   for (uint32_t c = blockIdx.x; c < table.chunks; c += gridDim.x) {
     e = tensor_of(table, c, e);
     const GradEntry& en = table.t[e];
-    const int64_t i0 = static_cast<int64_t>(c - en.first) * kOptimChunk + 16 * threadIdx.x;
-    const int n = clamp16(en.n - i0);
-    if (n == 0) continue;
     if (en.dtype == TACO_DTYPE_F32)
-      s += en.vec ? squares16<float, true>(en.p, i0, n, en.wide) : squares16<float, false>(en.p, i0, n, false);
+      s += squares<float>(en, c - en.first);
     else if (en.dtype == TACO_DTYPE_BF16)
-      s += en.vec ? squares16<__nv_bfloat16, true>(en.p, i0, n, en.wide)
-                  : squares16<__nv_bfloat16, false>(en.p, i0, n, false);
+      s += squares<__nv_bfloat16>(en, c - en.first);
     else
-      s += en.vec ? squares16<__half, true>(en.p, i0, n, en.wide) : squares16<__half, false>(en.p, i0, n, false);
+      s += squares<__half>(en, c - en.first);
   }
   const double w = warp_sum64(static_cast<double>(s));
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = w;
@@ -85,7 +105,7 @@ __global__ void __launch_bounds__(kOptimThreads) grad_norm_kernel(const double* 
 
 cudaError_t launch_grad_squares(const GradEntry* entries, int count, uint32_t chunks, int sms, double* partial,
                                 int* ctas, cudaStream_t st) {
-  const uint32_t most = static_cast<uint32_t>(sms * 6 < kNormCtas ? sms * 6 : kNormCtas);
+  const uint32_t most = static_cast<uint32_t>(sms * kNormPerSm < kNormCtas ? sms * kNormPerSm : kNormCtas);
   const uint32_t grid = chunks < most ? chunks : most;
   *ctas = static_cast<int>(grid);
   const auto go = [&](auto cap) {

@@ -215,7 +215,8 @@ taco_status taco_grad_norm(const taco_grad_tensor* tensors, int64_t count, doubl
       if (t.n == 0) continue;
       entries[filled++] = GradEntry{t.data, t.n, chunks, static_cast<int16_t>(t.dtype), addr(t.data) % 16 == 0,
                                     addr(t.data) % 32 == 0};
-      chunks += static_cast<uint32_t>((t.n + kChunk - 1) / kChunk);
+      const int64_t chunk = kNormChunkBytes / elem(t.dtype);
+      chunks += static_cast<uint32_t>((t.n + chunk - 1) / chunk);
       --present;
     }
     int ctas = 0;

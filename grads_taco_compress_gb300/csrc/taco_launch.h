@@ -330,6 +330,7 @@ struct GradEntry {
   bool vec, wide;           // p on 16 bytes, on 32
 };
 constexpr int kNormFew = 128, kNormMany = 1300;
+constexpr int64_t kNormChunkBytes = 16384;
 constexpr int kNormCtas = 1024;   // most CTAs, and so partial sums, of a launch
 // Partial sums of squares of one launch to partial[0 .. the returned CTAs - 1].
 cudaError_t launch_grad_squares(const GradEntry* entries, int count, uint32_t chunks, int sms, double* partial,
