@@ -642,10 +642,7 @@ class Items {
     if (!fast_) throw std::bad_alloc();
   }
   Items(PyObject* o, const char* what, Py_ssize_t n) : Items(o, what) {
-    if (size() != n) {
-      Py_DECREF(fast_);
-      refuse(std::string(what) + " must have as many items as there are parameters");
-    }
+    if (size() != n) refuse(std::string(what) + " must have as many items as there are parameters");
   }
   Items(const Items&) = delete;
   Items& operator=(const Items&) = delete;

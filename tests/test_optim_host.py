@@ -192,3 +192,18 @@ def test_rounding_by_thresholds_keeps_the_mean():
         assert abs(q.mean() - x) < 4e-3 * O.step_at(np.array(x), "e4m3")
         assert set(np.unique(np.abs(q) / O.step_at(np.array(x), "e4m3"))) <= {np.floor(abs(x) / O.step_at(np.array(x), "e4m3")),
                                                                              np.ceil(abs(x) / O.step_at(np.array(x), "e4m3"))}
+
+
+@no_gpu_only
+def test_refusals_hold_no_reference_and_drop_none():
+    import sys
+
+    lists = [[fake(512)], [fake(512, at=5)], [state(at=6)], [fake(512, dtype=f32)]]
+    empty = [[] for _ in lists]
+    before = [sys.getrefcount(x) for x in lists + empty]
+    for _ in range(50):
+        for k in (1, 2, 3):
+            arg = ("params", "grads", "states", "masters")[k]
+            with pytest.raises(ValueError):
+                call(**{"params": lists[0], "grads": lists[1], "states": lists[2], arg: empty[k]})
+    assert [sys.getrefcount(x) for x in lists + empty] == before
