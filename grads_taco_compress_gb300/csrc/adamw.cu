@@ -148,7 +148,7 @@ constexpr int adamw_ctas() { return SMALL ? 4 : 2; }
 
 // What every chunk of a launch shares.
 struct StepFacts {
-  float gm, gv;        // factor (1 - b1); factor sqrt(1 - b2)
+  float factor;
   float rate;          // of m' over the denominator
   float root_c, lr;
   uint32_t weyl;       // of element 0 at this step
@@ -164,7 +164,7 @@ __device__ __forceinline__ void step16(const AdamwArgs& a, const AdamwEntry& en,
   const bool wide = en.wide;
   const float keep = 1.0f - f.lr * en.decay;
   P* const param = static_cast<P*>(en.param) + base + i0;
-  // b1 m and b2 v, or the root of the latter
+  // b1 m and the root of v in 8 bits, m and v in 32
   float g[16], x[16], m[16], v[16];
   const Row16<G> gr = load16<G, VEC>(static_cast<const G*>(en.grad) + base + i0, n, wide);
   if (en.master)
@@ -182,7 +182,7 @@ __device__ __forceinline__ void step16(const AdamwArgs& a, const AdamwEntry& en,
     const bool any = WHOLE || n > 0;
     const uint32_t sm = any ? *ms : kScaleOne, sv = any ? *vs : kScaleOne;
     decode16(cm, fp8_scale(sm) * a.b1, m);
-    decode16(cv, fp8_scale(sv) * a.root_b2, v);
+    decode16(cv, fp8_scale(sv), v);
     if (!WHOLE && (sm == kScaleNan || sv == kScaleNan)) {   // which must not reach elements that do not exist
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -197,15 +197,11 @@ __device__ __forceinline__ void step16(const AdamwArgs& a, const AdamwEntry& en,
   unpack<G>(gr, g);
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
-    const f2 gi{g[i], g[i + 1]}, h = mul2(gi, f2{f.gv, f.gv});
+    const f2 gi = mul2(f2{g[i], g[i + 1]}, f2{f.factor, f.factor}), gs = mul2(gi, f2{a.one_b2, a.one_b2});
     f2 mi{m[i], m[i + 1]}, vi{v[i], v[i + 1]}, xi{x[i], x[i + 1]};
-    if (SMALL) {
-      mi = fma2(gi, f2{f.gm, f.gm}, mi);
-      vi = fma2(vi, vi, mul2(h, h));
-    } else {
-      mi = fma2(mi, f2{a.b1, a.b1}, mul2(gi, f2{f.gm, f.gm}));
-      vi = fma2(vi, f2{a.b2, a.b2}, mul2(h, h));
-    }
+    mi = SMALL ? fma2(gi, f2{a.one_b1, a.one_b1}, mi) : fma2(mi, f2{a.b1, a.b1}, mul2(gi, f2{a.one_b1, a.one_b1}));
+    vi = SMALL ? mul2(vi, vi) : vi;   // of a root in 8 bits, exact
+    vi = fma2(gs, gi, mul2(vi, f2{a.b2, a.b2}));
     const f2 root{sqrt_approx(vi.x), sqrt_approx(vi.y)};
     const f2 den = fma2(root, f2{f.root_c, f.root_c}, f2{a.eps, a.eps});
     const f2 q = mul2(mi, f2{reciprocal(den.x), reciprocal(den.y)});
@@ -260,8 +256,7 @@ adamw_kernel(const __grid_constant__ AdamwTable<CAP> table) {
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const float t = static_cast<float>(step);
   StepFacts f;
-  f.gm = factor * a.one_b1;
-  f.gv = factor * a.root_one_b2;
+  f.factor = factor;
   f.rate = -lr / -expm1f(t * a.log_b1);
   f.root_c = rsqrtf(-expm1f(t * a.log_b2));
   f.lr = lr;

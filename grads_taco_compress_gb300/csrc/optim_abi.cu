@@ -130,8 +130,7 @@ taco_status taco_adamw(const taco_adamw_tensor* tensors, int64_t count, double l
   a.b1 = static_cast<float>(beta1);
   a.one_b1 = static_cast<float>(1.0 - beta1);
   a.b2 = static_cast<float>(beta2);
-  a.root_b2 = static_cast<float>(std::sqrt(beta2));
-  a.root_one_b2 = static_cast<float>(std::sqrt(1.0 - beta2));
+  a.one_b2 = static_cast<float>(1.0 - beta2);
   a.log_b1 = static_cast<float>(std::log(beta1));
   a.log_b2 = static_cast<float>(std::log(beta2));
   a.eps = eps32;

@@ -311,7 +311,7 @@ struct AdamwEntry {
 struct AdamwArgs {
   uint32_t chunks;
   bool last;                // of the step's launches: counts it
-  float b1, one_b1, b2, root_b2, root_one_b2, log_b1, log_b2, eps, lr;   // root_*: square roots
+  float b1, one_b1, b2, one_b2, log_b1, log_b2, eps, lr;
   const float* lr_dev;      // null: lr
   const float* factor;      // null: 1
   int32_t* counter;         // steps done, CTAs arrived
