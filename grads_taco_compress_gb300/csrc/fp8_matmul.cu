@@ -393,8 +393,12 @@ constexpr int kPart = kFp8Block / 4;
 struct LinearShared {
   static constexpr uint32_t bias = 0, kBias = 2 * kPart * 4;
   static constexpr uint32_t amax = kEpilogueWarps * kBias, kSlot = kEpilogueWarps * 32 * 4;
-  static constexpr uint32_t box = amax + 2 * kSlot, kBox = 32 * 16;   // a warp's, 32 rows of 16 bytes
-  static constexpr uint32_t bytes = box + kEpilogueWarps * kBox;
+  static constexpr uint32_t box = amax + 2 * kSlot;
+  // a warp's box, 32 rows of as many bytes as there is room for
+  template <int TN>
+  static constexpr int kBoxRow = TN == 128 ? 64 : 16;
+  template <int TN>
+  static constexpr uint32_t bytes = box + kEpilogueWarps * 32 * kBoxRow<TN>;
 };
 
 // Scale byte of the lane's block, from its values and those of the other three
@@ -462,50 +466,65 @@ __device__ __forceinline__ void store_row32(const float (&v)[kPart], T* p, int64
     }
   }
 }
-// Rows that start anywhere go through the warp's box, 16 bytes of each of its 32
-// rows at a time, so that consecutive lanes hold consecutive elements. p: element
-// (0, 0) of the warp's 32 x 32; rows, cols: how many of them exist.
-template <typename T>
+// Rows that start anywhere go through the warp's box, BYTES of each of its 32 rows
+// at a time, so that consecutive lanes hold consecutive elements. Pieces of 16
+// bytes are permuted by the row, for the banks. p: element (0, 0) of the warp's 32 x
+// 32; rows, cols: how many of them exist.
+template <typename T, int BYTES>
 struct Box {
-  static constexpr int kPer = 16 / static_cast<int>(sizeof(T)), kRows = 32 / kPer;   // elements; rows an access
+  static constexpr int kEs = static_cast<int>(sizeof(T)), kPieces = BYTES / 16;
+  static constexpr int kPer = BYTES / kEs, kRows = 32 / kPer;   // elements of a row; rows an access
+  static __device__ __forceinline__ uint32_t piece(uint32_t box, int row, int i) {
+    return box + row * BYTES + 16 * (i ^ ((row >> 1) & (kPieces - 1)));
+  }
+  static __device__ __forceinline__ uint32_t element(uint32_t box, int row, int e) {
+    return piece(box, row, (e * kEs) >> 4) + ((e * kEs) & 15);
+  }
 };
-template <typename T>
+template <int BYTES, typename T>
 __device__ __forceinline__ void add_rows_anywhere(float (&v)[kPart], const T* p, int64_t ld, int rows, int cols,
                                                   uint32_t box) {
-  using B = Box<T>;
+  using B = Box<T, BYTES>;
   const int lane = threadIdx.x & 31, e = lane % B::kPer, r0 = lane / B::kPer;
-  const uint32_t mine = box + lane * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
   for (int q = 0; q < kPart; q += B::kPer) {
-    T in[B::kPer];
 #pragma unroll
-    for (int k = 0; k < B::kPer; ++k) {
-      const int r = r0 + k * B::kRows;
-      in[k] = r < rows && q + e < cols ? p[r * ld + q + e] : from_f32<T>(0.0f);
+    for (int k0 = 0; k0 < B::kPer; k0 += 8) {   // 8 loads in flight
+      constexpr int kLoads = B::kPer < 8 ? B::kPer : 8;
+      T in[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int r = r0 + (k0 + k) * B::kRows;
+        in[k] = r < rows && q + e < cols ? p[r * ld + q + e] : from_f32<T>(0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) store_staged<T>(B::element(box, r0 + (k0 + k) * B::kRows, e), in[k]);
     }
-#pragma unroll
-    for (int k = 0; k < B::kPer; ++k) store_staged<T>(mine + 32 * k * static_cast<uint32_t>(sizeof(T)), in[k]);
     __syncwarp();
-    const uint4 w = lds128(box + 16 * lane);
 #pragma unroll
-    for (int i = 0; i < B::kPer; ++i) v[q + i] += to_f32(reinterpret_cast<const T*>(&w)[i]);
+    for (int i = 0; i < B::kPieces; ++i) {
+      const uint4 w = lds128(B::piece(box, lane, i));
+#pragma unroll
+      for (int j = 0; j < 16 / B::kEs; ++j)
+        v[q + i * (16 / B::kEs) + j] += to_f32(reinterpret_cast<const T*>(&w)[j]);
+    }
     __syncwarp();
   }
 }
-template <typename T>
+template <int BYTES, typename T>
 __device__ __forceinline__ void store_rows_anywhere(const float (&v)[kPart], T* p, int64_t ld, int rows, int cols,
                                                     uint32_t box) {
-  using B = Box<T>;
+  using B = Box<T, BYTES>;
   const int lane = threadIdx.x & 31, e = lane % B::kPer, r0 = lane / B::kPer;
-  const uint32_t mine = box + lane * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
   for (int q = 0; q < kPart; q += B::kPer) {
-    sts128(box + 16 * lane, pack16<T>(&v[q]));
+#pragma unroll
+    for (int i = 0; i < B::kPieces; ++i) sts128(B::piece(box, lane, i), pack16<T>(&v[q + i * (16 / B::kEs)]));
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < B::kPer; ++k) {
       const int r = r0 + k * B::kRows;
-      const T out = load_staged<T>(mine + 32 * k * static_cast<uint32_t>(sizeof(T)));
+      const T out = load_staged<T>(B::element(box, r, e));
       if (r < rows && q + e < cols) p[r * ld + q + e] = out;
     }
     __syncwarp();
@@ -519,14 +538,15 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
                                                 int64_t pairs, int kb, uint32_t base, uint32_t tmem, uint32_t rank,
                                                 volatile uint32_t* abort_flag) {
   using S = Pair<TN>;
-  static_assert(LinearShared::bytes <= 4 * S::kBoxes * 4096, "in the place of the staging");
+  static_assert(LinearShared::bytes<TN> <= 4 * S::kBoxes * 4096, "in the place of the staging");
   constexpr bool kSeg = std::is_same<T, float>::value;
   constexpr int kBlocks = TN / kFp8Block;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, quad = warp & 3, part = (warp - 4) >> 2;
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t biases = base + S::staging + LinearShared::bias + (warp - 4) * LinearShared::kBias;
   const uint32_t slots = base + S::staging + LinearShared::amax;
-  const uint32_t box = base + S::staging + LinearShared::box + (warp - 4) * LinearShared::kBox;
+  constexpr int kBoxRow = LinearShared::kBoxRow<TN>;
+  const uint32_t box = base + S::staging + LinearShared::box + (warp - 4) * (32 * kBoxRow);
   const uint32_t tempty0 = in_cta(base + S::tempty, 0);
   uint32_t u = 0, turn = 0;
   for (int64_t t = pair; t < tiles; t += pairs) {
@@ -616,13 +636,13 @@ __device__ __forceinline__ void linear_epilogue(const Args& a, const TileMap& tm
           if (a.vec_add)
             add_row32(v, p + m * a.ldadd, left, a.wide_add);
           else
-            add_rows_anywhere(v, p + (m - lane) * a.ldadd, a.ldadd, rows, cols, box);
+            add_rows_anywhere<kBoxRow>(v, p + (m - lane) * a.ldadd, a.ldadd, rows, cols, box);
         }
         T* const p = static_cast<T*>(a.out) + n;
         if (a.vec_out)
           store_row32(v, p + m * a.ldo, left, a.wide_out);
         else
-          store_rows_anywhere(v, p + (m - lane) * a.ldo, a.ldo, rows, cols, box);
+          store_rows_anywhere<kBoxRow>(v, p + (m - lane) * a.ldo, a.ldo, rows, cols, box);
       }
     }
     if constexpr (!kSeg) ++u;
