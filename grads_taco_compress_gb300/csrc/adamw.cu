@@ -20,6 +20,10 @@
 // in some steps comes back in others, with less variance than random bits and
 // no state of its own. A root that is not zero is not rounded to zero, which
 // would make m' / (0 + eps) of an element much smaller than its block's largest.
+//
+// Measured, 134M bf16 parameters with f32 gradients (a plain copy: 6.78 TB/s): 8-bit
+// states 252 us, 6.4 TB/s, bound by memory at 56% of the issue slots; 32-bit states
+// with masters 627-637 us, 6.3 TB/s. 96 vectors of a few thousand elements 5 us.
 
 #include "optim.cuh"
 
@@ -29,9 +33,9 @@ namespace {
 
 // 2^32 times the inverse of the plastic number and of the golden ratio. Of eight
 // factors of t tried on constant, decaying and random gradients the golden ratio
-// kept the second moment nearest to an exact one's: 2% off in the mean after 300
-// to 1500 steps (random bits: 2%, and twice the spread), 10% below where it has
-// decayed to a fifth.
+// kept the second moment nearest to an exact one's: up to 3% off in the mean after
+// 300 to 1500 steps (random bits: 3% to 6%, and up to 3 times the spread), 10% below
+// where it has decayed to a fifth.
 constexpr uint32_t kWeylI = 0xC13FA9A9u, kWeylT = 0x9E3779B1u;
 
 template <int CAP>
@@ -41,11 +45,6 @@ struct AdamwTable {
   AdamwEntry t[CAP];
 };
 
-__device__ __forceinline__ float reciprocal(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float sqrt_approx(float v) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));

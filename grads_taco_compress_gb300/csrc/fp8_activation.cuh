@@ -21,11 +21,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float reciprocal(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ f2 both(float v) { return f2{v, v}; }
 __device__ __forceinline__ f2 ex2_2(f2 x) { return f2{ex2(x.x), ex2(x.y)}; }
 // 1 / (1 + 2^t)

@@ -558,8 +558,8 @@ PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
     }
     void* stream = on.handle();
     const taco_status st = call([&] {
-      return taco_linear_fp8(&ad, &bd, bp, bp ? dtype_of(bias.scalar_type()) : 0, act, res.p, res.ld, o.p, o.ld, o.dtype,
-                             y ? &yd : nullptr, kept ? &kd : nullptr, stream);
+      return taco_linear_fp8(&ad, &bd, bp, bp ? dtype_of(bias.scalar_type()) : 0, act, res.p, res.ld, o.p, o.ld,
+                             o.dtype, y ? &yd : nullptr, kept ? &kd : nullptr, stream);
     });
     if (st != TACO_OK) return PyLong_FromLong(st);
     return tuple(&PyTuple_Type, {y ? object(y) : object(out), object(kept)});

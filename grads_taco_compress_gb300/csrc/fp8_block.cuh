@@ -407,6 +407,13 @@ struct Divider {
   __device__ __forceinline__ uint64_t quotient(uint64_t n) const { return d == 1 ? n : __umul64hi(n, magic); }
 };
 
+// 1 / x to fp32's last bit or two; 0 of what is beyond 2^126.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Sum over a warp, the same in every lane.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll

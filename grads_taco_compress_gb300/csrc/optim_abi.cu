@@ -97,7 +97,8 @@ taco_status taco_adamw(const taco_adamw_tensor* tensors, int64_t count, double l
   if ((count > 0 && !tensors) || !counter) return TACO_ERR_NULL;
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return TACO_ERR_ARG;
   const float eps32 = static_cast<float>(eps);
-  if (!(eps32 >= std::numeric_limits<float>::min()) || std::isinf(eps32) || (!lr_dev && !std::isfinite(static_cast<float>(lr)))) return TACO_ERR_ARG;
+  if (!(eps32 >= std::numeric_limits<float>::min()) || std::isinf(eps32)) return TACO_ERR_ARG;
+  if (!lr_dev && !std::isfinite(static_cast<float>(lr))) return TACO_ERR_ARG;
   if (addr(counter) % 4 || addr(lr_dev) % 4 || addr(grad_scale) % 4) return TACO_ERR_ALIGN;
   int64_t total = 0, members[kKinds] = {};
   for (int64_t i = 0; i < count; ++i) {

@@ -42,7 +42,8 @@ FP8_OUT = dict(out=None, y=fp8(6, 4, 300), dtype=77)
 @pytest.mark.parametrize("kw,status", [
     (dict(a=None), NULL), (dict(b=None), NULL), (dict(act=-1), ARG), (dict(act=5), ARG), (dict(bd=3), ARG),
     (dict(dtype=4), ARG), (dict(out=None), NULL), (dict(y=fp8(6, 4, 300)), ARG),
-    (dict(FP8_OUT, res=7 * A, ldr=300), ARG), (dict(b=fp8(2, 300, 384)), SHAPE), (dict(a=fp8(1, 4, 256, tile=3)), BLOCK),
+    (dict(FP8_OUT, res=7 * A, ldr=300), ARG), (dict(b=fp8(2, 300, 384)), SHAPE),
+    (dict(a=fp8(1, 4, 256, tile=3)), BLOCK),
     (dict(bias=3 * A + 2), ALIGN), (dict(res=7 * A, ldr=299), SHAPE), (dict(res=7 * A + 1, ldr=300), ALIGN),
     (dict(ldo=200), SHAPE), (dict(out=4 * A + 1), ALIGN), (dict(ck=fp8(5, 5, 300)), SHAPE),
     (dict(ck=fp8(5, 4, 300, tile=128)), BLOCK), (dict(FP8_OUT, y=fp8(6, 4, 300, tile=128)), BLOCK),
@@ -72,7 +73,8 @@ def _backward(lib, **kw):
     (dict(rows=None, cols=None, db=None), NULL), (dict(rows=fp8(3, 200, 300, tile=128)), BLOCK),
     (dict(rows=fp8(3, 199, 300)), SHAPE), (dict(cols=fp8(4, 200, 300)), SHAPE), (dict(db=5 * A + 2), ALIGN),
     (dict(ws=None), WS), (dict(wsb=2399), WS), (dict(ws=6 * A + 8), ALIGN), (dict(rows=fp8(1, 200, 300)), ARG),
-    (dict(cols=fp8(2, 300, 200)), ARG), (dict(cols=fp8(3, 300, 200)), ARG), (dict(db=A + 512), ARG), (dict(ws=5 * A), ARG),
+    (dict(cols=fp8(2, 300, 200)), ARG), (dict(cols=fp8(3, 300, 200)), ARG), (dict(db=A + 512), ARG),
+    (dict(ws=5 * A), ARG),
     (dict(ws=4 * A), ARG),
 ])
 def test_backward_rejects(lib, kw, status):  # noqa: F811
@@ -94,11 +96,13 @@ def linear(**kw):
 
 @no_gpu_only
 @pytest.mark.parametrize("kw,text", [
-    (dict(x=fake(4, 256)), "x must be an Fp8Tensor"), (dict(w=None), "w must be"), (dict(activation="tanh"), "activation"),
+    (dict(x=fake(4, 256)), "x must be an Fp8Tensor"), (dict(w=None), "w must be"),
+    (dict(activation="tanh"), "activation"),
     (dict(activation=1), "activation"), (dict(bias=fake(63)), "bias"), (dict(bias=fake(64, dtype=torch.int32)), "bias"),
     (dict(bias=fake(64, device=1)), "one device"), (dict(out=fake(4, 63)), "rows of x and of w"),
     (dict(out=fake(4, 64, dtype=torch.int8)), "out"), (dict(residual=fake(4, 63)), "residual"),
-    (dict(residual=fake(4, 64, dtype=torch.float32)), "another type"), (dict(residual=fake(4, 64, device=1)), "one device"),
+    (dict(residual=fake(4, 64, dtype=torch.float32)), "another type"),
+    (dict(residual=fake(4, 64, device=1)), "one device"),
     (dict(out=fp8_fake(4, 64, at=9), residual=fake(4, 64)), "16 or 32"),
     (dict(out=None, out_dtype=F8, residual=fake(4, 64)), "16 or 32"), (dict(out=None, out_dtype="f8"), "out_dtype"),
     (dict(out=None, out_dtype=torch.int32), "out_dtype"), (dict(out=None, out_dtype=torch.float8_e5m2), "out_dtype"),
@@ -123,7 +127,8 @@ def backward(**kw):
 @pytest.mark.parametrize("kw,text", [
     (dict(dy=fake(200)), "dy"), (dict(dy=fake(200, 0)), "a column"), (dict(checkpoint=None), "takes the checkpoint"),
     (dict(activation=None), "where there is an activation"), (dict(activation="Gelu"), "activation"),
-    (dict(rows=False, cols=False, bias=False), "nothing"), (dict(rows=fake(3, 2)), "rows"), (dict(out=fake(200, 64)), "out"),
+    (dict(rows=False, cols=False, bias=False), "nothing"), (dict(rows=fake(3, 2)), "rows"),
+    (dict(out=fake(200, 64)), "out"),
     (dict(out_t=fp8_fake(64, 200, device=1)), "one device"), (dict(db=fake(64)), "db"),
     (dict(db=fake(63, dtype=torch.float32)), "db"), (dict(workspace=torch.zeros(9)), "workspace"),
     (dict(workspace=fake(512, dtype=torch.uint8, device=1)), "one device"),

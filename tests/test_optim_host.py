@@ -64,7 +64,8 @@ def test_step_rejects(lib, kw, status):  # noqa: F811
     (dict(weight_decay=float("nan")), ARG), (dict(weight_decay=float("inf")), ARG), (dict(n=-1), SHAPE),
     (dict(n=(1 << 40) + 1), SHAPE), (dict(param=None), NULL), (dict(grad=None), NULL), (dict(m=None), NULL),
     (dict(v=None), NULL), (dict(m_scales=5 * A), NULL), (dict(v_scales=5 * A), NULL), (dict(param=A + 1), ALIGN),
-    (dict(grad=2 * A + 2), ALIGN), (dict(master=5 * A + 2), ALIGN), (dict(m=3 * A + 2), ALIGN), (dict(v=4 * A + 1), ALIGN),
+    (dict(grad=2 * A + 2), ALIGN), (dict(master=5 * A + 2), ALIGN), (dict(m=3 * A + 2), ALIGN),
+    (dict(v=4 * A + 1), ALIGN),
     (dict(m=3 * A + 8, m_scales=5 * A, v_scales=6 * A), ALIGN), (dict(grad=A), ARG), (dict(grad=A + 1996), ARG),
     (dict(m=4 * A - 3996), ARG), (dict(master=A), ARG), (dict(m_scales=3 * A + 992, v_scales=6 * A), ARG),
     (dict(m_scales=5 * A, v_scales=5 * A + 7), ARG),
@@ -143,12 +144,14 @@ def every_other(n):
     (dict(params=[fake(512, dtype=torch.float64)]), "bf16"), (dict(params=[every_other(512)]), "contiguous"),
     (dict(grads=[]), "as many"), (dict(grads=[fake(256)]), r"grads\[0\].*shape"), (dict(grads=[fake(2, 256)]), "shape"),
     (dict(grads=[fake(512, dtype=torch.float16)]), "type"), (dict(grads=[fake(512, device=1)]), "one device"),
-    (dict(states=[]), "as many"), (dict(states=[None]), "AdamState"), (dict(states=[state(256)]), r"states\[0\]\.m.*512"),
+    (dict(states=[]), "as many"), (dict(states=[None]), "AdamState"),
+    (dict(states=[state(256)]), r"states\[0\]\.m.*512"),
     (dict(states=[state(256, 8)]), "512"), (dict(states=[(state().m, state(bits=8).v)]), "both"),
     (dict(states=[state(device=1)]), "one device"), (dict(states=[state(bits=8, device=1)]), "one device"),
     (dict(counter=fake(2)), "int32"), (dict(counter=fake(3, dtype=torch.int32)), "int32"), (dict(counter=1), "tensor"),
     (dict(counter=fake(2, dtype=torch.int32, device=1)), "one device"), (dict(lr="x"), "lr"), (dict(lr=None), "lr"),
-    (dict(lr=fake(2, dtype=f32)), "lr"), (dict(lr=fake(1)), "lr"), (dict(betas=0.9), "betas"), (dict(betas=(1, 2, 3)), "betas"),
+    (dict(lr=fake(2, dtype=f32)), "lr"), (dict(lr=fake(1)), "lr"), (dict(betas=0.9), "betas"),
+    (dict(betas=(1, 2, 3)), "betas"),
     (dict(betas=("a", 0.9)), "betas"), (dict(eps=None), "eps"), (dict(weight_decay=[0.1, 0.1]), "as many"),
     (dict(weight_decay=["x"]), "weight_decay"), (dict(weight_decay=None), "weight_decay"),
     (dict(grad_scale=0.5), "grad_scale"), (dict(grad_scale=fake(2, dtype=f32)), "grad_scale"),
@@ -165,7 +168,8 @@ def test_binding_refuses(kw, text):
     (dict(grads=[]), "a tensor"), (dict(grads=fake(3)), "list"), (dict(grads=[fake(3), 1]), "tensor"),
     (dict(grads=[torch.zeros(3)]), "CUDA"), (dict(grads=[fake(3, dtype=torch.int32)]), "bf16"),
     (dict(grads=[fake(3), fake(3, device=1)]), "one device"), (dict(max_norm="x"), "max_norm"),
-    (dict(out=fake(2)), "out"), (dict(out=fake(3, dtype=f32)), "out"), (dict(out=fake(2, dtype=f32, device=1)), "one device"),
+    (dict(out=fake(2)), "out"), (dict(out=fake(3, dtype=f32)), "out"),
+    (dict(out=fake(2, dtype=f32, device=1)), "one device"),
     (dict(workspace=every_other(8192)), "workspace"), (dict(workspace=torch.zeros(9)), "workspace"),
 ])
 def test_norm_binding_refuses(kw, text):
