@@ -114,6 +114,18 @@ cudaError_t device_facts(const DeviceFacts** out) {
   return g_err[dev];
 }
 
+// The same for the layer's products, whose kernels a program without them need
+// not load.
+std::once_flag g_linear_once[kMaxDevices];
+cudaError_t g_linear_err[kMaxDevices];
+cudaError_t linear_facts(const DeviceFacts** out) {
+  const cudaError_t e = device_facts(out);
+  if (e != cudaSuccess) return e;
+  const int64_t dev = *out - g_device;
+  std::call_once(g_linear_once[dev], [dev]() { g_linear_err[dev] = prepare_linear(); });
+  return g_linear_err[dev];
+}
+
 inline taco_status done(cudaError_t e) { return e == cudaSuccess ? TACO_OK : TACO_ERR_CUDA; }
 
 #define TACO_TRY(expr)                        \
@@ -481,7 +493,7 @@ taco_status taco_linear_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
     l.wide_k = wide_codes(*checkpoint);
   }
   const DeviceFacts* dev = nullptr;
-  if (device_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
+  if (linear_facts(&dev) != cudaSuccess) return TACO_ERR_CUDA;
   return done(launch_linear(l, dtype, dev->sms, dev->clusters, static_cast<cudaStream_t>(stream)));
 }
 

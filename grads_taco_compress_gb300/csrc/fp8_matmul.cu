@@ -1348,33 +1348,32 @@ cudaLaunchConfig_t few_config(int splits, unsigned gx, unsigned gy, size_t smem,
   return cfg;
 }
 
-cudaError_t prepare_matmul(int* clusters) {
+// The shared memory of every form with these arguments and output type.
+template <typename T, typename Args>
+cudaError_t prepare_forms() {
   cudaError_t e = cudaSuccess;
   const auto set = [&](auto k, uint32_t bytes) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(bytes));
   };
-  const auto all = [&](auto t, auto* args) {
-    using T = decltype(t);
-    using Args = std::remove_pointer_t<decltype(args)>;
-    if constexpr (!std::is_same<T, float>::value) set(matmul_pair_kernel<T, 256, Args>, Pair<256>::bytes);
-    set(matmul_pair_kernel<T, 128, Args>, Pair<128>::bytes);
-    set(matmul_few_kernel<T, 16, Args>, Few<16>::bytes);
-    set(matmul_few_kernel<T, 32, Args>, Few<32>::bytes);
-    set(matmul_few_kernel<T, 64, Args>, Few<64>::bytes);
-    set(matmul_few_kernel<T, 128, Args>, Few<128>::bytes);
-  };
-  MatmulArgs* const plain = nullptr;
-  LinearArgs* const layer = nullptr;
-  LinearFp8Args* const layer_fp8 = nullptr;
-  all(__nv_bfloat16{}, plain);
-  all(__half{}, plain);
-  all(float{}, plain);
-  all(__nv_bfloat16{}, layer);
-  all(__half{}, layer);
-  all(float{}, layer);
-  all(__nv_bfloat16{}, layer_fp8);
+  if constexpr (!std::is_same<T, float>::value) set(matmul_pair_kernel<T, 256, Args>, Pair<256>::bytes);
+  set(matmul_pair_kernel<T, 128, Args>, Pair<128>::bytes);
+  set(matmul_few_kernel<T, 16, Args>, Few<16>::bytes);
+  set(matmul_few_kernel<T, 32, Args>, Few<32>::bytes);
+  set(matmul_few_kernel<T, 64, Args>, Few<64>::bytes);
+  set(matmul_few_kernel<T, 128, Args>, Few<128>::bytes);
+  return e;
+}
+template <typename Args>
+cudaError_t prepare_types() {
+  cudaError_t e = prepare_forms<__nv_bfloat16, Args>();
+  if (e == cudaSuccess) e = prepare_forms<__half, Args>();
+  return e != cudaSuccess ? e : prepare_forms<float, Args>();
+}
+
+cudaError_t prepare_matmul(int* clusters) {
+  cudaError_t e = prepare_types<MatmulArgs>();
   // one CTA per SM in every form: the count is the same for all of them
   for (int splits = 1; splits <= kMaxSplits && e == cudaSuccess; ++splits) {
     cudaLaunchAttribute attr[2];
@@ -1382,6 +1381,10 @@ cudaError_t prepare_matmul(int* clusters) {
     e = cudaOccupancyMaxActiveClusters(&clusters[splits], matmul_few_kernel<__nv_bfloat16, 128, MatmulArgs>, &cfg);
   }
   return e;
+}
+cudaError_t prepare_linear() {
+  const cudaError_t e = prepare_types<LinearArgs>();
+  return e != cudaSuccess ? e : prepare_forms<__nv_bfloat16, LinearFp8Args>();
 }
 
 // One 256 x TN tile per CTA pair, at most one pair per two SMs.

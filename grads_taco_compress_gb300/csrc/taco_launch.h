@@ -288,6 +288,7 @@ cudaError_t launch_quantize(const QuantizeArgs& a, int dtype, int vec, cudaStrea
 // Fills clusters[1 .. 8]: how many clusters of that many CTAs run at once.
 cudaError_t prepare_matmul(int* clusters);
 cudaError_t launch_matmul(const MatmulArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
+cudaError_t prepare_linear();
 cudaError_t launch_linear(const LinearArgs& a, int dtype, int sms, const int* clusters, cudaStream_t st);
 cudaError_t matmul_fault(unsigned int* bits, bool clear);
 // db: the columns' sums (null: none), through `workspace` where there are more than 128 rows.

@@ -24,8 +24,9 @@ products have biases, and their epilogues do what lies between them:
 Weights are bf16 masters, quantised with one scale per 128 x 128 tile by
 ``refresh`` (after every update); weight gradients are running f32 sums. As in
 ``allreduce``, every step is a libtaco call, but for the addition of the norm
-weight's and the biases' gradients to their running sums. ``step`` updates the
-masters by an ``optim.AdamW`` over ``parameters()`` and quantises them again.
+weight's and the biases' gradients to their running sums, which ``step`` zeroes.
+``step`` updates the masters by an ``optim.AdamW`` over ``parameters()`` and
+quantises them again.
 
 Several forward passes may be open at a time (micro-batches)::
 
