@@ -37,8 +37,8 @@
 // MB would take 2.5, and 5.5 us where they are in L2 from the call before; 1 x
 // 16384 x 4096 13.6 us, 4.9 TB/s.
 // A layer of 8192 x 16384 x 4096 with bias, tanh GELU, FP8 output and checkpoint
-// 317 us, 3.46 PFLOP/s, tensor pipe 84% (the product alone 297), and 380 us in a long
-// loop (363); 8192 x 16384 x 1024 161 us, bound by the epilogue (95).
+// 311-320 us, 3.5 PFLOP/s, tensor pipe 84% (the product alone 297-306), and 382 us in
+// a long loop (363); 8192 x 16384 x 1024 155 us, bound by the epilogue (95).
 
 #include "fp8_activation.cuh"
 #include "tcgen05.cuh"
@@ -392,8 +392,8 @@ __device__ __forceinline__ void store_block4(const float (&v)[4], int64_t left, 
 // of them, and the largest magnitude of a block is four lanes' to exchange,
 // through shared memory and a barrier of the four warps. Rows go out by whole
 // 32-byte sectors of a lane. 8192 x 16384 x 1024 with tanh GELU, FP8 output and
-// checkpoint: 161 us; 8 warps of 64 columns 176; 16 warps of 64 columns 150, but
-// they spill, and at K = 4096 take 327 us for 317.
+// checkpoint (before the stores below had their hint): 161 us; 8 warps of 64 columns
+// 176; 16 warps of 64 columns 150, but they spill, and at K = 4096 take 327 for 317.
 constexpr int kPart = kFp8Block / 4;
 // Shared memory of the epilogue in the place of the output's staging: each
 // warp's bias for the two blocks of a tile, and two slots of largest magnitudes.
@@ -421,6 +421,22 @@ __device__ __forceinline__ uint32_t block_scale(const float (&v)[kPart], uint32_
   const uint4 all = lds128(at);
   return fp8_scale_byte(max(max(all.x, all.y), max(all.z, all.w)));
 }
+// Eight words of a row, 32 bytes that no other lane of the warp shares a line with:
+// kept out of L1, where 32 of them at a time displaced each other (8192 x 16384 x
+// 1024 without an activation, FP8 output and checkpoint: 138 us, 121 with this).
+__device__ __forceinline__ void store_sector(void* p, bool wide, const uint32_t* w) {
+  if (wide) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                 :: "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.L1::no_allocate.v4.b32 [%4], {%0,%1,%2,%3};"
+                   :: "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3]),
+                      "l"(static_cast<char*>(p) + 16 * i) : "memory");
+  }
+}
 // 32 codes of a row of which `left` exist.
 __device__ __forceinline__ void store_codes32(const float (&v)[kPart], uint32_t b, uint8_t* p, int64_t left,
                                               bool wide) {
@@ -433,8 +449,10 @@ __device__ __forceinline__ void store_codes32(const float (&v)[kPart], uint32_t 
     for (int i = 0; i < 16; ++i) t[i] = v[16 * h + i];
     c[h] = codes16(t, inv);
   }
-  if (left >= kPart) {
-    store_words8(p, wide, reinterpret_cast<const uint32_t*>(c));
+  if (left >= kPart && wide) {
+    store_sector(p, true, reinterpret_cast<const uint32_t*>(c));
+  } else if (left >= kPart) {
+    store_sector(p, false, reinterpret_cast<const uint32_t*>(c));
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) store_codes16(p + 16 * h, clamp16(left - 16 * h), c[h]);
@@ -466,7 +484,7 @@ __device__ __forceinline__ void store_row32(const float (&v)[kPart], T* p, int64
   for (int q = 0; q < kPart; q += kPer) {
     if (left >= q + kPer) {
       uint4 w[2] = {pack16<T>(&v[q]), pack16<T>(&v[q + kPer / 2])};
-      store_words8(p + q, wide, reinterpret_cast<const uint32_t*>(w));
+      store_sector(p + q, wide, reinterpret_cast<const uint32_t*>(w));
     } else {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
