@@ -12,9 +12,9 @@
 // they leave as whole 128-byte rows. Tiles write their column sums; a second kernel
 // adds them in the order of the rows.
 //
-// Measured, 8192 x 16384 bf16 (a plain copy: 6.78 TB/s): tanh GELU 156 us, 4.3 TB/s,
-// 62% of the issue slots at 27 instructions an element; without an activation 114
-// us, 4.7 TB/s; f32 188 us, 5.0 TB/s.
+// Measured, 8192 x 16384 bf16 (a plain copy: 6.78 TB/s): tanh GELU 154-156 us, 4.4 TB/s,
+// 62% of the issue slots at 27 instructions an element; without an activation 113
+// us, 4.8 TB/s; f32 188 us, 5.0 TB/s.
 
 #include "fp8_activation.cuh"
 
@@ -89,6 +89,14 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int n, uint2 c) {
     for (int i = 0; i < kCols; ++i)
       if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
   }
+}
+// Codes that leave for good, kept out of L1 (1% of the kernel's time).
+__device__ __forceinline__ void store_past_l1(uint8_t* p, uint2 c) {
+  asm volatile("st.global.L1::no_allocate.v2.b32 [%2], {%0,%1};" :: "r"(c.x), "r"(c.y), "l"(p) : "memory");
+}
+__device__ __forceinline__ void store_past_l1(uint8_t* p, uint4 c) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%4], {%0,%1,%2,%3};"
+               :: "r"(c.x), "r"(c.y), "r"(c.z), "r"(c.w), "l"(p) : "memory");
 }
 __device__ __forceinline__ uint32_t codes4(f2 a, f2 b, float inv) {
   const f2 x = mul2(a, both(inv)), y = mul2(b, both(inv));
@@ -186,7 +194,7 @@ __device__ __forceinline__ void backward_tile(const LinearBackwardArgs& a, int64
       const uint2 c = make_uint2(codes4(f2{d[i][0], d[i][1]}, f2{d[i][2], d[i][3]}, f),
                                  codes4(f2{d[i][4], d[i][5]}, f2{d[i][6], d[i][7]}, f));
       if (FULL)
-        *reinterpret_cast<uint2*>(q + i * a.ldc) = c;
+        store_past_l1(q + i * a.ldc, c);
       else
         store_codes8(q + i * a.ldc, i < rows ? n : 0, c);
     }
@@ -258,14 +266,17 @@ __device__ __forceinline__ void backward_tile(const LinearBackwardArgs& a, int64
   __syncthreads();
   // 8 lanes write the 128 codes of a column, 16 each
   const int lane8 = threadIdx.x & 7;
-  const int left = FULL ? 16 : clamp16(a.M - r0 - 16 * lane8);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int c = (threadIdx.x >> 3) + 64 * i;
     const int at = word_of_tile(c, 4 * lane8);   // two words, the other two at ^ 2
     const uint2 lo = *reinterpret_cast<const uint2*>(&words[at]), hi = *reinterpret_cast<const uint2*>(&words[at ^ 2]);
     const uint4 w = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    if (FULL || c0 + c < a.N) store_codes16(a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8, left, w);
+    uint8_t* const to = a.t_codes + (c0 + c) * a.t_ldc + r0 + 16 * lane8;
+    if (FULL)
+      store_past_l1(to, w);
+    else if (c0 + c < a.N)
+      store_codes16(to, clamp16(a.M - r0 - 16 * lane8), w);
   }
 }
 
