@@ -37,7 +37,7 @@
 // MB would take 2.5, and 5.5 us where they are in L2 from the call before; 1 x
 // 16384 x 4096 13.6 us, 4.9 TB/s.
 // A layer of 8192 x 16384 x 4096 with bias, tanh GELU, FP8 output and checkpoint
-// 311-320 us, 3.5 PFLOP/s, tensor pipe 84% (the product alone 297-306), and 382 us in
+// 311-320 us, 3.5 PFLOP/s, tensor pipe 84% (the product alone 297-306), and 373-382 us in
 // a long loop (363); 8192 x 16384 x 1024 155 us, bound by the epilogue (95).
 
 #include "fp8_activation.cuh"
