@@ -22,7 +22,7 @@
 // would make m' / (0 + eps) of an element much smaller than its block's largest.
 //
 // Measured, 134M bf16 parameters with f32 gradients (a plain copy: 6.78 TB/s): 8-bit
-// states 252 us, 6.4 TB/s, bound by memory at 56% of the issue slots; 32-bit states
+// states 255 us, 6.3 TB/s, bound by memory and issue slots; 32-bit states
 // with masters 627-637 us, 6.3 TB/s. 96 vectors of a few thousand elements 5 us.
 
 #include "optim.cuh"
@@ -45,9 +45,12 @@ struct AdamwTable {
   AdamwEntry t[CAP];
 };
 
+// Off by its last bit at most, of subnormal numbers too: a root that they lost would
+// leave eps alone in the denominator (134M parameters, 8-bit states, f32 and bf16
+// gradients: 255 and 242 us; 252 and 232 with a root that flushes them).
 __device__ __forceinline__ float sqrt_approx(float v) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -199,7 +202,7 @@ __device__ __forceinline__ void step16(const AdamwArgs& a, const AdamwEntry& en,
     const f2 gi = mul2(f2{g[i], g[i + 1]}, f2{f.factor, f.factor}), gs = mul2(gi, f2{a.one_b2, a.one_b2});
     f2 mi{m[i], m[i + 1]}, vi{v[i], v[i + 1]}, xi{x[i], x[i + 1]};
     mi = SMALL ? fma2(gi, f2{a.one_b1, a.one_b1}, mi) : fma2(mi, f2{a.b1, a.b1}, mul2(gi, f2{a.one_b1, a.one_b1}));
-    vi = SMALL ? mul2(vi, vi) : vi;   // of a root in 8 bits, exact
+    vi = SMALL ? mul2(vi, vi) : vi;   // of a root in 8 bits, exact but where it is subnormal
     vi = fma2(gs, gi, mul2(vi, f2{a.b2, a.b2}));
     const f2 root{sqrt_approx(vi.x), sqrt_approx(vi.y)};
     const f2 den = fma2(root, f2{f.root_c, f.root_c}, f2{a.eps, a.eps});

@@ -553,8 +553,11 @@ typedef struct taco_adamw_tensor {
  * far below s are kept on average (a 16-bit parameter that this takes beyond its
  * type's largest value becomes infinite). The root of a second moment that is not zero
  * gets no zero code. A block with an infinity or a NaN becomes NaN.
- * 0 <= beta1, beta2 < 1; eps at least 2^-126 (the smallest normal f32). Calls on the same tensors or counter must be
- * in order on one stream. */
+ * v is an f32 number with either form of the states: what lies below 2^-149 is zero,
+ * and what lies below 2^-126 a multiple of that. Where (1 - beta2) g^2 is so small,
+ * an eps that is not well above |g| is all that the quotient has to go by.
+ * 0 <= beta1, beta2 < 1; eps at least 2^-126 (the smallest normal f32). Calls on the
+ * same tensors or counter must be in order on one stream. */
 taco_status taco_adamw(const taco_adamw_tensor* tensors, int64_t count, double lr, const float* lr_dev,
                        double beta1, double beta2, double eps, const float* grad_scale, int32_t* counter,
                        void* stream);
