@@ -506,7 +506,8 @@ typedef struct taco_grad_tensor {
  * the factor that clips it: max_norm / out[0] where out[0] > max_norm, else 1,
  * and NaN where out[0] is infinite or NaN (taco_adamw then changes nothing).
  * Squares are formed in fp32 and summed in it 32 at a time at most, those sums in
- * fp64, all in a fixed order: magnitudes up to 2^63 and down to 2^-63 are fully counted.
+ * fp64, all in a fixed order. Every finite value counts, whatever its magnitude:
+ * out[0] is infinite only where the norm itself lies beyond fp32.
  * max_norm >= 0, infinity included. `workspace`: taco_grad_norm_workspace_bytes
  * bytes, 8-byte aligned, need not be zeroed. */
 size_t taco_grad_norm_workspace_bytes(int64_t count);
