@@ -32,9 +32,9 @@ constexpr float kLog2e = 1.44269504f;
 constexpr float kTanhC = 1.59576912f;    // sqrt(8 / pi)
 constexpr float kTanhA = 0.044715f;
 
-// (1 - erf(|x| / sqrt 2)) / 2, and e = exp(-x^2 / 2).
-__device__ __forceinline__ f2 upper_tail(f2 x, f2& e) {
-  const f2 z{fabsf(x.x), fabsf(x.y)};
+// (1 - erf(z / sqrt 2)) / 2 of z = |x|, and e = exp(-x^2 / 2). From 64 on both are
+// zero, and z may be held there.
+__device__ __forceinline__ f2 upper_tail(f2 x, f2 z, f2& e) {
   const f2 d = fma2(z, both(0.3275911f * 0.70710678f), both(1.0f));
   const f2 t{reciprocal(d.x), reciprocal(d.y)};
   f2 p = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
@@ -49,9 +49,10 @@ template <int ACT>
 __device__ __forceinline__ f2 activate2(f2 x) {
   if constexpr (ACT == TACO_ACT_GELU) {
     f2 e;
-    const f2 h = upper_tail(x, e);
+    const f2 z{fminf(fabsf(x.x), 64.0f), fminf(fabsf(x.y), 64.0f)}, h = upper_tail(x, z, e);
     const f2 top{x.x < 0.0f ? 0.0f : x.x, x.y < 0.0f ? 0.0f : x.y};
-    return fma2(f2{-fabsf(x.x), -fabsf(x.y)}, h, top);
+    // -|x| h, but no infinity times 0 at +infinity, which stays what it is (-infinity gives NaN, as the formula)
+    return fma2(f2{fminf(x.x, -z.x), fminf(x.y, -z.y)}, h, top);
   } else if constexpr (ACT == TACO_ACT_GELU_TANH) {
     const f2 t = fma2(mul2(x, x), both(-kTanhC * kTanhA * kLog2e), both(-kTanhC * kLog2e));
     return mul2(x, logistic2(mul2(x, t)));
@@ -88,7 +89,7 @@ template <int ACT>
 __device__ __forceinline__ f2 slope2(f2 x) {
   if constexpr (ACT == TACO_ACT_GELU) {
     f2 e;
-    const f2 h = upper_tail(x, e);
+    const f2 h = upper_tail(x, f2{fabsf(x.x), fabsf(x.y)}, e);
     const f2 phi{x.x < 0.0f ? h.x : 1.0f - h.x, x.y < 0.0f ? h.y : 1.0f - h.y};
     return fma2(mul2(x, e), both(0.39894228f), phi);
   } else if constexpr (ACT == TACO_ACT_GELU_TANH) {
