@@ -22,8 +22,8 @@
 // would make m' / (0 + eps) of an element much smaller than its block's largest.
 //
 // Measured, 134M bf16 parameters with f32 gradients (a plain copy: 6.78 TB/s): 8-bit
-// states 255 us, 6.3 TB/s, bound by memory and issue slots; 32-bit states
-// with masters 627-637 us, 6.3 TB/s. 96 vectors of a few thousand elements 5 us.
+// states 255 us, 6.3 TB/s, bound by memory at 63% of the issue slots; 32-bit states
+// with masters 623-639 us, 6.3 TB/s. 96 vectors of a few thousand elements 6 us.
 
 #include "optim.cuh"
 
@@ -139,12 +139,12 @@ __device__ __forceinline__ Row16<T> pack_by_threshold(float (&x)[16], uint32_t w
 
 // CTAs per SM that the registers are held to, with 2, 3 and 4, and the copy peak's
 // share at 134M bf16 parameters with f32 gradients:
-//   32-bit states     484, 507, -  us    0.98, 0.94
-//   with masters      637, 644, -  us    0.93, 0.92
-//   8-bit states      318, 263, 252 us   0.75, 0.91, 0.95
-//   with masters      382, 388, 391 us   0.93, 0.92, 0.91
+//   32-bit states     482, 508, -  us    0.99, 0.94
+//   with masters      625, 643, -  us    0.95, 0.92
+//   8-bit states      319, 267, 255 us   0.75, 0.89, 0.93
+//   with masters      382, 388, 398 us   0.93, 0.92, 0.90
 // In 32 bits fewer CTAs with 230 bytes a thread in flight stay nearer to memory's
-// order; in 8 bits a step is some 35 instructions an element and wants warps.
+// order; in 8 bits a step is some 39 instructions an element and wants warps.
 template <bool SMALL>
 constexpr int adamw_ctas() { return SMALL ? 4 : 2; }
 

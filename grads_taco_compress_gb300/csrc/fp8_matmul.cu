@@ -37,8 +37,9 @@
 // MB would take 2.5, and 5.5 us where they are in L2 from the call before; 1 x
 // 16384 x 4096 13.6 us, 4.9 TB/s.
 // A layer of 8192 x 16384 x 4096 with bias, tanh GELU, FP8 output and checkpoint
-// 311-320 us, 3.5 PFLOP/s, tensor pipe 84% (the product alone 297-306), and 373-382 us in
-// a long loop (363); 8192 x 16384 x 1024 155 us, bound by the epilogue (95).
+// 311-327 us, 3.4-3.5 PFLOP/s, tensor pipe 84% (the product alone 297-306), and 372-382
+// us in a long loop, 2.9 PFLOP/s (363); 8192 x 16384 x 1024 153-159 us, bound by the
+// epilogue (95).
 
 #include "fp8_activation.cuh"
 #include "tcgen05.cuh"
@@ -349,7 +350,12 @@ struct Pair {
 // epilogue overlaps the next one's MMAs. SEG: the sum over K is formed in
 // segments of kSegment blocks, each started from zero in tensor memory, that
 // the epilogue adds in registers: the tensor cores cut, not round, what falls
-// below an accumulator's last bit, and a long sum drifts.
+// below an accumulator's last bit, and a long sum drifts (sums of positive terms by
+// 5e-5 of themselves over 16384 columns at worst, 7e-6 for random codes). Outputs of
+// 16 and 8 bits take the sum as it is: that is below their own rounding, 2^-11 at the
+// finest, and segments, which need the narrow tile, would cost more than a fifth (a
+// layer of 8192 x 16384 x 4096 with FP8 output 398 us for 327, of 8192 x 6400 x 1600
+// 80 for 74).
 constexpr int kSegment = 8;
 
 // ------------------------------------------------- a layer's epilogue ----
@@ -1446,6 +1452,12 @@ cudaError_t launch_few(EncodeTiled encode, const Args& a, int splits, cudaStream
 // columns wide where that is one wave (256 rows: 9.4 us, 14.0 at 256 wide),
 // else 256 wide (1024 rows: 15.7 us, 18.4 at 128 wide); f32 always 128, whose
 // sum its epilogue can hold.
+// A layer (tanh GELU, FP8 output, kept) goes by the same rules. N = K = 4096: 65 rows
+// 8.7 us split, 12.1 in pairs; 128 rows 10.1 and 12.6; 256 rows 14.8 and 12.6; 256
+// rows at K = 16384 28.2 and 35.1. In pairs, 128 and 256 wide: 512 rows 13.7 and 17.6,
+// 1024 rows 20.7 and 19.2, 2048 rows 33.2 and 29.0. Where the wide tiles are a wave
+// and a bit, the narrow ones, which the rules pass over, are up to a tenth faster
+// (1024 x 6400 x 1600: 16.8 and 18.7).
 constexpr int kFewSaves = 24;
 template <typename T, typename Args>
 cudaError_t launch_product(const Args& a, int sms, const int* clusters, cudaStream_t st) {

@@ -317,8 +317,10 @@ struct AdamwArgs {
   const float* factor;      // null: 1
   int32_t* counter;         // steps done, CTAs arrived
 };
-// Tensors of one launch: a table that fits what launches cost least with, and
-// one that fills the 32764 bytes that a kernel's parameters may take.
+// Tensors of one launch: a small table, and one that fills the 32764 bytes that a
+// kernel's parameters may take and costs the host a microsecond more to pass. A call
+// on 4 tensors: AdamW 4.5 us with 40 entries, 5.3 with 400, norm 4.9 us with 128 (3
+// KB as well), 5.9 with 1300; GPU 0.1 us apart.
 constexpr int kAdamwFew = 40, kAdamwMany = 400;
 // One launch over tensors of the same types and forms.
 cudaError_t launch_adamw(const AdamwArgs& a, const AdamwEntry* entries, int count, int param_dtype, int grad_dtype,

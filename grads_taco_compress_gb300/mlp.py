@@ -101,7 +101,10 @@ class TensorParallelMlp:
 
     def refresh(self) -> None:
         """Quantise the weights and their transposes (after an update of the
-        masters), into the same memory each time: a captured forward pass reads it."""
+        masters), into the same memory each time: a captured forward pass reads it.
+        So forward and backward passes on other streams have to be done before,
+        and wait for this before they begin. A backward pass after it goes through
+        the new weights, whichever its forward pass had."""
         def quantized(weights, old):
             return [F.taco_fp8_quantize(w, cols=True, tile=F.BLOCK, out=q, out_t=t) for w, (q, t) in zip(weights, old)]
 

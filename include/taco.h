@@ -462,6 +462,10 @@ taco_status taco_matmul_fp8(const taco_fp8_tensor* a, const taco_fp8_tensor* b, 
 
 /* The same product with a layer's epilogue, before anything is rounded:
  *   pre = a b^T + bias,   y = act(pre) + residual
+ * Sums are fp32, those of outputs in 16 and 8 bits (and of the checkpoint beside
+ * them) as the tensor cores leave them, which cut where fp32 rounds: off by
+ * (K / 32 + 32) 2^-23 of their products' magnitudes at most. f32 outputs are sums of
+ * segments of 1024 columns.
  * bias [N] (bias_dtype), residual [M, N] (dtype) and `checkpoint` may be NULL.
  * y goes to `out` (dtype), or quantised to y_fp8 (tile_rows 1; out and residual
  * NULL then, dtype unused): exactly one of the two. `checkpoint` (tile_rows 1)
