@@ -34,12 +34,11 @@ def check(grads, want, max_norm=math.inf):
 
 
 @pytest.mark.parametrize("n", [1, 2, 3, 15, 16, 31, 33, 100000])
-@pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("e", [-149, -140, -127, -126, -100, -75, -64, -63, -62, -46, -45, -44, 56, 57, 58, 62, 63, 64, 80, 100,
-                               118])
+@pytest.mark.parametrize("dtype,e", [
+    (dtype, e) for dtype, smallest in ((F32, -149), (BF16, -133))
+    for e in (-149, -140, -133, -127, -126, -100, -75, -64, -63, -62, -46, -45, -44, 56, 57, 58, 62, 63, 64, 80, 100, 118)
+    if e >= smallest])
 def test_equal_values(n, dtype, e):
-    if dtype == BF16 and e < -133:
-        pytest.skip("not a bf16 number")
     t = torch.full((n,), 2.0 ** e, dtype=dtype, device="cuda")
     if n > 2:
         t[1] *= -1
